@@ -37,3 +37,14 @@ from ._binding import (  # noqa: F401
     timing_enable,
     timing_read,
 )
+from ._attn import (  # noqa: F401
+    NO_WINDOW,
+    compact_pages,
+    copy_pages,
+    tree_attention,
+    tree_attn_paged,
+    window_attention,
+    window_attention_backward,
+    window_attn_bwd,
+    window_attn_fwd,
+)

@@ -22,7 +22,9 @@ LIB_NAME = "libsdl_spmm.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["api.hip", "plan.hip", "worker.hip", "sddmm.hip", "eb.hip",
            "worker_f32_buf.hip", "worker_f32_flat.hip", "worker_bf16_buf.hip",
-           "worker_bf16_flat.hip", "worker_fused_buf.hip", "worker_fused_flat.hip"]
+           "worker_bf16_flat.hip", "worker_fused_buf.hip", "worker_fused_flat.hip",
+           "attn/api.hip", "attn/window_fwd.hip", "attn/window_bwd.hip", "attn/tree.hip",
+           "attn/pages.hip"]
 CEILING_SOURCE = "ceiling.hip"
 CEILING_PATH = os.path.join(HERE, "libsdl_ceiling.so")
 ARCH = "gfx950"
@@ -51,7 +53,7 @@ def build(verbose: bool = False) -> str:
     flags = compile_flags()
 
     def one(src: str) -> str:
-        obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
+        obj = os.path.join(BUILD_DIR, src.replace("/", "_").replace(".hip", ".o"))
         cmd = [hipcc, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)

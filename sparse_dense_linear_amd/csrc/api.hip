@@ -993,6 +993,27 @@ hipError_t take_fault_count(char *block, hipStream_t stream, uint32_t *seen, uin
 
 }  // namespace
 
+// A text that cannot be stored (out of memory) leaves none; the status stays.
+int32_t sdl::record_error(int32_t status, const char *msg) noexcept
+{
+    try {
+        return fail(status, msg);
+    } catch (...) {
+        g_last_error.clear();
+        return status;
+    }
+}
+
+int32_t sdl::record_hip_error(hipError_t err, const char *where) noexcept
+{
+    try {
+        return fail_hip(err, where);
+    } catch (...) {
+        g_last_error.clear();
+        return SPMM_ERROR_HIP;
+    }
+}
+
 int32_t sdl::current_wait_polls() { return g_wait_polls.load(std::memory_order_relaxed); }
 
 extern "C" {

@@ -1,0 +1,162 @@
+// exact.h -- single rows of attention from their definition, by one
+// wavefront.
+//
+// The tiled kernels give a masked pair the weight 0 and multiply it with the
+// row of V (K, q, do) all the same; where that row holds an infinity or a
+// NaN the product is NaN, though the pair is not part of the result.  A row
+// that comes out of a tiled kernel non-finite is therefore computed once
+// more here, from the pairs that are seen alone.  Data without infinities
+// and NaN never come here, and the tiles pay one test per output row.
+#pragma once
+
+#include "tile.h"
+
+namespace sdl {
+
+__device__ inline float wave_max(float x)
+{
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        x = fmaxf(x, __shfl_xor(x, d));
+    return x;
+}
+
+__device__ inline float wave_sum(float x)
+{
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        x += __shfl_xor(x, d);
+    return x;
+}
+
+template <class T>
+__device__ inline float dot_row(const T *a, const T *b, int D)
+{
+    float s = 0.0f;
+    for (int d = 0; d < D; d += 8) {
+        const Frag<T> x = load8(a + d), y = load8(b + d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            s = fmaf((float)x[e], (float)y[e], s);
+    }
+    return s;
+}
+
+// Adds w * row[d] to (a0: d = lane, a1: d = lane + 64).
+template <class T>
+__device__ inline void add_row(const T *row, float w, int D, int lane, float &a0, float &a1)
+{
+    if (lane < D)
+        a0 = fmaf(w, (float)row[lane], a0);
+    if (lane + 64 < D)
+        a1 = fmaf(w, (float)row[lane + 64], a1);
+}
+
+template <class T>
+__device__ inline void put_row(T *row, float a0, float a1, int D, int lane)
+{
+    if (lane < D)
+        row[lane] = (T)a0;
+    if (lane + 64 < D)
+        row[lane + 64] = (T)a1;
+}
+
+// o and lse of one query over keys 0 .. a - 1 and b .. c - 1 (a <= b) that
+// seen(j) lets through; key(j) and val(j) are their rows.  c2 = scale *
+// log2(e).  No key at all: 0 and -inf.
+template <class T, class Key, class Val, class SeenAt>
+__device__ inline void exact_row(const T *q, Key key, Val val, SeenAt seen, int a, int b, int c,
+                                 int D, float c2, T *o, float *lse, int lane)
+{
+    float top = SDL_NEG_INF, total = 0.0f, a0 = 0.0f, a1 = 0.0f;
+    bool any = false;
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int j0 = 0; j0 < c; j0 += 64) {
+            if (j0 >= a && j0 + 64 <= b)
+                continue;
+            const int j = j0 + lane;
+            const bool in = j < c && (j < a || j >= b) && seen(j);
+            const float x = in ? dot_row(q, key(j), D) * c2 : SDL_NEG_INF;
+            if (pass == 0) {
+                top = fmaxf(top, x);
+                any = any || __any(in);
+                continue;
+            }
+            const float base = top == SDL_NEG_INF ? 0.0f : top;
+            const float p = in ? __builtin_amdgcn_exp2f(x - base) : 0.0f;
+            total += p;
+            for (uint64_t left = __ballot(in); left != 0; left &= left - 1) {
+                const int n = __ffsll((unsigned long long)left) - 1;
+                add_row(val(j0 + n), __shfl(p, n), D, lane, a0, a1);
+            }
+        }
+        if (pass == 0)
+            top = wave_max(top);
+    }
+    total = wave_sum(total);
+    const float inv = 1.0f / total;
+    put_row(o, any ? a0 * inv : 0.0f, any ? a1 * inv : 0.0f, D, lane);
+    if (lane == 0)
+        *lse = any ? kLn2 * (top + __builtin_amdgcn_logf(total)) : SDL_NEG_INF;
+}
+
+// What a row of the gradients needs of the other operands.
+template <class T>
+struct GradRows {
+    const T *q, *k, *v, *dout;      // first query / key of the sequence, at the head
+    int64_t q_stride, k_stride, v_stride, dout_stride;
+    const float *lse, *delta;       // of the first query, at the head
+};
+
+// dq of query i from keys 0 .. a - 1 and b .. c - 1 that seen(j) lets through.
+template <class T, class SeenAt>
+__device__ inline void exact_dq_row(const GradRows<T> &r, int i, float delta, SeenAt seen, int a,
+                                    int b, int c, int D, float c2, float scale, T *dq, int lane)
+{
+    const T *q = r.q + (int64_t)i * r.q_stride, *g = r.dout + (int64_t)i * r.dout_stride;
+    const float lse2 = r.lse[i] * kLog2e;
+    float a0 = 0.0f, a1 = 0.0f;
+    for (int j0 = 0; j0 < c; j0 += 64) {
+        if (j0 >= a && j0 + 64 <= b)
+            continue;
+        const int j = j0 + lane;
+        const bool in = j < c && (j < a || j >= b) && seen(j);
+        float ds = 0.0f;
+        if (in) {
+            const float p =
+                __builtin_amdgcn_exp2f(dot_row(q, r.k + (int64_t)j * r.k_stride, D) * c2 - lse2);
+            ds = p * (dot_row(g, r.v + (int64_t)j * r.v_stride, D) - delta);
+        }
+        for (uint64_t left = __ballot(in); left != 0; left &= left - 1) {
+            const int n = __ffsll((unsigned long long)left) - 1;
+            add_row(r.k + (int64_t)(j0 + n) * r.k_stride, __shfl(ds, n), D, lane, a0, a1);
+        }
+    }
+    put_row(dq, a0 * scale, a1 * scale, D, lane);
+}
+
+// Adds what queries i0 .. i1 - 1 of one head that seen(i) lets through give
+// to dk and dv of key j.
+template <class T, class SeenAt>
+__device__ inline void exact_dkv_add(const GradRows<T> &r, int j, SeenAt seen, int i0, int i1, int D,
+                                     float c2, int lane, float (&dk)[2], float (&dv)[2])
+{
+    const T *k = r.k + (int64_t)j * r.k_stride, *v = r.v + (int64_t)j * r.v_stride;
+    for (int b = i0; b < i1; b += 64) {
+        const int i = b + lane;
+        const bool in = i < i1 && seen(i);
+        float p = 0.0f, ds = 0.0f;
+        if (in) {
+            p = __builtin_amdgcn_exp2f(dot_row(r.q + (int64_t)i * r.q_stride, k, D) * c2 -
+                                       r.lse[i] * kLog2e);
+            ds = p * (dot_row(r.dout + (int64_t)i * r.dout_stride, v, D) - r.delta[i]);
+        }
+        for (uint64_t left = __ballot(in); left != 0; left &= left - 1) {
+            const int n = __ffsll((unsigned long long)left) - 1;
+            add_row(r.q + (int64_t)(b + n) * r.q_stride, __shfl(ds, n), D, lane, dk[0], dk[1]);
+            add_row(r.dout + (int64_t)(b + n) * r.dout_stride, __shfl(p, n), D, lane, dv[0], dv[1]);
+        }
+    }
+}
+
+}  // namespace sdl

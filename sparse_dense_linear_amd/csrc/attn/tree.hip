@@ -1,0 +1,565 @@
+// tree.hip -- attention of drafted tokens over a paged cache.
+//
+// A sequence has ctx cached keys and T drafts whose keys follow them in the
+// cache; draft t sees the context (through the window and the first keys)
+// and the drafts that its mask names.  One answered token is T = 1.
+//
+// The T * (Hq / Hkv) queries that share a key head are the columns of one
+// matrix product with its keys, so each cached row is read once for all of
+// them (for up to 32 * RG of them; more take another turn over L2).
+//
+// Work is counted in tiles of 128 keys over (sequence, key head, block of
+// queries) and cut into equal spans, one per workgroup, so that ragged
+// batches and single long sequences fill the GPU alike.  A unit that lies
+// within one span is finished there; one that is cut leaves its running
+// maximum, sum and unnormalised output (fp32) in a slot of each span it
+// touches, and a second launch joins them in span order: no atomics, the
+// same result every time.
+#include "ops.h"
+#include "exact.h"
+#include "tile.h"
+#include "spmm.h"
+
+namespace sdl {
+
+namespace {
+
+constexpr int kTileKeys = 128;
+
+// What sequence s asks for.
+struct Unit {
+    int q_begin, drafts, ctx, end;   // end: ctx + drafts
+    int low;                         // first key of the window (any draft's)
+    int first_tiles, band, tiles;    // key tiles [0, first_tiles) and [band, ..)
+    int blocks;                      // blocks of queries
+};
+
+__device__ inline Unit unit_of(const TreeArgs &a, int s, int block_rows)
+{
+    Unit u;
+    u.q_begin = a.q_rowptr[s];
+    u.drafts = a.q_rowptr[s + 1] - u.q_begin;
+    u.ctx = a.ctx[s];
+    u.end = u.ctx + u.drafts;
+    u.low = u.ctx - a.window + 1 > 0 ? u.ctx - a.window + 1 : 0;
+    u.band = u.low / kTileKeys;
+    u.first_tiles = (a.sinks + kTileKeys - 1) / kTileKeys;
+    u.first_tiles = u.first_tiles < u.band ? u.first_tiles : u.band;
+    u.tiles = u.first_tiles + (u.end + kTileKeys - 1) / kTileKeys - u.band;
+    u.blocks = (u.drafts * (a.Hq / a.Hkv) + block_rows - 1) / block_rows;
+    return u;
+}
+
+__device__ inline int first_key(const Unit &u, int n)
+{
+    return (n < u.first_tiles ? n : u.band + n - u.first_tiles) * kTileKeys;
+}
+
+// A key of tile n that may be read: tiles reach over keys that no draft
+// sees (behind the window their pages may have been given away), which
+// repeat the nearest key that is seen.
+__device__ inline int readable(const TreeArgs &a, const Unit &u, int n, int j)
+{
+    if (j >= u.end)
+        return u.end - 1;
+    if (j < u.low && j >= a.sinks)
+        return n < u.first_tiles ? a.sinks - 1 : u.low;
+    return j;
+}
+
+// Which keys draft t sees, and from where.
+struct DraftSeen {
+    int ctx, drafts, window, sinks;
+    int pos;              // of the draft
+    uint64_t mask;
+    const int *place;     // positions of the drafts' keys (null: a chain)
+    __device__ bool operator()(int j) const
+    {
+        if (j < ctx || place == nullptr)
+            return j <= pos && (pos - j < window || j < sinks);
+        const int d = j - ctx;
+        if (d >= drafts || d >= 64 || !(mask >> d & 1))
+            return false;
+        return pos - place[d] < window || place[d] < sinks;
+    }
+};
+
+__device__ inline uint64_t draft_mask(const TreeArgs &a, int q_begin, int drafts, int t)
+{
+    const uint64_t m = a.tree[q_begin + t];
+    return drafts < 64 ? m & (((uint64_t)1 << drafts) - 1) : m;
+}
+
+__device__ inline int draft_place(int ctx, uint64_t mask)
+{
+    const int n = __popcll(mask);
+    return ctx + (n > 1 ? n - 1 : 0);
+}
+
+// The spans: `workers` of them (at most one for each tile), span w from
+// tile span_start(w) on.
+struct Spans {
+    int64_t tiles;
+    int workers;
+    __device__ int64_t start(int w) const { return w * tiles / workers; }
+    // the span that holds a tile
+    __device__ int of(int64_t tile) const
+    {
+        return (int)(((tile + 1) * workers + tiles - 1) / tiles) - 1;
+    }
+};
+
+// Workspace: first tile of every sequence (S + 1), then for each span two
+// slots (its first and its last unit) of maximum and sum, then their outputs.
+struct Slots {
+    int64_t *base;
+    float *stat, *out;
+    __device__ Slots(const TreeArgs &a, int block_rows)
+    {
+        base = (int64_t *)a.partial;
+        stat = a.partial + 2 * (((int64_t)a.S + 1 + 31) / 32 * 32);
+        out = stat + (int64_t)2 * a.workers * block_rows * 2;
+    }
+};
+
+template <class T, int DP, int RG>
+__global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) void tree_attn(TreeArgs a)
+{
+    constexpr int KS = 4 / RG;                 // wavefronts that share a query group's keys
+    constexpr int RB = 32 * RG;                // queries of a block
+    constexpr int STEPS = DP / 16, DB = DP / 32;
+    typedef Tile<T, DP, kTileKeys> Tl;
+    typedef Tile<float, DP, 32> Out;
+    constexpr int kPiecesPer = kTileKeys * Tl::kPieces / kAttnThreads;
+    constexpr int kBytes = 2 * Tl::kBytes > 4 * Out::kBytes ? 2 * Tl::kBytes : 4 * Out::kBytes;
+    __shared__ __align__(16) char lds[kBytes];
+    __shared__ int64_t scan[8];
+    __shared__ int found;
+    __shared__ int64_t found_base;
+    __shared__ int place[64];
+    __shared__ float tops[4][32], totals[4][32];
+    __shared__ int redo[RB];
+
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
+    const int group = a.Hq / a.Hkv;
+    const int rg = wave % RG, ks = wave / RG;
+    const float c2 = a.scale * kLog2e;
+    const Slots slots(a, RB);
+
+    // ---- this workgroup's span: total of all tiles, then the sequence that
+    // holds the span's first one
+    Spans spans;
+    spans.tiles = 0;
+    for (int s0 = 0; s0 < a.S; s0 += kAttnThreads) {
+        int64_t n = 0;
+        if (s0 + t < a.S) {
+            const Unit u = unit_of(a, s0 + t, RB);
+            n = (int64_t)a.Hkv * u.blocks * u.tiles;
+        }
+        for (int d = 32; d > 0; d >>= 1)
+            n += __shfl_xor(n, d);
+        if (lane == 0)
+            scan[wave] = n;
+        __syncthreads();
+        spans.tiles += scan[0] + scan[1] + scan[2] + scan[3];
+        __syncthreads();
+    }
+    if (spans.tiles == 0)
+        return;
+    spans.workers = spans.tiles < a.workers ? (int)spans.tiles : a.workers;
+    const int w = xcd_order(blockIdx.x, gridDim.x);
+    if (w >= spans.workers)
+        return;
+    int64_t at = spans.start(w);
+    const int64_t stop = spans.start(w + 1);
+    int64_t base = 0;
+    for (int s0 = 0; s0 < a.S; s0 += kAttnThreads) {
+        int64_t n = 0;
+        if (s0 + t < a.S) {
+            const Unit u = unit_of(a, s0 + t, RB);
+            n = (int64_t)a.Hkv * u.blocks * u.tiles;
+        }
+        int64_t upto = n;                      // inclusive sum over the wavefront
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t y = __shfl_up(upto, d);
+            if (lane >= d)
+                upto += y;
+        }
+        if (lane == 63)
+            scan[wave] = upto;
+        __syncthreads();
+        for (int i = 0; i < wave; ++i)
+            upto += scan[i];
+        upto += base;
+        if (s0 + t < a.S) {
+            if (upto - n <= at && at < upto) {
+                found = s0 + t;
+                found_base = upto - n;
+            }
+            if (w == 0) {
+                slots.base[s0 + t] = upto - n;
+                if (s0 + t == a.S - 1)
+                    slots.base[a.S] = upto;
+            }
+        }
+        base += scan[0] + scan[1] + scan[2] + scan[3];
+        __syncthreads();
+    }
+    int seq = found;
+    base = found_base;
+
+    // ---- the units of the span, one piece after another
+    int64_t piece_no = 0;
+    while (at < stop) {
+        Unit u = unit_of(a, seq, RB);
+        int64_t mine = (int64_t)a.Hkv * u.blocks * u.tiles;
+        while (at >= base + mine) {            // the next sequence that has tiles
+            base += mine;
+            ++seq;
+            u = unit_of(a, seq, RB);
+            mine = (int64_t)a.Hkv * u.blocks * u.tiles;
+        }
+        const int unit = (int)((at - base) / u.tiles);
+        const int hk = unit / u.blocks, block = unit % u.blocks;
+        const int n0 = (int)((at - base) % u.tiles);
+        const int n1 = stop - at < u.tiles - n0 ? n0 + (int)(stop - at) : u.tiles;
+        const int rows = u.drafts * group;
+
+        // the drafts' positions, for the tiles that reach past the context
+        __syncthreads();
+        if (a.tree != nullptr && t < 64 && t < u.drafts)
+            place[t] = draft_place(u.ctx, draft_mask(a, u.q_begin, u.drafts, t));
+        if (t < RB)
+            redo[t] = 0;
+
+        // this lane's query
+        const int r = block * RB + 32 * rg + (lane & 31);
+        const int token = (r < rows ? r : rows - 1) / group, head = hk * group + (r < rows ? r : rows - 1) % group;
+        DraftSeen seen;
+        seen.ctx = u.ctx;
+        seen.drafts = u.drafts;
+        seen.window = a.window;
+        seen.sinks = a.sinks;
+        seen.mask = a.tree != nullptr ? draft_mask(a, u.q_begin, u.drafts, token) : 0;
+        seen.pos = a.tree != nullptr ? draft_place(u.ctx, seen.mask) : u.ctx + token;
+        seen.place = a.tree != nullptr ? place : nullptr;
+        const T *q = (const T *)a.q + (int64_t)(u.q_begin + token) * a.q_row + head * a.q_head;
+        Frag<T> qf[STEPS];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            qf[s] = 16 * s + 8 * half < a.D ? load8(q + 16 * s + 8 * half) : zero_frag<T>();
+
+        f32x16 O[DB];
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+            O[d] = f32x16(0.0f);
+        float top = SDL_NEG_INF, total = 0.0f;
+
+        // pages of a tile's rows, one tile ahead of the rows themselves
+        const int32_t *table = a.table + (int64_t)seq * a.table_stride;
+        const T *kp = (const T *)a.k_pages + hk * a.head_stride, *vp = (const T *)a.v_pages + hk * a.head_stride;
+        int id[kPiecesPer], in_page[kPiecesPer];
+        u32x4 pk[kPiecesPer], pv[kPiecesPer];
+        auto fetch_ids = [&](int n) {
+#pragma unroll
+            for (int i = 0; i < kPiecesPer; ++i) {
+                const int j = readable(a, u, n, first_key(u, n) + (t + i * kAttnThreads) / Tl::kPieces);
+                const int p = j / a.page;
+                in_page[i] = j - p * a.page;
+                id[i] = table[p];
+            }
+        };
+        auto fetch_rows = [&]() {
+#pragma unroll
+            for (int i = 0; i < kPiecesPer; ++i) {
+                const int p = (t + i * kAttnThreads) % Tl::kPieces;
+                const int d = p * Tl::kElems < a.D ? p * Tl::kElems : a.D - Tl::kElems;
+                const int64_t off = (int64_t)id[i] * a.page_stride + (int64_t)in_page[i] * a.row_stride + d;
+                pk[i] = *(const u32x4 *)(kp + off);
+                pv[i] = *(const u32x4 *)(vp + off);
+            }
+        };
+        fetch_ids(n0);
+        fetch_rows();
+        if (n0 + 1 < n1)
+            fetch_ids(n0 + 1);
+        for (int n = n0; n < n1; ++n) {
+            char *kt = lds, *vt = lds + Tl::kBytes;
+#pragma unroll
+            for (int i = 0; i < kPiecesPer; ++i) {
+                const int m = t + i * kAttnThreads;
+                *(u32x4 *)(kt + Tl::at(m / Tl::kPieces, m % Tl::kPieces)) = pk[i];
+                *(u32x4 *)(vt + Tl::at(m / Tl::kPieces, m % Tl::kPieces)) = pv[i];
+            }
+            __syncthreads();
+            if (n + 1 < n1) {
+                fetch_rows();
+                if (n + 2 < n1)
+                    fetch_ids(n + 2);
+            }
+#pragma unroll 1
+            for (int b = ks; b < kTileKeys / 32; b += KS) {
+                const int j0 = first_key(u, n) + 32 * b;
+                if (j0 >= u.end || (j0 + 31 < u.low && j0 >= a.sinks))
+                    continue;
+                f32x16 x = f32x16(0.0f);
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s)
+                    x = mma(Tl::row_frag(kt, 32 * b + (lane & 31), s, half), qf[s], x);
+                const bool whole = j0 + 31 < u.ctx && (u.end - 1 - j0 < a.window || j0 + 31 < a.sinks);
+                float most = SDL_NEG_INF;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float y = x[i] * c2;
+                    if (!whole && !seen(j0 + 8 * (i >> 2) + 4 * half + (i & 3)))
+                        y = SDL_NEG_INF;
+                    x[i] = y;
+                    most = fmaxf(most, y);
+                }
+                const float now = fmaxf(top, max_halves(most));
+                const float ref = now == SDL_NEG_INF ? 0.0f : now;
+                const float keep = __builtin_amdgcn_exp2f(top - ref);
+                top = now;
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[i] = __builtin_amdgcn_exp2f(x[i] - ref);
+                    sum += x[i];
+                }
+                total = total * keep + sum;
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        O[d][i] *= keep;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const Frag<T> pf = result_frag<T>(x, s);
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+                        O[d] = mma(Tl::col_frag(vt, 32 * b + 16 * s, d, lane), pf, O[d]);
+                }
+            }
+            __syncthreads();
+        }
+
+        // ---- join the wavefronts of a query group, and write
+        total = sum_halves(total);
+        if (half == 0) {
+            tops[wave][lane] = top;
+            totals[wave][lane] = total;
+        }
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                store4((float *)(lds + wave * Out::kBytes + Out::at(lane & 31, 8 * d + 2 * g + half)),
+                       O[d][4 * g], O[d][4 * g + 1], O[d][4 * g + 2], O[d][4 * g + 3]);
+        __syncthreads();
+        const bool done = n0 == 0 && n1 == u.tiles;
+        const int64_t slot = 2 * (int64_t)w + (piece_no == 0 ? 0 : 1);
+        constexpr int kOutPieces = DP / 4;
+        for (int m = t; m < RB * kOutPieces; m += kAttnThreads) {
+            const int lr = m / kOutPieces, p = m % kOutPieces;
+            const int rr = block * RB + lr;
+            if (rr >= rows)
+                break;
+            float best = SDL_NEG_INF;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+                best = fmaxf(best, tops[k * RG + lr / 32][lr & 31]);
+            const float ref = best == SDL_NEG_INF ? 0.0f : best;
+            float sum = 0.0f;
+            f32x4 o = f32x4(0.0f);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const int wv = k * RG + lr / 32;
+                const float f = __builtin_amdgcn_exp2f(tops[wv][lr & 31] - ref);
+                sum = fmaf(f, totals[wv][lr & 31], sum);
+                const f32x4 x = *(const f32x4 *)(lds + wv * Out::kBytes + Out::at(lr & 31, p));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[e] = fmaf(f, x[e], o[e]);
+            }
+            if (!done) {
+                float *to = slots.out + (slot * RB + lr) * DP + 4 * p;
+                *(f32x4 *)to = o;
+                if (p == 0) {
+                    slots.stat[(slot * RB + lr) * 2] = best;
+                    slots.stat[(slot * RB + lr) * 2 + 1] = sum;
+                }
+                continue;
+            }
+            const int64_t tk = u.q_begin + rr / group;
+            const int hd = hk * group + rr % group;
+            const float lse = kLn2 * (best + __builtin_amdgcn_logf(sum));
+            // nothing seen: the maximum of no score at all
+            const float inv = 1.0f / sum;
+            bool clean = finite(lse);
+            if (4 * p < a.D) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[e] = o[e] * inv;
+                    clean = clean && finite(y[e]);
+                }
+                store4((T *)a.o + (tk * a.Hq + hd) * a.D + 4 * p, y[0], y[1], y[2], y[3]);
+            }
+            if (p == 0)
+                a.lse[hd * a.Tq + tk] = lse;
+            if (!clean)
+                redo[lr] = 1;
+        }
+        __syncthreads();
+        if (done)
+            for (int lr = wave; lr < RB; lr += 4)
+                if (redo[lr]) {                // uniform over the wavefront
+                    const int rr = block * RB + lr;
+                    const int64_t tk = u.q_begin + rr / group;
+                    const int hd = hk * group + rr % group;
+                    DraftSeen one = seen;
+                    one.mask = a.tree != nullptr ? draft_mask(a, u.q_begin, u.drafts, rr / group) : 0;
+                    one.pos = a.tree != nullptr ? draft_place(u.ctx, one.mask) : u.ctx + rr / group;
+                    auto at_key = [&](const T *pool, int j) {
+                        const int p = j / a.page;
+                        return pool + (int64_t)table[p] * a.page_stride + (int64_t)(j - p * a.page) * a.row_stride;
+                    };
+                    exact_row<T>(
+                        (const T *)a.q + tk * a.q_row + hd * a.q_head,
+                        [&](int j) { return at_key(kp, j); }, [&](int j) { return at_key(vp, j); }, one,
+                        a.sinks < u.low ? a.sinks : u.low, u.low, u.end, a.D, c2,
+                        (T *)a.o + (tk * a.Hq + hd) * a.D, a.lse + hd * a.Tq + tk, lane);
+                }
+        at += n1 - n0;
+        ++piece_no;
+    }
+}
+
+// One wavefront for each query row: joins the slots of the spans that its
+// unit was cut over (units within one span are written already).
+template <class T, int DP>
+__global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int RB = 32 * a.row_groups, group = a.Hq / a.Hkv;
+    const int64_t tk = row / a.Hq;
+    const int hd = (int)(row % a.Hq), hk = hd / group;
+    if (tk >= a.q_rowptr[a.S] || tk < a.q_rowptr[0])
+        return;
+    int lo = 0, hi = a.S;                      // the last sequence that begins at or before tk
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.q_rowptr[mid] <= tk)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int seq = lo;
+    const Unit u = unit_of(a, seq, RB);
+    const int token = (int)(tk - u.q_begin);
+    const int r = token * group + hd % group;
+    const Slots slots(a, RB);
+    Spans spans;
+    spans.tiles = slots.base[a.S];
+    spans.workers = spans.tiles < a.workers ? (int)spans.tiles : a.workers;
+    const int64_t from = slots.base[seq] + (int64_t)(hk * u.blocks + r / RB) * u.tiles;
+    const int w0 = spans.of(from), w1 = spans.of(from + u.tiles - 1);
+    if (w0 == w1)
+        return;
+
+    float best = SDL_NEG_INF;
+    for (int w = w0; w <= w1; ++w) {
+        const int64_t slot = 2 * (int64_t)w + (spans.start(w) >= from ? 0 : 1);
+        best = fmaxf(best, slots.stat[(slot * RB + r % RB) * 2]);
+    }
+    const float ref = best == SDL_NEG_INF ? 0.0f : best;
+    float sum = 0.0f, o0 = 0.0f, o1 = 0.0f;
+    for (int w = w0; w <= w1; ++w) {
+        const int64_t slot = 2 * (int64_t)w + (spans.start(w) >= from ? 0 : 1);
+        const float f = __builtin_amdgcn_exp2f(slots.stat[(slot * RB + r % RB) * 2] - ref);
+        sum = fmaf(f, slots.stat[(slot * RB + r % RB) * 2 + 1], sum);
+        const float *o = slots.out + (slot * RB + r % RB) * DP;
+        o0 = fmaf(f, o[lane], o0);
+        if (DP > 64)
+            o1 = fmaf(f, o[64 + lane], o1);
+    }
+    const float inv = 1.0f / sum;
+    o0 *= inv;
+    o1 *= inv;
+    const float lse = kLn2 * (best + __builtin_amdgcn_logf(sum));
+    T *out = (T *)a.o + (tk * a.Hq + hd) * a.D;
+    float *lse_at = a.lse + hd * a.Tq + tk;
+    if (__all(finite(lse) && (lane >= a.D || finite(o0)) && (lane + 64 >= a.D || finite(o1)))) {
+        put_row(out, o0, o1, a.D, lane);
+        if (lane == 0)
+            *lse_at = lse;
+        return;
+    }
+    // drafts' positions for the exact row: from their masks, one per lane
+    __shared__ int places[4][64];
+    int *place = places[threadIdx.x >> 6];
+    if (a.tree != nullptr && lane < u.drafts)
+        place[lane] = draft_place(u.ctx, draft_mask(a, u.q_begin, u.drafts, lane));
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    DraftSeen seen;
+    seen.ctx = u.ctx;
+    seen.drafts = u.drafts;
+    seen.window = a.window;
+    seen.sinks = a.sinks;
+    seen.mask = a.tree != nullptr ? draft_mask(a, u.q_begin, u.drafts, token) : 0;
+    seen.pos = a.tree != nullptr ? draft_place(u.ctx, seen.mask) : u.ctx + token;
+    seen.place = a.tree != nullptr ? place : nullptr;
+    const int32_t *table = a.table + (int64_t)seq * a.table_stride;
+    auto at_key = [&](const void *pool, int j) {
+        const int p = j / a.page;
+        return (const T *)pool + hk * a.head_stride + (int64_t)table[p] * a.page_stride +
+               (int64_t)(j - p * a.page) * a.row_stride;
+    };
+    exact_row<T>(
+        (const T *)a.q + tk * a.q_row + hd * a.q_head, [&](int j) { return at_key(a.k_pages, j); },
+        [&](int j) { return at_key(a.v_pages, j); }, seen, a.sinks < u.low ? a.sinks : u.low, u.low,
+        u.end, a.D, a.scale * kLog2e, out, lse_at, lane);
+}
+
+template <class T, int DP>
+hipError_t launch(const TreeArgs &a, hipStream_t stream)
+{
+    if (a.row_groups == 1)
+        tree_attn<T, DP, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    else if (a.row_groups == 2)
+        tree_attn<T, DP, 2><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    else
+        tree_attn<T, DP, 4><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess)
+        return err;
+    tree_join<T, DP><<<dim3((uint32_t)((a.Tq * a.Hq + 3) / 4)), kAttnThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+TreeShape tree_shape(int dtype, int64_t S, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    TreeShape sh;
+    const int DP = D <= 64 ? 64 : 128;
+    // two workgroups to a CU where their tiles fit its LDS side by side
+    sh.workers = dtype == SPMM_DTYPE_BF16 || DP == 64 ? 512 : 256;
+    // groups of 32 queries that the mean sequence fills
+    const int64_t rows = S > 0 ? (Tq + S - 1) / S * (Hq / Hkv) : 0;
+    sh.row_groups = rows <= 32 ? 1 : (rows <= 64 ? 2 : 4);
+    const int64_t block_rows = 32 * sh.row_groups;
+    sh.bytes = 4 * (2 * ((S + 1 + 31) / 32 * 32) + 2 * sh.workers * block_rows * (2 + DP));
+    return sh;
+}
+
+hipError_t launch_tree(int dtype, const TreeArgs &a, hipStream_t stream)
+{
+    if (dtype == SPMM_DTYPE_BF16)
+        return a.D <= 64 ? launch<__bf16, 64>(a, stream) : launch<__bf16, 128>(a, stream);
+    return a.D <= 64 ? launch<float, 64>(a, stream) : launch<float, 128>(a, stream);
+}
+
+}  // namespace sdl

@@ -24,6 +24,11 @@ __device__ inline int wave_exclusive_sum(int v)
     return x - v;
 }
 
+// Host: keep the text behind spmm_last_error on the calling thread, and
+// return the status.
+int32_t record_error(int32_t status, const char *msg) noexcept;
+int32_t record_hip_error(hipError_t err, const char *where) noexcept;
+
 constexpr int kWave = 64;            // CDNA wavefront width
 constexpr int kWavesPerBlock = 4;    // worker block = 256 threads
 constexpr int kBlock = kWave * kWavesPerBlock;

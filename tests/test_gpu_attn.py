@@ -1,0 +1,404 @@
+"""Window attention, forward and backward, against its definition in 64 bits
+(tests/attn_ref.py states the bounds)."""
+import math
+
+import pytest
+import torch
+
+import sparse_dense_linear_amd as sdl
+from attn_ref import assert_close, window_ref
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def starts(lengths, first=0):
+    out = [first]
+    for x in lengths:
+        out.append(out[-1] + x)
+    return out
+
+
+def i32(values):
+    return torch.tensor(values, dtype=torch.int32).cuda()
+
+
+def operands(ql, kl, Hq, Hkv, D, dtype, seed=0, first=0, behind=0):
+    g = torch.Generator().manual_seed(seed)
+    qs, ks = starts(ql, first), starts(kl, first)
+
+    def normal(rows, heads):
+        return torch.randn(rows + behind, heads, D, generator=g).to(dtype)
+
+    return normal(qs[-1], Hq), normal(ks[-1], Hkv), normal(ks[-1], Hkv), normal(qs[-1], Hq), qs, ks
+
+
+def check(ql, kl, Hq, Hkv, D, dtype, window, sinks, seed=0, scale=None, grad=True):
+    q, k, v, do, qs, ks = operands(ql, kl, Hq, Hkv, D, dtype, seed)
+    w = sdl.NO_WINDOW if window is None else window
+    want = window_ref(q, k, v, qs, ks, w, sinks, scale, do if grad else None)
+    a = dict(window=window, sinks=sinks, scale=scale)
+    qc, kc, vc, dc = q.cuda(), k.cuda(), v.cuda(), do.cuda()
+    o, lse = sdl.window_attention(qc, kc, vc, i32(qs), i32(ks), **a)
+    torch.cuda.synchronize()
+    assert o.dtype == dtype and lse.dtype == F32
+    assert_close(o, want["o"], want["o_tol"], "o")
+    assert_close(lse, want["lse"], want["lse_tol"], "lse")
+    if not grad:
+        return
+    got = sdl.window_attention_backward(dc, qc, kc, vc, o, lse, i32(qs), i32(ks), **a)
+    torch.cuda.synchronize()
+    for n, x in zip(("dq", "dk", "dv"), got):
+        assert x.dtype == dtype
+        assert_close(x, want[n], want[n + "_tol"], n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [8, 40, 64, 72, 128])
+def test_head_sizes(dtype, D):
+    check([150, 1, 33], [150, 1, 33], 4, 2, D, dtype, 40, 3, seed=D)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 5), (31, 0), (32, 4), (33, 32), (64, 64),
+                                          (100, 128), (None, 0), (None, 7), (300, 0), (200, 65)])
+def test_windows(dtype, window, sinks):
+    check([290, 70], [290, 70], 2, 1, 64, dtype, window, sinks, seed=1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 257])
+def test_lengths(dtype, n):
+    check([n], [n], 2, 2, 128, dtype, 50, 2, seed=n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (3, 1), (8, 2), (12, 4)])
+def test_shared_heads(dtype, Hq, Hkv):
+    check([100, 41], [100, 41], Hq, Hkv, 64, dtype, 37, 2, seed=Hq)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("ql,kl", [
+    ([1, 60, 129], [500, 60, 700]),          # queries are the last positions
+    ([5, 0, 7], [5, 9, 0]),                  # no queries; no keys
+    ([200, 3], [130, 2]),                    # more queries than keys: some see nothing
+    ([0, 0], [3, 0]),                        # nothing at all
+    ([40], [1500]),                          # every query past the window of the first keys
+])
+def test_pieces_and_empty_sequences(dtype, ql, kl):
+    check(ql, kl, 4, 2, 64, dtype, 48, 3, seed=5)
+    check(ql, kl, 4, 2, 128, dtype, None, 0, seed=6)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_many_far_runs(dtype):
+    """First keys that several runs of queries past the window see."""
+    check([1700, 600, 513], [1700, 600, 513], 2, 1, 64, dtype, 20, 33, seed=8)
+    check([1100], [2100], 2, 2, 128, dtype, 100, 128, seed=9)
+
+
+def test_scale():
+    check([90], [90], 2, 1, 64, F32, 33, 1, seed=2, scale=0.7)
+    check([90], [90], 2, 1, 64, BF16, 33, 1, seed=2, scale=0.05)
+
+
+def test_rows_of_no_sequence_are_left():
+    """Rows before rowptr[0] and behind rowptr[S] are not written, and what
+    they hold is not read."""
+    ql = [50, 130]
+    q, k, v, do, qs, ks = operands(ql, ql, 4, 2, 64, BF16, seed=3, first=9, behind=11)
+    for t in (q, k, v, do):
+        t[:9] = float("nan")
+        t[qs[-1]:] = float("nan")
+    want = window_ref(q, k, v, qs, ks, 40, 2, None, do)
+    qc, kc, vc, dc = (t.cuda() for t in (q, k, v, do))
+    o = torch.full_like(qc, 7.0)
+    lse = torch.full((4, q.shape[0]), 7.0, device="cuda")
+    a = dict(window=40, sinks=2)
+    sdl.window_attn_fwd(qc, kc, vc, i32(qs), i32(ks), o, lse, **a)
+    grads = [torch.full_like(t, 7.0) for t in (qc, kc, vc)]
+    sdl.window_attn_bwd(dc, qc, kc, vc, o, lse, i32(qs), i32(ks), *grads, **a)
+    torch.cuda.synchronize()
+    inside = slice(9, qs[-1])
+    for n, x in zip(("o", "dq", "dk", "dv"), [o] + grads):
+        assert_close(x[inside], want[n][inside], want[n + "_tol"][inside], n)
+        assert bool((x[:9] == 7.0).all()) and bool((x[qs[-1]:] == 7.0).all()), n
+    assert_close(lse[:, inside], want["lse"][:, inside], want["lse_tol"][:, inside], "lse")
+    assert bool((lse[:, :9] == 7.0).all()) and bool((lse[:, qs[-1]:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_strides(dtype):
+    """Slices of one fused tensor, heads-first layouts, a key head shared by a
+    stride of zero, and strided outputs."""
+    n, Hq, Hkv, D = 140, 4, 2, 64
+    q, k, v, do, qs, ks = operands([n], [n], Hq, Hkv, D, dtype, seed=4)
+    want = window_ref(q, k, v, qs, ks, 50, 3, None, do)
+    fused = torch.cat([q, k, v], 1).cuda()
+    qf, kf, vf = fused[:, :Hq], fused[:, Hq:Hq + Hkv], fused[:, Hq + Hkv:]
+    heads_first = do.permute(1, 0, 2).contiguous().cuda().permute(1, 0, 2)
+    o = torch.empty((Hq, n, D), dtype=dtype, device="cuda").permute(1, 0, 2)
+    lse = torch.empty((Hq, n), device="cuda")
+    a = dict(window=50, sinks=3)
+    sdl.window_attn_fwd(qf, kf, vf, i32(qs), i32(ks), o, lse, **a)
+    dfused = torch.empty_like(fused)
+    grads = dfused[:, :Hq], dfused[:, Hq:Hq + Hkv], dfused[:, Hq + Hkv:]
+    sdl.window_attn_bwd(heads_first, qf, kf, vf, o, lse, i32(qs), i32(ks), *grads, **a)
+    torch.cuda.synchronize()
+    for name, x in zip(("o", "dq", "dk", "dv"), (o,) + grads):
+        assert_close(x, want[name], want[name + "_tol"], name)
+
+    one = k[:, :1].expand(n, Hkv, D)                   # one key head under two names
+    want = window_ref(q, one, v, qs, ks, 50, 3)
+    shared = k[:, :1].contiguous().cuda().expand(n, Hkv, D)
+    o, lse = sdl.window_attention(q.cuda(), shared, v.cuda(), i32(qs), **a)
+    assert_close(o, want["o"], want["o_tol"], "o")
+    same = do[:1, :1].expand(n, Hq, D)                 # a broadcast gradient
+    want = window_ref(q, k, v, qs, ks, 50, 3, None, same)
+    o, lse = sdl.window_attention(q.cuda(), k.cuda(), v.cuda(), i32(qs), **a)
+    got = sdl.window_attention_backward(do[:1, :1].cuda().expand(n, Hq, D), q.cuda(), k.cuda(), v.cuda(),
+                                        o, lse, i32(qs), **a)
+    for name, x in zip(("dq", "dk", "dv"), got):
+        assert_close(x, want[name], want[name + "_tol"], name)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_masked_places_may_hold_anything(dtype, value):
+    """Key 90's row of k and v is out of the window of queries 130 and later;
+    queries before 90 do not reach it either.  What it holds changes no result
+    of a query that does not see it, and no gradient of a pair without it."""
+    n, w, s, at = 260, 40, 2, 90
+    q, k, v, do, qs, ks = operands([n], [n], 2, 1, 64, dtype, seed=6)
+    k[at], v[at] = value, value
+    a = dict(window=w, sinks=s)
+    blind = torch.tensor([i for i in range(n) if i < at or i - at >= w])
+    clean_k, clean_v = k.clone(), v.clone()
+    clean_k[at], clean_v[at] = 0, 0
+    o, lse = sdl.window_attention(q.cuda(), k.cuda(), v.cuda(), i32(qs), **a)
+    want = window_ref(q, clean_k, clean_v, qs, ks, w, s)
+    assert_close(o.cpu()[blind], want["o"][blind], want["o_tol"][blind], "o")
+    assert_close(lse.cpu()[:, blind], want["lse"][:, blind], want["lse_tol"][:, blind], "lse")
+
+    # a query row whose q and do hold it: keys that it does not see keep
+    # their gradients (their sums do not contain it)
+    q, k, v, do, qs, ks = operands([n], [n], 2, 1, 64, dtype, seed=7)
+    want = window_ref(q, k, v, qs, ks, w, s, None, do)
+    row = 150
+    q2, do2 = q.clone(), do.clone()
+    q2[row], do2[row] = value, value
+    o, lse = sdl.window_attention(q2.cuda(), k.cuda(), v.cuda(), i32(qs), **a)
+    dq, dk, dv = sdl.window_attention_backward(do2.cuda(), q2.cuda(), k.cuda(), v.cuda(), o, lse, i32(qs), **a)
+    unseen = torch.tensor([j for j in range(s, n) if j > row or row - j >= w])
+    others = torch.tensor([i for i in range(n) if i != row])
+    for name, x, keep in (("o", o, others), ("dq", dq, others), ("dk", dk, unseen), ("dv", dv, unseen)):
+        assert_close(x.cpu()[keep], want[name][keep], want[name + "_tol"][keep], name)
+    # and the far runs of the first keys: a row past the window sees key 0,
+    # a row of another sequence does not
+    q, k, v, do, qs, ks = operands([700, 300], [700, 300], 2, 1, 64, dtype, seed=8)
+    want = window_ref(q, k, v, qs, ks, w, s, None, do)
+    k2 = k.clone()
+    k2[300] = value
+    o, lse = sdl.window_attention(q.cuda(), k2.cuda(), v.cuda(), i32(qs), **a)
+    got = sdl.window_attention_backward(do.cuda(), q.cuda(), k2.cuda(), v.cuda(), o, lse, i32(qs), **a)
+    hit = set(range(300, 300 + w))
+    keep = torch.tensor([i for i in range(1000) if i not in hit])
+    assert_close(got[0].cpu()[keep], want["dq"][keep], want["dq_tol"][keep], "dq")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_seen_infinities_and_nan_go_where_arithmetic_sends_them(dtype):
+    """An infinity or a NaN in a value reaches exactly the queries that see
+    it; a key of -infinity scores nothing or everything by the query's sign."""
+    n, w, s = 200, 40, 2
+    q, k, v, do, qs, ks = operands([n], [n], 2, 1, 64, dtype, seed=9)
+    v[50, 0, 3], v[60, 0, 5] = float("inf"), float("nan")
+    o, _ = sdl.window_attention(q.cuda(), k.cuda(), v.cuda(), i32(qs), window=w, sinks=s)
+    o = o.cpu()
+    i = torch.arange(n)
+    sees = lambda j: (i >= j) & (i - j < w)  # noqa: E731
+    assert bool((torch.isposinf(o[:, 0, 3]) == sees(50)).all())
+    assert bool((torch.isnan(o[:, 1, 5]) == sees(60)).all())
+    assert bool(torch.isfinite(o[:, :, :3]).all())
+
+
+def test_large_scores():
+    """Scores far apart: weights of exactly 0 and 1, no overflow."""
+    n = 100
+    for dtype in (F32, BF16):
+        q, k, v, do, qs, ks = operands([n], [n], 1, 1, 64, dtype, seed=10)
+        want = window_ref(q * 64, k * 64, v, qs, ks, 30, 2, None, do)
+        q, k = (q * 64).cuda(), (k * 64).cuda()
+        o, lse = sdl.window_attention(q, k, v.cuda(), i32(qs), window=30, sinks=2)
+        assert_close(o, want["o"], want["o_tol"], "o")
+        assert_close(lse, want["lse"], want["lse_tol"], "lse")
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_gradients_against_differences(which):
+    """<gradient, direction> against central differences of the definition in
+    64 bits.  The differences are off by h^2 / 6 times a third derivative,
+    which for unit-scale operands and h = 1e-3 stays below 1e-4 of the sum of
+    magnitudes; the gradient is off by its bound."""
+    q, k, v, do, qs, ks = operands([70, 33], [70, 40], 4, 2, 64, F32, seed=11)
+    a = dict(window=30, sinks=3)
+    o, lse = sdl.window_attention(q.cuda(), k.cuda(), v.cuda(), i32(qs), i32(ks), **a)
+    got = sdl.window_attention_backward(do.cuda(), q.cuda(), k.cuda(), v.cuda(), o, lse, i32(qs), i32(ks), **a)
+    want = window_ref(q, k, v, qs, ks, 30, 3, None, do)
+    name = ("dq", "dk", "dv")[which]
+    x = [t.double() for t in (q, k, v)]
+    u = torch.randn(x[which].shape, generator=torch.Generator().manual_seed(12), dtype=torch.float64)
+    h = 1e-3
+
+    def loss(sign):
+        y = list(x)
+        y[which] = y[which] + sign * h * u
+        return (window_ref(*y, qs, ks, 30, 3)["o"] * do.double()).sum()
+
+    slope = float(loss(1) - loss(-1)) / (2 * h)
+    along = float((got[which].cpu().double() * u).sum())
+    bound = float((want[name + "_tol"] * u.abs()).sum()) + 1e-4 * float((want[name] * u).abs().sum())
+    assert abs(along - slope) <= bound
+
+
+def test_same_as_the_products_on_the_pattern():
+    """The library's own SDDMM and SpMM on the window's CSR pattern, with a
+    softmax between them."""
+    n, w, s, D = 300, 25, 2, 64
+    q, k, v, _, qs, ks = operands([n], [n], 1, 1, D, F32, seed=13)
+    rows = [[j for j in range(i + 1) if i - j < w or j < s] for i in range(n)]
+    rowptr = i32(starts([len(r) for r in rows]))
+    colind = i32([j for r in rows for j in r])
+    qc, kc, vc = (t[:, 0].contiguous().cuda() for t in (q, k, v))
+    x = sdl.sddmm(rowptr, colind, qc, kc) / math.sqrt(D)
+    of = torch.repeat_interleave(torch.arange(n), torch.tensor([len(r) for r in rows])).cuda()
+    top = torch.full((n,), -math.inf, device="cuda").scatter_reduce(0, of, x, "amax")
+    e = torch.exp(x - top[of])
+    p = e / torch.zeros(n, device="cuda").index_add_(0, of, e)[of]
+    o, _ = sdl.window_attention(q.cuda(), k.cuda(), v.cuda(), i32(qs), window=w, sinks=s)
+    want = window_ref(q, k, v, qs, ks, w, s)
+    assert_close(sdl.spmm(rowptr, colind, p, vc), want["o"][:, 0], 2 * want["o_tol"][:, 0], "products")
+    assert_close(o, want["o"], want["o_tol"], "o")
+
+
+def test_repeats_bit_for_bit():
+    q, k, v, do, qs, ks = operands([900, 300], [900, 300], 8, 2, 128, BF16, seed=14)
+    a = dict(window=100, sinks=4)
+    t = [x.cuda() for x in (q, k, v, do)]
+    first = None
+    for _ in range(3):
+        o, lse = sdl.window_attention(*t[:3], i32(qs), **a)
+        out = (o, lse) + sdl.window_attention_backward(t[3], *t[:3], o, lse, i32(qs), **a)
+        if first is not None:
+            assert all(torch.equal(x, y) for x, y in zip(first, out))
+        first = out
+
+
+def test_streams_and_graphs():
+    """Calls on two streams at once, and two captured steps replayed several
+    times with eager work between, all equal to the eager results."""
+    a = dict(window=60, sinks=3)
+    sets = []
+    for seed, n in ((15, 400), (16, 333)):
+        q, k, v, do, qs, ks = operands([n, 50], [n, 50], 4, 2, 64, BF16, seed=seed)
+        sets.append([x.cuda() for x in (q, k, v, do)] + [i32(qs)])
+
+    def step(q, k, v, do, rp, stream=None):
+        o, lse = sdl.window_attention(q, k, v, rp, stream=stream, **a)
+        return (o, lse) + sdl.window_attention_backward(do, q, k, v, o, lse, rp, stream=stream, **a)
+
+    eager = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for i in (0, 1):
+            got[i].append(step(*sets[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for out in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(out, eager[i]))
+
+    graphs, outs = [], []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(*s))
+        graphs.append(g)
+    for _ in range(4):
+        for out in outs:
+            for x in out:
+                x.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[0]):
+            graphs[0].replay()
+        with torch.cuda.stream(streams[1]):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            assert all(torch.equal(x, y) for x, y in zip(outs[i], eager[i]))
+        again = step(*sets[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(again, eager[0]))
+
+
+def test_offsets_past_32_bits():
+    """A token stride that puts the second sequence's rows more than 2^32
+    elements behind the first's."""
+    n, D = 40, 64
+    stride = (1 << 32) // 60 + 8 & ~7
+    rows = 2 * n
+    if torch.cuda.mem_get_info()[0] < 3 * rows * stride * 2:
+        pytest.skip("needs 35 GB")
+    q, k, v, do, qs, ks = operands([n, n], [n, n], 1, 1, D, BF16, seed=17)
+    big = torch.empty(rows * stride, dtype=BF16, device="cuda")
+    views = []
+    for i, t in enumerate((q, k, v, do)):
+        x = torch.as_strided(big, (rows, 1, D), (stride, D, 1), i * D)
+        x.copy_(t.cuda())
+        views.append(x)
+    a = dict(window=20, sinks=2)
+    want = window_ref(q, k, v, qs, ks, 20, 2, None, do)
+    o, lse = sdl.window_attention(*views[:3], i32(qs), **a)
+    dq, dk, dv = sdl.window_attention_backward(views[3], *views[:3], o, lse, i32(qs), **a)
+    for name, x in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv)):
+        assert_close(x, want[name], want[name + "_tol"], name)
+
+
+def test_binding_refusals():
+    """Arguments that the binding turns away before the library sees them."""
+    q = torch.zeros(10, 4, 64, device="cuda")
+    k = torch.zeros(10, 2, 64, device="cuda")
+    rp = i32([0, 10])
+    ok = dict(q=q, k=k, v=k, q_rowptr=rp)
+
+    def bad(error, **change):
+        with pytest.raises(error):
+            sdl.window_attention(**(ok | change))
+
+    bad(TypeError, q=q.half(), k=k.half(), v=k.half())
+    bad(TypeError, k=k.bfloat16())
+    bad(TypeError, q_rowptr=rp.long())
+    bad(ValueError, q=q[0])
+    bad(ValueError, k=k[:, :, :32], v=k[:, :, :32])
+    bad(ValueError, v=k[:5])
+    bad(ValueError, k=k.cpu())
+    bad(ValueError, q_rowptr=rp[:0])
+    bad(ValueError, q=torch.zeros(10, 64, 4, device="cuda").transpose(1, 2))
+    bad(ValueError, k_rowptr=i32([0, 5, 10]))
+    bad(sdl.SpmmError, q=q[:, :3])                       # 3 heads on 2
+    bad(sdl.SpmmError, q=q[:, :, :60], k=k[:, :, :60], v=k[:, :, :60])
+    bad(sdl.SpmmError, q=torch.zeros(10, 4, 66, device="cuda")[:, :, :64])   # strides
+    bad(sdl.SpmmError, window=0)
+    bad(sdl.SpmmError, sinks=200)
+    bad(sdl.SpmmError, scale=-1.0)
+    o, lse = sdl.window_attention(**ok)
+    with pytest.raises(ValueError):
+        sdl.window_attention_backward(q, q, k, k, o, lse.t(), rp)
+    with pytest.raises(TypeError):
+        sdl.window_attention_backward(q, q, k, k, o.bfloat16(), lse, rp)
+    with pytest.raises(ValueError):
+        sdl.window_attention_backward(q[:, :2], q, k, k, o, lse, rp)
