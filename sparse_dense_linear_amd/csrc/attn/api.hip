@@ -16,7 +16,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;      // positions and windows fit 31 bits
 constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
-constexpr int64_t kMaxSinks = 128;                  // one key tile of the backward pass
+constexpr int64_t kMaxSinks = 128;                  // a few first tokens
 constexpr int64_t kMaxStride = (int64_t)1 << 32;
 
 spmm_status_t bad(const char *msg) { return record_error(SPMM_ERROR_INVALID_VALUE, msg); }
@@ -112,7 +112,7 @@ spmm_status_t check_window(int32_t dtype, const attn_window_t *w)
     if (w->S >= kMaxRows || w->Tq >= kMaxRows || w->Tk >= kMaxRows)
         return bad("S, Tq and Tk must be below 2^30");
     // workgroups of the largest launch, with room
-    if ((w->Tq / 128 + w->Tk / 128 + 2 * w->S) * w->Hq > kMaxGrid ||
+    if (2 * (w->Tq / 32 + w->Tk / 32 + 2 * w->S) * w->Hq > kMaxGrid ||
         w->S * w->Hkv * (w->sinks > 0 ? w->sinks : 1) > kMaxGrid)
         return unsupported("too many workgroups: fewer sequences, rows or heads");
     return SPMM_SUCCESS;

@@ -21,8 +21,6 @@ struct OutRows {
     int64_t row_stride, head_stride;
 };
 
-constexpr int kFwdRows = 128;   // queries of a forward or dq workgroup
-
 struct WindowArgs {
     Rows q, k, v;
     const int32_t *q_rowptr, *k_rowptr;
@@ -38,6 +36,10 @@ struct WindowArgs {
     float *delta;             // [Hq, Tq]
     float *partial;           // see window_bwd.hip
 };
+
+// Whether workgroups of 128 queries are too few to fill the 512 places that
+// the GPU has for them (two to a CU): then 64 queries each.
+inline bool few_tiles(const WindowArgs &a) { return (a.Tq / 128 + a.S) * a.Hq < 1024; }
 
 hipError_t launch_window_fwd(int dtype, const WindowArgs &a, hipStream_t stream);
 hipError_t launch_window_bwd(int dtype, const WindowArgs &a, hipStream_t stream);

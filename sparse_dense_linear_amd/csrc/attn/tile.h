@@ -88,6 +88,22 @@ __device__ inline float sum_halves(float x)
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+__device__ inline float max_of(const f32x16 &x)
+{
+    float m = fmaxf(fmaxf(x[0], x[1]), x[2]);
+#pragma unroll
+    for (int r = 3; r < 15; r += 2)
+        m = fmaxf(fmaxf(m, x[r]), x[r + 1]);
+    return fmaxf(m, x[15]);
+}
+
+// The running maximum of a softmax is a reference, not an exact maximum: it
+// moves (and the output so far is rescaled) only when a score passes it by
+// more than this, in base 2.  Weights then reach up to 2^8, which fp32 sums
+// and bf16 operands hold with the same relative precision.  Without it some
+// query of a wavefront finds a new maximum in almost every tile.
+constexpr float kLazy = 8.0f;
+
 // Eight consecutive elements of global memory (16-byte aligned).
 __device__ inline bf16x8 load8(const __bf16 *p) { return *(const bf16x8 *)p; }
 __device__ inline f32x8 load8(const float *p)
@@ -110,9 +126,37 @@ __device__ inline void store4(float *p, float a, float b, float c, float d)
 
 // ------------------------------------------------------------ LDS tiles
 
+// 16 bytes a lane from `from` (any address) to `to` + 16 * lane, where `to`
+// is the same for the whole wavefront.
+__device__ inline void load_to_lds(const void *from, char *to)
+{
+    typedef __attribute__((address_space(1))) const uint32_t global_u32;
+    typedef __attribute__((address_space(3))) uint32_t lds_u32;
+    __builtin_amdgcn_global_load_lds((global_u32 *)from, (lds_u32 *)to, 16, 0, 0);
+}
+
+// Until every load of this wavefront has arrived.
+__device__ inline void wait_loads()
+{
+    __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt(0), nothing else
+}
+
+// A number that the compiler takes to be new here.  Addresses of fragments
+// differ from a lane's base by an exclusive or and a constant; left alone,
+// the compiler computes all of them (some 60) once before a loop over tiles
+// and has no registers left for the tiles themselves.
+__device__ inline int renewed(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // A tile of ROWS rows of DP elements.  The 16-byte pieces of a row are
-// exchanged among themselves by its row number, so that lanes reading one
-// piece of 16 consecutive rows, or one row across, touch different banks.
+// exchanged among themselves by its row number: neighbouring rows differ by
+// a pair of pieces and every eighth one by the order within the pair, so
+// that 8 lanes that read one piece of 8 consecutive rows, 16 lanes that read
+// 32 bytes of 4 rows, and 32 lanes that read across a row and across the one
+// 4 further touch different banks.  Rows 16 apart are exchanged alike.
 template <class T, int DP, int ROWS>
 struct Tile {
     static constexpr int kRowBytes = DP * (int)sizeof(T);
@@ -120,90 +164,188 @@ struct Tile {
     static constexpr int kElems = 16 / (int)sizeof(T);        // per piece
     static constexpr int kBytes = ROWS * kRowBytes;
     static constexpr int kShift = kRowBytes <= 128 ? 1 : 0;   // rows per 256 bytes
-    static constexpr int kMask = (kPieces < 16 ? kPieces : 16) - 1;
+    static constexpr int kMask = (kPieces < 16 ? kPieces : 16) / 2 - 1;
+
+    __device__ static int exchange(int row)
+    {
+        return ((row >> kShift) & kMask) << 1 | ((row >> 3) & 1);
+    }
 
     __device__ static int at(int row, int piece)
     {
-        return row * kRowBytes + ((piece ^ ((row >> kShift) & kMask)) << 4);
+        return row * kRowBytes + ((piece ^ exchange(row)) << 4);
     }
 
-    // A operand with the tile's rows as rows: row `row`, terms 16 * step +
-    // 8 * half .. + 7 along D.
-    __device__ static Frag<T> row_frag(const char *base, int row, int step, int half)
+    // Where a lane's fragments start: row_frag and col_frag add the rest.
+    __device__ static int row_base(int lane)
+    {
+        return at(lane & 31, (sizeof(T) == 2 ? 1 : 2) * (lane >> 5));
+    }
+    __device__ static int col_base(int lane)
     {
         if constexpr (sizeof(T) == 2) {
-            return *(const bf16x8 *)(base + at(row, 2 * step + half));
+            const int i = lane & 15;
+            const int row = 4 * (lane >> 5) + (i >> 2), d = (lane & 16) + 4 * (i & 3);
+            return at(row, d >> 3) + 2 * (d & 7);
         } else {
-            const f32x4 a = *(const f32x4 *)(base + at(row, 4 * step + 2 * half));
-            const f32x4 b = *(const f32x4 *)(base + at(row, 4 * step + 2 * half + 1));
+            return at(4 * (lane >> 5), (lane & 31) >> 2) + 4 * (lane & 3);
+        }
+    }
+
+    // A operand with the tile's rows as rows: row 32 * block + lane % 32,
+    // terms 16 * step + 8 * half .. + 7 along D.
+    __device__ static Frag<T> row_frag(const char *tile, int row_base, int block, int step)
+    {
+        const char *p = tile + 32 * block * kRowBytes;
+        if constexpr (sizeof(T) == 2) {
+            return *(const bf16x8 *)(p + (row_base ^ (step << 5)));
+        } else {
+            const f32x4 a = *(const f32x4 *)(p + (row_base ^ (step << 6)));
+            const f32x4 b = *(const f32x4 *)(p + (row_base ^ (step << 6 | 16)));
             return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
 
-    // A operand with D as rows (32 * block + l % 32) and 16 of the tile's
-    // rows, from `first` on, as terms in the order of result_frag.  bf16: two
+    // A operand with D as rows (32 * block + l % 32) and the tile's rows
+    // 16 * group .. + 15 as terms in the order of result_frag.  bf16: two
     // transposing reads (each group of 16 lanes hands in 4 rows of 16
     // elements and takes one column of them per lane).
-    __device__ static Frag<T> col_frag(const char *base, int first, int block, int lane)
+    __device__ static Frag<T> col_frag(const char *tile, int col_base, int group, int block)
     {
-        const int half = lane >> 5;
+        const char *p = tile + 16 * group * kRowBytes;
         if constexpr (sizeof(T) == 2) {
-            const int i = lane & 15;
-            const int row = first + 4 * half + (i >> 2);
-            const int d = 32 * block + (lane & 16) + 4 * (i & 3);
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
             const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4 *)(base + at(row, d >> 3) + 2 * (d & 7)));
+                (lds_s16x4 *)(p + (col_base ^ (block << 6))));
             const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4 *)(base + at(row + 8, d >> 3) + 2 * (d & 7)));
+                (lds_s16x4 *)(p + 8 * kRowBytes + (col_base ^ exchanged(8) ^ (block << 6))));
             const auto ab = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
             return __builtin_bit_cast(bf16x8, ab);
         } else {
-            const int d = 32 * block + (lane & 31);
             f32x8 f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int row = first + 4 * half + (e & 3) + 8 * (e >> 2);
-                f[e] = *(const float *)(base + at(row, d >> 2) + 4 * (d & 3));
+                const int row = (e & 3) + 8 * (e >> 2);
+                f[e] = *(const float *)(p + row * kRowBytes + (col_base ^ exchanged(row) ^ (block << 7)));
             }
             return f;
         }
     }
+
+    // The exchange of a row r + c against that of row r, where c = 0 .. 3 or
+    // 8 .. 11 is added to a multiple of 4 below 8, in bytes.  (c and the
+    // multiple share no bit, so the exchange of their sum is that of c
+    // applied to that of the multiple.)
+    __device__ static constexpr int exchanged(int c)
+    {
+        return (((c >> kShift) & kMask) << 1 | ((c >> 3) & 1)) << 4;
+    }
 };
 
-// Pieces of a tile's rows on their way from global memory to LDS: thread t
-// of THREADS carries pieces t, t + THREADS, ...
-template <class T, int DP, int ROWS, int THREADS>
-struct Carrier {
+// A tile's rows on their way from global memory into LDS without passing
+// through registers: a wavefront's lanes write 16 consecutive bytes each, so
+// the exchange of pieces is done on the side of the addresses that are read.
+// Each of WAVES wavefronts moves its share; the tile is whole once all of
+// them have passed wait_loads() and a barrier.
+//
+// Row r of the tile at `first` is row min(first + r, last) of the operand;
+// pieces past D repeat the row's last one, whose products meet zeros of the
+// other operand.
+template <class T, int DP, int ROWS, int WAVES>
+struct Stager {
     typedef Tile<T, DP, ROWS> Tl;
-    static constexpr int kCount = ROWS * Tl::kPieces / THREADS;
-    static_assert(ROWS * Tl::kPieces % THREADS == 0, "whole pieces per thread");
-    u32x4 piece[kCount];
+    static constexpr int kThreads = 64 * WAVES;
+    static constexpr int kCount = ROWS * Tl::kPieces / kThreads;
+    static constexpr int kStep = kThreads / Tl::kPieces;      // rows of one turn
+    static_assert(ROWS * Tl::kPieces % kThreads == 0, "whole pieces per thread");
+    static_assert(kStep * Tl::kPieces == kThreads, "whole rows per turn");
 
-    // Row r of the tile is row min(first + r, last) of `base` (element
-    // stride `stride`); pieces past D repeat the row's last one, whose
-    // products meet zeros of the other operand.
-    __device__ void load(const T *base, int64_t stride, int first, int last, int D, int t)
+    static_assert(kStep % 8 == 0, "every second turn is exchanged alike");
+
+    int64_t stride;
+    int row, d[2];            // the lane's row of a turn; its element in even and odd turns
+    uint32_t offset[2];       // row * stride + d in bytes
+    bool near;                // which fits 32 bits
+
+    __device__ Stager(int64_t stride_, int D, int wave, int lane) : stride(stride_)
     {
+        const int n = wave * 64 + lane;
+        row = n / Tl::kPieces;
+        near = kStep * stride * (int64_t)sizeof(T) < ((int64_t)1 << 31);
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            const int n = t + i * THREADS;
-            const int r = n / Tl::kPieces, p = n % Tl::kPieces;
-            const int row = first + r < last ? first + r : last;
-            const int d = p * Tl::kElems < D ? p * Tl::kElems : D - Tl::kElems;
-            piece[i] = *(const u32x4 *)(base + (int64_t)row * stride + d);
+        for (int i = 0; i < 2; ++i) {
+            const int p = (n % Tl::kPieces) ^ Tl::exchange(row + i * kStep);
+            d[i] = p * Tl::kElems < D ? p * Tl::kElems : D - Tl::kElems;
+            offset[i] = (uint32_t)((row * stride + d[i]) * (int64_t)sizeof(T));
         }
     }
 
-    __device__ void store(char *tile, int t) const
+    __device__ void load(char *tile, const T *base, int first, int last, int wave) const
     {
+        char *to = tile + wave * 1024;
+        if (near && first + ROWS - 1 <= last) {
+            // all rows are there: one scalar address a turn, one offset a lane
+            const char *from = (const char *)(base + first * stride);
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            const int n = t + i * THREADS;
-            *(u32x4 *)(tile + Tl::at(n / Tl::kPieces, n % Tl::kPieces)) = piece[i];
+            for (int i = 0; i < kCount; ++i)
+                load_to_lds(from + i * kStep * stride * (int64_t)sizeof(T) + offset[i & 1],
+                            to + i * kThreads * 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kCount; ++i) {
+                const int r = first + i * kStep + row < last ? first + i * kStep + row : last;
+                load_to_lds(base + r * stride + d[i & 1], to + i * kThreads * 16);
+            }
         }
     }
 };
+
+// A wavefront's 32 columns of DP results to LDS and back, for the wavefronts
+// that share them: `block` of the results is rows 32 * block .. of D.
+template <int DP>
+struct Parked {
+    typedef Tile<float, DP, 32> Tl;
+    static constexpr int kBytes = Tl::kBytes;
+    __device__ static void put(char *to, int lane, const f32x16 (&x)[DP / 32])
+    {
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                store4((float *)(to + Tl::at(lane & 31, 8 * d + 2 * g + (lane >> 5))), x[d][4 * g],
+                       x[d][4 * g + 1], x[d][4 * g + 2], x[d][4 * g + 3]);
+    }
+    // x = mine * x + theirs * what was put
+    __device__ static void add(const char *from, int lane, float mine, float theirs,
+                               f32x16 (&x)[DP / 32])
+    {
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 y =
+                    *(const f32x4 *)(from + Tl::at(lane & 31, 8 * d + 2 * g + (lane >> 5)));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[d][4 * g + e] = fmaf(theirs, y[e], mine * x[d][4 * g + e]);
+            }
+    }
+};
+
+// Asks the compiler to keep `ahead` LDS reads in front of the matrix
+// instructions of a chain of `count` of them (one read each) instead of
+// waiting for each read right where it is used.
+template <int COUNT, int AHEAD>
+__device__ inline void read_ahead()
+{
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < COUNT - AHEAD; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
+}
 
 // --------------------------------------------------------------- window
 
@@ -213,7 +355,8 @@ struct Seen {
     int window, sinks;
     __device__ bool operator()(int p, int j) const
     {
-        return j <= p && (p - j < window || j < sinks);
+        // p - j as unsigned: a later key is past every limit
+        return (uint32_t)(p - j) < (uint32_t)(j < sinks ? 0x7fffffff : window);
     }
     // every key of j0 .. j1 seen from every position of p0 .. p1
     __device__ bool all(int p0, int p1, int j0, int j1) const

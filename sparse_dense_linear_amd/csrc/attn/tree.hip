@@ -302,10 +302,11 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
                 const int j0 = first_key(u, n) + 32 * b;
                 if (j0 >= u.end || (j0 + 31 < u.low && j0 >= a.sinks))
                     continue;
+                const int rows_at = renewed(Tl::row_base(lane)), cols_at = renewed(Tl::col_base(lane));
                 f32x16 x = f32x16(0.0f);
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s)
-                    x = mma(Tl::row_frag(kt, 32 * b + (lane & 31), s, half), qf[s], x);
+                    x = mma(Tl::row_frag(kt, rows_at, b, s), qf[s], x);
                 const bool whole = j0 + 31 < u.ctx && (u.end - 1 - j0 < a.window || j0 + 31 < a.sinks);
                 float most = SDL_NEG_INF;
 #pragma unroll
@@ -337,7 +338,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
                     const Frag<T> pf = result_frag<T>(x, s);
 #pragma unroll
                     for (int d = 0; d < DB; ++d)
-                        O[d] = mma(Tl::col_frag(vt, 32 * b + 16 * s, d, lane), pf, O[d]);
+                        O[d] = mma(Tl::col_frag(vt, cols_at, 2 * b + s, d), pf, O[d]);
                 }
             }
             __syncthreads();

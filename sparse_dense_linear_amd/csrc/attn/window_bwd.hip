@@ -17,16 +17,17 @@
 // each; those and the window's part leave fp32 partial sums, which a last
 // small launch adds in a fixed order.
 #include "ops.h"
+
 #include "exact.h"
-#include "tile.h"
 #include "spmm.h"
+#include "tile.h"
 
 namespace sdl {
 
 namespace {
 
-constexpr int kKeyRows = 128;     // keys of a dk/dv workgroup
-constexpr int kStepRows = 32;     // queries of one step of it
+constexpr int kKeyRows = 64;      // keys of a dk/dv workgroup
+constexpr int kStepRows = 64;     // queries of one step of it
 constexpr int kFarRows = 512;     // queries of a far run
 
 template <class T>
@@ -48,34 +49,55 @@ __device__ GradRows<T> grad_rows(const WindowArgs &a, int q_begin, int k_begin, 
 
 // ------------------------------------------------------------------- dq
 
-template <class T, int DP>
+template <class T, int DP, int RG>
 __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_dq(WindowArgs a, int slots)
 {
-    constexpr int KT = sizeof(T) == 2 ? 64 : (DP == 64 ? 64 : 32);
-    constexpr int SB = KT / 32, STEPS = DP / 16, DB = DP / 32;
+    constexpr int KT = 64;                       // keys of a tile
+    constexpr int KS = 4 / RG;                   // wavefronts that share a group's keys
+    constexpr int NB = KT / 32 / KS;             // 32-key blocks of a wavefront
+    constexpr int STEPS = DP / 16, DB = DP / 32;
+    constexpr int kRows = 32 * RG;
     typedef Tile<T, DP, KT> Tl;
-    __shared__ __align__(16) char lds[2][2][Tl::kBytes];
+    __shared__ __align__(16) char k_even[Tl::kBytes], v_even[Tl::kBytes], k_odd[Tl::kBytes], v_odd[Tl::kBytes];
 
     const int group = a.Hq / a.Hkv;
     const int idx = xcd_order(blockIdx.x, gridDim.x);
     const int hk = idx / (slots * group), rest = idx % (slots * group);
     const int head = hk * group + rest % group;
-    const SeqTile st = find_seq_tile(a.q_rowptr, a.S, kFwdRows, slots - 1 - rest / group);
+    const SeqTile st = find_seq_tile(a.q_rowptr, a.S, kRows, slots - 1 - rest / group);
     if (st.seq < 0)
         return;
     const int q_begin = a.q_rowptr[st.seq], lq = a.q_rowptr[st.seq + 1] - q_begin;
     const int k_begin = a.k_rowptr[st.seq], lk = a.k_rowptr[st.seq + 1] - k_begin;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ks = KS == 1 ? 0 : wave / RG;
     const Seen seen = {a.window, a.sinks};
     const int shift = lk - lq;
-    const int i0 = st.tile * kFwdRows, i1 = (i0 + kFwdRows < lq ? i0 + kFwdRows : lq) - 1;
-    const int wi0 = i0 + 32 * wave;
+    const int i0 = st.tile * kRows, i1 = (i0 + kRows < lq ? i0 + kRows : lq) - 1;
+    const int wi0 = i0 + 32 * (wave % RG);
     const int qi = wi0 + (lane & 31);
     const int pos = qi + shift;
     const int wp0 = wi0 + shift, wp1 = (wi0 + 31 < i1 ? wi0 + 31 : i1) + shift;
     const float c2 = a.scale * kLog2e;
     const GradRows<T> r = grad_rows<T>(a, q_begin, k_begin, head, hk);
     const int row = qi < lq ? qi : lq - 1;
+
+    const int p0 = i0 + shift, p1 = i1 + shift;
+    const int low = p0 - seen.window + 1 > 0 ? p0 - seen.window + 1 : 0;
+    const int band = low / KT;
+    int first_tiles = (seen.sinks + KT - 1) / KT;
+    first_tiles = first_tiles < band ? first_tiles : band;
+    const int count = p1 < 0 ? 0 : first_tiles + p1 / KT + 1 - band;
+
+    const Stager<T, DP, KT, 4> k_in(r.k_stride, a.D, wave, lane), v_in(r.v_stride, a.D, wave, lane);
+    auto first_key = [&](int n) { return (n < first_tiles ? n : band + n - first_tiles) * KT; };
+    auto fetch = [&](int n, char *kt, char *vt) {
+        k_in.load(kt, r.k, first_key(n), lk - 1, wave);
+        v_in.load(vt, r.v, first_key(n), lk - 1, wave);
+    };
+    if (count > 0)
+        fetch(0, k_even, v_even);
 
     Frag<T> qf[STEPS], gf[STEPS];
     float delta = 0.0f;
@@ -94,7 +116,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
                 delta = fmaf((float)gf[s][e], (float)of[e], delta);
         }
         delta = sum_halves(delta);
-        if (qi <= i1 && half == 0)
+        if (qi <= i1 && half == 0 && ks == 0)
             a.delta[(int64_t)head * a.Tq + q_begin + qi] = delta;
     }
     const float lse2 = r.lse[row] * kLog2e;
@@ -104,64 +126,70 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     for (int d = 0; d < DB; ++d)
         dQ[d] = f32x16(0.0f);
 
-    const int p0 = i0 + shift, p1 = i1 + shift;
-    const int low = p0 - seen.window + 1 > 0 ? p0 - seen.window + 1 : 0;
-    const int band = low / KT;
-    int first_tiles = (seen.sinks + KT - 1) / KT;
-    first_tiles = first_tiles < band ? first_tiles : band;
-    const int count = p1 < 0 ? 0 : first_tiles + p1 / KT + 1 - band;
-
-    Carrier<T, DP, KT, kAttnThreads> ck, cv;
-    if (count > 0) {
-        const int j0 = (first_tiles > 0 ? 0 : band) * KT;
-        ck.load(r.k, r.k_stride, j0, lk - 1, a.D, t);
-        cv.load(r.v, r.v_stride, j0, lk - 1, a.D, t);
-        ck.store(lds[0][0], t);
-        cv.store(lds[0][1], t);
-    }
-    __syncthreads();
-    for (int n = 0; n < count; ++n) {
-        const int j0 = (n < first_tiles ? n : band + n - first_tiles) * KT;
-        if (n + 1 < count) {
-            const int next = (n + 1 < first_tiles ? n + 1 : band + n + 1 - first_tiles) * KT;
-            ck.load(r.k, r.k_stride, next, lk - 1, a.D, t);
-            cv.load(r.v, r.v_stride, next, lk - 1, a.D, t);
-        }
-        if (wi0 <= i1 && !seen.none(wp0, wp1, j0, j0 + KT - 1)) {
-            const char *kt = lds[n & 1][0], *vt = lds[n & 1][1];
-            const bool whole = seen.all(wp0, wp1, j0, j0 + KT - 1);
+    auto compute = [&](int n, const char *kt, const char *vt) {
+        if (wi0 > i1)
+            return;
 #pragma unroll
-            for (int b = 0; b < SB; ++b) {
-                f32x16 x = f32x16(0.0f), dp = f32x16(0.0f);
+        for (int b = 0; b < NB; ++b) {
+            const int j0 = first_key(n) + 32 * (NB * ks + b);
+            if (seen.none(wp0, wp1, j0, j0 + 31))
+                continue;
+            const int rows_at = renewed(Tl::row_base(lane) + 32 * NB * ks * Tl::kRowBytes);
+            const int cols_at = renewed(Tl::col_base(lane) + 32 * NB * ks * Tl::kRowBytes);
+            f32x16 x = f32x16(0.0f), dp = f32x16(0.0f);
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    x = mma(Tl::row_frag(kt, 32 * b + (lane & 31), s, half), qf[s], x);
-                    dp = mma(Tl::row_frag(vt, 32 * b + (lane & 31), s, half), gf[s], dp);
-                }
+            for (int s = 0; s < STEPS; ++s) {
+                x = mma(Tl::row_frag(kt, rows_at, b, s), qf[s], x);
+                dp = mma(Tl::row_frag(vt, rows_at, b, s), gf[s], dp);
+            }
+            if constexpr (sizeof(T) == 2)
+                read_ahead<2 * STEPS, 6>();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(fmaf(x[i], c2, -lse2));
-                    float ds = p * (dp[i] - delta);
-                    if (!whole && !seen(pos, j0 + 32 * b + 8 * (i >> 2) + 4 * half + (i & 3)))
-                        ds = 0.0f;
-                    x[i] = ds;
-                }
+            for (int i = 0; i < 16; ++i)
+                x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c2, -lse2)) * (dp[i] - delta);
+            if (!seen.all(wp0, wp1, j0, j0 + 31)) {
+                const int p = renewed(pos);    // keeps the comparisons on this side of the branch
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const Frag<T> df = result_frag<T>(x, s);
+                for (int i = 0; i < 16; ++i)
+                    if (!seen(p, j0 + 8 * (i >> 2) + 4 * half + (i & 3)))
+                        x[i] = 0.0f;
+            }
 #pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        dQ[d] = mma(Tl::col_frag(kt, 32 * b + 16 * s, d, lane), df, dQ[d]);
-                }
+            for (int s = 0; s < 2; ++s) {
+                const Frag<T> df = result_frag<T>(x, s);
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    dQ[d] = mma(Tl::col_frag(kt, cols_at, 2 * b + s, d), df, dQ[d]);
             }
         }
-        if (n + 1 < count) {
-            ck.store(lds[(n + 1) & 1][0], t);
-            cv.store(lds[(n + 1) & 1][1], t);
-        }
+    };
+    wait_loads();
+    __syncthreads();
+    for (int n = 0; n < count; n += 2) {
+        if (n + 1 < count)
+            fetch(n + 1, k_odd, v_odd);
+        compute(n, k_even, v_even);
+        wait_loads();
+        __syncthreads();
+        if (n + 1 >= count)
+            break;
+        if (n + 2 < count)
+            fetch(n + 2, k_even, v_even);
+        compute(n + 1, k_odd, v_odd);
+        wait_loads();
         __syncthreads();
     }
 
+    if constexpr (KS == 2) {
+        static_assert(RG == 2 && Parked<DP>::kBytes <= Tl::kBytes, "a buffer for each group");
+        char *room = wave % RG == 0 ? k_even : k_odd;
+        if (ks == 1)
+            Parked<DP>::put(room, lane, dQ);
+        __syncthreads();
+        if (ks == 1)
+            return;
+        Parked<DP>::add(room, lane, 1.0f, 1.0f, dQ);
+    }
     if (wi0 > i1)
         return;
     const bool some = pos >= 0;
@@ -241,39 +269,45 @@ __device__ void exact_dkv_row(const WindowArgs &a, int q_begin, int k_begin, int
     put_row(v, dv[0], dv[1], a.D, lane);
 }
 
+// Two wavefronts share 32 keys and take the halves of each step's queries;
+// their sums are joined at the end.
 template <class T, int DP>
-__global__ __launch_bounds__(kAttnThreads, 1) void window_dkv(WindowArgs a, int key_slots, int far_slots)
+__global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_dkv(WindowArgs a, int key_slots,
+                                                                                   int far_slots, int far_tiles)
 {
     constexpr int QT = kStepRows, STEPS = DP / 16, DB = DP / 32;
     typedef Tile<T, DP, QT> Tl;
-    __shared__ __align__(16) char lds[2][2][Tl::kBytes];
-    __shared__ float row_lse[2][QT], row_delta[2][QT];
+    __shared__ __align__(16) char q_even[Tl::kBytes], g_even[Tl::kBytes], q_odd[Tl::kBytes], g_odd[Tl::kBytes];
+    __shared__ __align__(16) float stat_even[2 * QT], stat_odd[2 * QT];    // lse, delta
 
     const int group = a.Hq / a.Hkv;
-    const int per_head = key_slots + far_slots;
+    const int far_items = far_slots * far_tiles;
+    const int per_head = key_slots + far_items;
     const int idx = xcd_order(blockIdx.x, gridDim.x);
     const int hk = idx / per_head, rest = idx % per_head;
-    const bool far = rest < far_slots;
-    const SeqTile st = far ? find_seq_tile(a.q_rowptr, a.S, kFarRows, rest)
-                           : find_seq_tile(a.k_rowptr, a.S, kKeyRows, rest - far_slots);
+    const bool far = rest < far_items;
+    const SeqTile st = far ? find_seq_tile(a.q_rowptr, a.S, kFarRows, rest / far_tiles)
+                           : find_seq_tile(a.k_rowptr, a.S, kKeyRows, rest - far_items);
     if (st.seq < 0)
         return;
     const int q_begin = a.q_rowptr[st.seq], lq = a.q_rowptr[st.seq + 1] - q_begin;
     const int k_begin = a.k_rowptr[st.seq], lk = a.k_rowptr[st.seq + 1] - k_begin;
-    if (lk <= 0)
+    const int j0 = (far ? rest % far_tiles : st.tile) * kKeyRows;
+    if (j0 >= lk)
         return;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
+    const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int kw = wave & 1, qw = wave >> 1;
     const Seen seen = {a.window, a.sinks};
     const int shift = lk - lq;
-    const int j0 = far ? 0 : st.tile * kKeyRows;
     const int j1 = (j0 + kKeyRows < lk ? j0 + kKeyRows : lk) - 1;
-    const int wj0 = j0 + 32 * wave, wj1 = wj0 + 31 < j1 ? wj0 + 31 : j1;
+    const int wj0 = j0 + 32 * kw, wj1 = wj0 + 31 < j1 ? wj0 + 31 : j1;
     const int key = wj0 + (lane & 31);
     const float c2 = a.scale * kLog2e;
 
     StepRange steps = window_steps(j0, j1, seen.window, shift, lq);
     const int all_steps = (lq + QT - 1) / QT;
-    const bool has_far = j0 == 0 && seen.sinks > 0 && steps.to < all_steps;
+    const bool has_far = j0 < seen.sinks && steps.to < all_steps;
     if (far) {
         const int b = st.tile * (kFarRows / QT), e = b + kFarRows / QT;
         steps.from = b > steps.to ? b : steps.to;
@@ -282,6 +316,34 @@ __global__ __launch_bounds__(kAttnThreads, 1) void window_dkv(WindowArgs a, int 
             return;
     }
     const bool working = wj0 <= j1 && (!far || wj0 < seen.sinks);
+
+    // items: head of the group, then step
+    const int count = group * (steps.to - steps.from);
+    float carried = 0.0f;            // lse or delta of one row on its way to LDS
+    const Stager<T, DP, QT, 4> q_in(a.q.row_stride, a.D, wave, lane), g_in(a.dout.row_stride, a.D, wave, lane);
+    int next_head = hk * group, next_step = steps.from;     // of the next fetch
+    auto fetch = [&](char *qt, char *gt) {
+        const int first = next_step * QT;
+        const GradRows<T> r = grad_rows<T>(a, q_begin, k_begin, next_head, hk);
+        q_in.load(qt, r.q, first, lq - 1, wave);
+        g_in.load(gt, r.dout, first, lq - 1, wave);
+        if (t < 2 * QT) {
+            const int i = first + (t & (QT - 1)) < lq ? first + (t & (QT - 1)) : lq - 1;
+            carried = t < QT ? r.lse[i] * kLog2e : r.delta[i];
+        }
+        if (++next_step == steps.to) {
+            next_step = steps.from;
+            ++next_head;
+        }
+    };
+    auto arrive = [&](float *stat) {
+        wait_loads();
+        if (t < 2 * QT)
+            stat[t] = carried;
+        __syncthreads();
+    };
+    if (count > 0)
+        fetch(q_even, g_even);
 
     Frag<T> kf[STEPS], vf[STEPS];
     {
@@ -302,85 +364,83 @@ __global__ __launch_bounds__(kAttnThreads, 1) void window_dkv(WindowArgs a, int 
         dV[d] = f32x16(0.0f);
     }
 
-    // items: head of the group, then step
-    const int n_steps = steps.to - steps.from;
-    const int count = group * n_steps;
-    Carrier<T, DP, QT, kAttnThreads> cq, cg;
-    float stat = 0.0f;
-    auto fetch = [&](int n) {
-        const int head = hk * group + n / n_steps, first = (steps.from + n % n_steps) * QT;
-        const GradRows<T> r = grad_rows<T>(a, q_begin, k_begin, head, hk);
-        cq.load(r.q, r.q_stride, first, lq - 1, a.D, t);
-        cg.load(r.dout, r.dout_stride, first, lq - 1, a.D, t);
-        if (t < 2 * QT) {
-            const int i = first + (t & (QT - 1)) < lq ? first + (t & (QT - 1)) : lq - 1;
-            stat = t < QT ? r.lse[i] * kLog2e : r.delta[i];
+    int this_step = steps.from;
+    auto compute = [&](const char *qt, const char *gt, const float *stat) {
+        const int first = this_step * QT + 32 * qw;          // the wavefront's rows
+        const int last = (first + 32 < lq ? first + 32 : lq) - 1;
+        if (++this_step == steps.to)
+            this_step = steps.from;
+        if (!working || first > last || seen.none(first + shift, last + shift, wj0, wj1))
+            return;
+        const int rows_at = renewed(Tl::row_base(lane) + 32 * qw * Tl::kRowBytes);
+        const int cols_at = renewed(Tl::col_base(lane) + 32 * qw * Tl::kRowBytes);
+        f32x16 x = f32x16(0.0f), dp = f32x16(0.0f);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            x = mma(Tl::row_frag(qt, rows_at, 0, s), kf[s], x);
+            dp = mma(Tl::row_frag(gt, rows_at, 0, s), vf[s], dp);
         }
-    };
-    auto stash = [&](int buf) {
-        cq.store(lds[buf][0], t);
-        cg.store(lds[buf][1], t);
-        if (t < QT)
-            row_lse[buf][t] = stat;
-        else if (t < 2 * QT)
-            row_delta[buf][t - QT] = stat;
-    };
-    if (count > 0) {
-        fetch(0);
-        stash(0);
-    }
-    __syncthreads();
-    for (int n = 0; n < count; ++n) {
-        if (n + 1 < count)
-            fetch(n + 1);
-        const int first = (steps.from + n % n_steps) * QT;
-        const int last = (first + QT < lq ? first + QT : lq) - 1;
-        if (working && !seen.none(first + shift, last + shift, wj0, wj1)) {
-            const char *qt = lds[n & 1][0], *gt = lds[n & 1][1];
-            f32x16 x = f32x16(0.0f), dp = f32x16(0.0f);
+        if constexpr (sizeof(T) == 2)
+            read_ahead<2 * STEPS, 4>();
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                x = mma(Tl::row_frag(qt, lane & 31, s, half), kf[s], x);
-                dp = mma(Tl::row_frag(gt, lane & 31, s, half), vf[s], dp);
-            }
-            const bool whole =
-                last == first + QT - 1 && seen.all(first + shift, last + shift, wj0, wj0 + 31);
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 l4 = *(const f32x4 *)(stat + 32 * qw + 8 * g + 4 * half);
+            const f32x4 d4 = *(const f32x4 *)(stat + QT + 32 * qw + 8 * g + 4 * half);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const f32x4 l4 = *(const f32x4 *)(row_lse[n & 1] + 8 * g + 4 * half);
-                const f32x4 d4 = *(const f32x4 *)(row_delta[n & 1] + 8 * g + 4 * half);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = first + 8 * g + 4 * half + e;
-                    float p = __builtin_amdgcn_exp2f(fmaf(x[4 * g + e], c2, -l4[e]));
-                    float ds = p * (dp[4 * g + e] - d4[e]);
-                    if (!whole && !(i <= last && seen(i + shift, key)))
-                        p = ds = 0.0f;
-                    x[4 * g + e] = p;
-                    dp[4 * g + e] = ds;
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const Frag<T> pf = result_frag<T>(x, s), df = result_frag<T>(dp, s);
-#pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    dV[d] = mma(Tl::col_frag(gt, 16 * s, d, lane), pf, dV[d]);
-                    dK[d] = mma(Tl::col_frag(qt, 16 * s, d, lane), df, dK[d]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                x[4 * g + e] = __builtin_amdgcn_exp2f(fmaf(x[4 * g + e], c2, -l4[e]));
+                dp[4 * g + e] = x[4 * g + e] * (dp[4 * g + e] - d4[e]);
             }
         }
+        if (last < first + 31 || !seen.all(first + shift, last + shift, wj0, wj0 + 31)) {
+            const int k = renewed(key);        // keeps the comparisons on this side of the branch
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int row = first + 8 * (i >> 2) + 4 * half + (i & 3);
+                if (!(row <= last && seen(row + shift, k)))
+                    x[i] = dp[i] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const Frag<T> pf = result_frag<T>(x, s), df = result_frag<T>(dp, s);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                dV[d] = mma(Tl::col_frag(gt, cols_at, s, d), pf, dV[d]);
+                dK[d] = mma(Tl::col_frag(qt, cols_at, s, d), df, dK[d]);
+            }
+        }
+    };
+    arrive(stat_even);
+    for (int n = 0; n < count; n += 2) {
         if (n + 1 < count)
-            stash((n + 1) & 1);
-        __syncthreads();
+            fetch(q_odd, g_odd);
+        compute(q_even, g_even, stat_even);
+        arrive(stat_odd);
+        if (n + 1 >= count)
+            break;
+        if (n + 2 < count)
+            fetch(q_even, g_even);
+        compute(q_odd, g_odd, stat_odd);
+        arrive(stat_even);
     }
 
+    static_assert(Parked<DP>::kBytes <= Tl::kBytes, "a buffer for each sum");
+    if (qw == 1) {
+        Parked<DP>::put(kw == 0 ? q_even : q_odd, lane, dK);
+        Parked<DP>::put(kw == 0 ? g_even : g_odd, lane, dV);
+    }
+    __syncthreads();
+    if (qw == 1)
+        return;
+    Parked<DP>::add(kw == 0 ? q_even : q_odd, lane, 1.0f, 1.0f, dK);
+    Parked<DP>::add(kw == 0 ? g_even : g_odd, lane, 1.0f, 1.0f, dV);
     if (!working)
         return;
     bool clean = true;
     const bool part = has_far && key < seen.sinks;    // summed by the last launch
     if (part && key <= j1) {
-        float *to = partial_at(a, far ? rest : far_slots + st.seq, hk, key, DP);
+        float *to = partial_at(a, far ? rest / far_tiles : far_slots + st.seq, hk, key, DP);
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -425,8 +485,9 @@ __global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slot
     const int k_begin = a.k_rowptr[seq], lk = a.k_rowptr[seq + 1] - k_begin;
     if (j >= lk)
         return;
-    const int j1 = (kKeyRows < lk ? kKeyRows : lk) - 1;
-    const StepRange steps = window_steps(0, j1, a.window, lk - lq, lq);
+    const int j0 = j / kKeyRows * kKeyRows;               // its key tile
+    const int j1 = (j0 + kKeyRows < lk ? j0 + kKeyRows : lk) - 1;
+    const StepRange steps = window_steps(j0, j1, a.window, lk - lq, lq);
     if (steps.to >= (lq + kStepRows - 1) / kStepRows)
         return;                                        // no far part: written already
     const int base = q_begin / kFarRows + seq;         // the sequence's first far run
@@ -468,21 +529,29 @@ int64_t far_runs(int64_t S, int64_t Tq, int64_t Tk, int64_t window, int64_t sink
     return sinks > 0 && window < Tk ? Tq / kFarRows + S : 0;
 }
 
+template <class T, int DP, int RG>
+hipError_t launch_dq(const WindowArgs &a, hipStream_t stream)
+{
+    const int64_t slots = a.Tq / (32 * RG) + a.S;
+    window_dq<T, DP, RG><<<dim3((uint32_t)(slots * a.Hq)), kAttnThreads, 0, stream>>>(a, (int)slots);
+    return hipGetLastError();
+}
+
 template <class T, int DP>
 hipError_t launch(const WindowArgs &a, hipStream_t stream)
 {
-    const int64_t slots = a.Tq / kFwdRows + a.S;
     const int64_t key_slots = a.Tk / kKeyRows + a.S;
     const int64_t far = far_runs(a.S, a.Tq, a.Tk, a.window, a.sinks);
+    const int64_t far_tiles = far > 0 ? (a.sinks + kKeyRows - 1) / kKeyRows : 0;
     hipError_t err;
     if (a.Tq > 0) {
-        window_dq<T, DP><<<dim3((uint32_t)(slots * a.Hq)), kAttnThreads, 0, stream>>>(a, (int)slots);
-        if ((err = hipGetLastError()) != hipSuccess)
+        err = few_tiles(a) ? launch_dq<T, DP, 2>(a, stream) : launch_dq<T, DP, 4>(a, stream);
+        if (err != hipSuccess)
             return err;
     }
     if (a.Tk > 0) {
-        window_dkv<T, DP><<<dim3((uint32_t)((key_slots + far) * a.Hkv)), kAttnThreads, 0, stream>>>(
-            a, (int)key_slots, (int)far);
+        window_dkv<T, DP><<<dim3((uint32_t)((key_slots + far * far_tiles) * a.Hkv)), kAttnThreads, 0, stream>>>(
+            a, (int)key_slots, (int)far, (int)far_tiles);
         if ((err = hipGetLastError()) != hipSuccess)
             return err;
         if (far > 0) {
