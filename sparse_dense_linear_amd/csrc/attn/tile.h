@@ -263,21 +263,25 @@ struct Stager {
     static_assert(kStep % 8 == 0, "every second turn is exchanged alike");
 
     int64_t stride;
-    int row, d[2];            // the lane's row of a turn; its element in even and odd turns
-    uint32_t offset[2];       // row * stride + d in bytes
-    bool near;                // which fits 32 bits
+    int D;
+    uint32_t offset[kStep % 16 == 0 ? 1 : 2];   // the lane's bytes of even and odd turns
+    bool near;                                  // which fit 32 bits
 
-    __device__ Stager(int64_t stride_, int D, int wave, int lane) : stride(stride_)
+    // the lane's row of a turn, and its element in turn i
+    __device__ static int row_of(int n) { return n / Tl::kPieces; }
+    __device__ int elem_of(int n, int i) const
     {
-        const int n = wave * 64 + lane;
-        row = n / Tl::kPieces;
+        const int p = (n % Tl::kPieces) ^ Tl::exchange(row_of(n) + i * kStep);
+        return p * Tl::kElems < D ? p * Tl::kElems : D - Tl::kElems;
+    }
+
+    __device__ Stager(int64_t stride_, int D_) : stride(stride_), D(D_)
+    {
+        const int n = threadIdx.x;
         near = kStep * stride * (int64_t)sizeof(T) < ((int64_t)1 << 31);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int p = (n % Tl::kPieces) ^ Tl::exchange(row + i * kStep);
-            d[i] = p * Tl::kElems < D ? p * Tl::kElems : D - Tl::kElems;
-            offset[i] = (uint32_t)((row * stride + d[i]) * (int64_t)sizeof(T));
-        }
+        for (int i = 0; i < (kStep % 16 == 0 ? 1 : 2); ++i)
+            offset[i] = (uint32_t)((row_of(n) * stride + elem_of(n, i)) * (int64_t)sizeof(T));
     }
 
     __device__ void load(char *tile, const T *base, int first, int last, int wave) const
@@ -288,13 +292,15 @@ struct Stager {
             const char *from = (const char *)(base + first * stride);
 #pragma unroll
             for (int i = 0; i < kCount; ++i)
-                load_to_lds(from + i * kStep * stride * (int64_t)sizeof(T) + offset[i & 1],
+                load_to_lds(from + i * kStep * stride * (int64_t)sizeof(T) +
+                                offset[kStep % 16 == 0 ? 0 : i & 1],
                             to + i * kThreads * 16);
         } else {
+            const int n = renewed(threadIdx.x);
 #pragma unroll
             for (int i = 0; i < kCount; ++i) {
-                const int r = first + i * kStep + row < last ? first + i * kStep + row : last;
-                load_to_lds(base + r * stride + d[i & 1], to + i * kThreads * 16);
+                const int r = first + i * kStep + row_of(n);
+                load_to_lds(base + (r < last ? r : last) * stride + elem_of(n, i), to + i * kThreads * 16);
             }
         }
     }
@@ -332,19 +338,25 @@ struct Parked {
     }
 };
 
-// Asks the compiler to keep `ahead` LDS reads in front of the matrix
-// instructions of a chain of `count` of them (one read each) instead of
-// waiting for each read right where it is used.
-template <int COUNT, int AHEAD>
-__device__ inline void read_ahead()
+// COUNT matrix instructions in a row, use(i, read(i)), with the LDS reads of
+// the next AHEAD of them under way.  Left to itself the compiler keeps one
+// operand's registers and waits out the latency of LDS before every
+// instruction, where registers are scarce; the order here is therefore fixed.
+template <int COUNT, int AHEAD, class Read, class Use>
+__device__ inline void chain(Read read, Use use)
 {
-    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+    decltype(read(0)) f[AHEAD];
 #pragma unroll
-    for (int i = 0; i < COUNT - AHEAD; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    for (int i = 0; i < AHEAD; ++i)
+        f[i] = read(i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+        use(i, f[i % AHEAD]);
+        if (i + AHEAD < COUNT)
+            f[i % AHEAD] = read(i + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
 }
 
 // --------------------------------------------------------------- window
@@ -369,6 +381,45 @@ struct Seen {
         return j0 > p1 || (p0 - j1 >= window && j0 >= sinks);
     }
 };
+
+// Scores of one 32 x 32 result whose pair is not seen become -infinity.  Lane:
+// one query at position p; rows: keys from j0 on.  (renewed() keeps the
+// comparisons on the caller's side of its branch: most tiles lie within the
+// window and skip them.)
+__device__ inline void mask_keys(f32x16 &x, const Seen &seen, int p, int j0, int half)
+{
+    const int t = renewed(p - j0 - 4 * half);
+    if (j0 >= seen.sinks) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if ((uint32_t)(t - (8 * (r >> 2) + (r & 3))) >= (uint32_t)seen.window)
+                x[r] = SDL_NEG_INF;
+    } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (!seen(p, p - t + 8 * (r >> 2) + (r & 3)))
+                x[r] = SDL_NEG_INF;
+    }
+}
+
+// The same with one key a lane, rows: queries from position p0 on, of which
+// `count` exist.
+__device__ inline void mask_queries(f32x16 &x, const Seen &seen, int key, int p0, int count, int half)
+{
+    const int t = renewed(p0 - key + 4 * half);
+    const uint32_t limit = key < seen.sinks ? 0x7fffffff : seen.window;
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+        if ((uint32_t)(t + 8 * (r >> 2) + (r & 3)) >= limit)
+            x[r] = SDL_NEG_INF;
+    if (count < 32) {
+        const int left = renewed(count - 4 * half);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (8 * (r >> 2) + (r & 3) >= left)
+                x[r] = SDL_NEG_INF;
+    }
+}
 
 // ------------------------------------------------------------- sequences
 

@@ -47,6 +47,10 @@ __device__ GradRows<T> grad_rows(const WindowArgs &a, int q_begin, int k_begin, 
     return r;
 }
 
+// lse in base 2.  A query that sees nothing has -infinity, which against a
+// masked score would be no number; any finite value gives it weights of 0.
+__device__ inline float base2(float lse) { return lse == SDL_NEG_INF ? 0.0f : lse * kLog2e; }
+
 // ------------------------------------------------------------------- dq
 
 template <class T, int DP, int RG>
@@ -57,6 +61,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     constexpr int NB = KT / 32 / KS;             // 32-key blocks of a wavefront
     constexpr int STEPS = DP / 16, DB = DP / 32;
     constexpr int kRows = 32 * RG;
+    constexpr int kAhead = sizeof(T) == 2 ? 6 : 2;
     typedef Tile<T, DP, KT> Tl;
     __shared__ __align__(16) char k_even[Tl::kBytes], v_even[Tl::kBytes], k_odd[Tl::kBytes], v_odd[Tl::kBytes];
 
@@ -90,7 +95,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     first_tiles = first_tiles < band ? first_tiles : band;
     const int count = p1 < 0 ? 0 : first_tiles + p1 / KT + 1 - band;
 
-    const Stager<T, DP, KT, 4> k_in(r.k_stride, a.D, wave, lane), v_in(r.v_stride, a.D, wave, lane);
+    const Stager<T, DP, KT, 4> k_in(r.k_stride, a.D), v_in(r.v_stride, a.D);
     auto first_key = [&](int n) { return (n < first_tiles ? n : band + n - first_tiles) * KT; };
     auto fetch = [&](int n, char *kt, char *vt) {
         k_in.load(kt, r.k, first_key(n), lk - 1, wave);
@@ -119,7 +124,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
         if (qi <= i1 && half == 0 && ks == 0)
             a.delta[(int64_t)head * a.Tq + q_begin + qi] = delta;
     }
-    const float lse2 = r.lse[row] * kLog2e;
+    const float lse2 = base2(r.lse[row]);
 
     f32x16 dQ[DB];
 #pragma unroll
@@ -137,30 +142,23 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
             const int rows_at = renewed(Tl::row_base(lane) + 32 * NB * ks * Tl::kRowBytes);
             const int cols_at = renewed(Tl::col_base(lane) + 32 * NB * ks * Tl::kRowBytes);
             f32x16 x = f32x16(0.0f), dp = f32x16(0.0f);
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                x = mma(Tl::row_frag(kt, rows_at, b, s), qf[s], x);
-                dp = mma(Tl::row_frag(vt, rows_at, b, s), gf[s], dp);
-            }
-            if constexpr (sizeof(T) == 2)
-                read_ahead<2 * STEPS, 6>();
+            chain<2 * STEPS, kAhead>(
+                [&](int i) { return Tl::row_frag(i & 1 ? vt : kt, rows_at, b, i >> 1); },
+                [&](int i, Frag<T> f) {
+                    if (i & 1)
+                        dp = mma(f, gf[i >> 1], dp);
+                    else
+                        x = mma(f, qf[i >> 1], x);
+                });
+            if (!seen.all(wp0, wp1, j0, j0 + 31))
+                mask_keys(x, seen, pos, j0, half);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c2, -lse2)) * (dp[i] - delta);
-            if (!seen.all(wp0, wp1, j0, j0 + 31)) {
-                const int p = renewed(pos);    // keeps the comparisons on this side of the branch
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (!seen(p, j0 + 8 * (i >> 2) + 4 * half + (i & 3)))
-                        x[i] = 0.0f;
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const Frag<T> df = result_frag<T>(x, s);
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-                    dQ[d] = mma(Tl::col_frag(kt, cols_at, 2 * b + s, d), df, dQ[d]);
-            }
+            const Frag<T> df[2] = {result_frag<T>(x, 0), result_frag<T>(x, 1)};
+            chain<2 * DB, kAhead>(
+                [&](int i) { return Tl::col_frag(kt, cols_at, 2 * b + i / DB, i % DB); },
+                [&](int i, Frag<T> f) { dQ[i % DB] = mma(f, df[i / DB], dQ[i % DB]); });
         }
     };
     wait_loads();
@@ -276,6 +274,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
                                                                                    int far_slots, int far_tiles)
 {
     constexpr int QT = kStepRows, STEPS = DP / 16, DB = DP / 32;
+    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
     typedef Tile<T, DP, QT> Tl;
     __shared__ __align__(16) char q_even[Tl::kBytes], g_even[Tl::kBytes], q_odd[Tl::kBytes], g_odd[Tl::kBytes];
     __shared__ __align__(16) float stat_even[2 * QT], stat_odd[2 * QT];    // lse, delta
@@ -320,7 +319,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     // items: head of the group, then step
     const int count = group * (steps.to - steps.from);
     float carried = 0.0f;            // lse or delta of one row on its way to LDS
-    const Stager<T, DP, QT, 4> q_in(a.q.row_stride, a.D, wave, lane), g_in(a.dout.row_stride, a.D, wave, lane);
+    const Stager<T, DP, QT, 4> q_in(a.q.row_stride, a.D), g_in(a.dout.row_stride, a.D);
     int next_head = hk * group, next_step = steps.from;     // of the next fetch
     auto fetch = [&](char *qt, char *gt) {
         const int first = next_step * QT;
@@ -329,7 +328,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
         g_in.load(gt, r.dout, first, lq - 1, wave);
         if (t < 2 * QT) {
             const int i = first + (t & (QT - 1)) < lq ? first + (t & (QT - 1)) : lq - 1;
-            carried = t < QT ? r.lse[i] * kLog2e : r.delta[i];
+            carried = t < QT ? base2(r.lse[i]) : r.delta[i];
         }
         if (++next_step == steps.to) {
             next_step = steps.from;
@@ -375,13 +374,16 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
         const int rows_at = renewed(Tl::row_base(lane) + 32 * qw * Tl::kRowBytes);
         const int cols_at = renewed(Tl::col_base(lane) + 32 * qw * Tl::kRowBytes);
         f32x16 x = f32x16(0.0f), dp = f32x16(0.0f);
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            x = mma(Tl::row_frag(qt, rows_at, 0, s), kf[s], x);
-            dp = mma(Tl::row_frag(gt, rows_at, 0, s), vf[s], dp);
-        }
-        if constexpr (sizeof(T) == 2)
-            read_ahead<2 * STEPS, 4>();
+        chain<2 * STEPS, kAhead>(
+            [&](int i) { return Tl::row_frag(i & 1 ? gt : qt, rows_at, 0, i >> 1); },
+            [&](int i, Frag<T> f) {
+                if (i & 1)
+                    dp = mma(f, vf[i >> 1], dp);
+                else
+                    x = mma(f, kf[i >> 1], x);
+            });
+        if (last < first + 31 || !seen.all(first + shift, last + shift, wj0, wj0 + 31))
+            mask_queries(x, seen, key, first + shift, last + 1 - first, half);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const f32x4 l4 = *(const f32x4 *)(stat + 32 * qw + 8 * g + 4 * half);
@@ -392,24 +394,17 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
                 dp[4 * g + e] = x[4 * g + e] * (dp[4 * g + e] - d4[e]);
             }
         }
-        if (last < first + 31 || !seen.all(first + shift, last + shift, wj0, wj0 + 31)) {
-            const int k = renewed(key);        // keeps the comparisons on this side of the branch
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int row = first + 8 * (i >> 2) + 4 * half + (i & 3);
-                if (!(row <= last && seen(row + shift, k)))
-                    x[i] = dp[i] = 0.0f;
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const Frag<T> pf = result_frag<T>(x, s), df = result_frag<T>(dp, s);
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                dV[d] = mma(Tl::col_frag(gt, cols_at, s, d), pf, dV[d]);
-                dK[d] = mma(Tl::col_frag(qt, cols_at, s, d), df, dK[d]);
-            }
-        }
+        const Frag<T> pf[2] = {result_frag<T>(x, 0), result_frag<T>(x, 1)};
+        const Frag<T> df[2] = {result_frag<T>(dp, 0), result_frag<T>(dp, 1)};
+        chain<4 * DB, kAhead>(
+            [&](int i) { return Tl::col_frag(i & 1 ? qt : gt, cols_at, i / (2 * DB), (i >> 1) % DB); },
+            [&](int i, Frag<T> f) {
+                const int d = (i >> 1) % DB;
+                if (i & 1)
+                    dK[d] = mma(f, df[i / (2 * DB)], dK[d]);
+                else
+                    dV[d] = mma(f, pf[i / (2 * DB)], dV[d]);
+            });
     };
     arrive(stat_even);
     for (int n = 0; n < count; n += 2) {

@@ -32,6 +32,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_f
     constexpr int NB = KT / 32 / KS;             // 32-key blocks of a wavefront
     constexpr int STEPS = DP / 16, DB = DP / 32;
     constexpr int kRows = 32 * RG;
+    constexpr int kAhead = sizeof(T) == 2 ? 6 : 2;
     typedef Tile<T, DP, KT> Tl;
     // K and V, two buffers of each; four objects, so that the compiler sees
     // that reading one does not wait for loads into another
@@ -73,7 +74,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_f
     first_tiles = first_tiles < band ? first_tiles : band;
     const int count = p1 < 0 ? 0 : first_tiles + p1 / KT + 1 - band;
 
-    const Stager<T, DP, KT, 4> k_in(a.k.row_stride, a.D, wave, lane), v_in(a.v.row_stride, a.D, wave, lane);
+    const Stager<T, DP, KT, 4> k_in(a.k.row_stride, a.D), v_in(a.v.row_stride, a.D);
     auto first_key = [&](int n) { return (n < first_tiles ? n : band + n - first_tiles) * KT; };
     auto fetch = [&](int n, char *kt, char *vt) {
         k_in.load(kt, K, first_key(n), lk - 1, wave);
@@ -101,22 +102,15 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_f
         const int cols_at = renewed(Tl::col_base(lane) + 32 * NB * ks * Tl::kRowBytes);
         f32x16 x[NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
+        for (int b = 0; b < NB; ++b)
             x[b] = f32x16(0.0f);
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s)
-                x[b] = mma(Tl::row_frag(kt, rows_at, b, s), qf[s], x[b]);
-        }
-        if constexpr (sizeof(T) == 2)
-            read_ahead<NB * STEPS, 6>();
+        chain<NB * STEPS, kAhead>(
+            [&](int i) { return Tl::row_frag(kt, rows_at, i / STEPS, i % STEPS); },
+            [&](int i, Frag<T> f) { x[i / STEPS] = mma(f, qf[i % STEPS], x[i / STEPS]); });
         if (!seen.all(wp0, wp1, j0, j1)) {
-            const int p = renewed(pos);        // keeps the comparisons on this side of the branch
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (!seen(p, j0 + 32 * b + 8 * (r >> 2) + 4 * half + (r & 3)))
-                        x[b][r] = SDL_NEG_INF;
+                mask_keys(x[b], seen, pos, j0 + 32 * b, half);
         }
         float most = max_of(x[0]);
 #pragma unroll
