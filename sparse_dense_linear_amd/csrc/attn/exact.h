@@ -5,8 +5,12 @@
 // row of V (K, q, do) all the same; where that row holds an infinity or a
 // NaN the product is NaN, though the pair is not part of the result.  A row
 // that comes out of a tiled kernel non-finite is therefore computed once
-// more here, from the pairs that are seen alone.  Data without infinities
-// and NaN never come here, and the tiles pay one test per output row.
+// more here, from the pairs that are seen alone, if a row that a masked pair
+// of its tiles brought in is not finite (any_odd): a few dozen rows at the
+// edges of the window, so infinities and NaN that are seen cost no more than
+// that look.  Finite data never come here; the tiles pay one test per
+// output.  A row all of whose elements have become NaN is not followed to
+// its end.
 #pragma once
 
 #include "tile.h"
@@ -27,6 +31,30 @@ __device__ inline float wave_sum(float x)
     for (int d = 32; d > 0; d >>= 1)
         x += __shfl_xor(x, d);
     return x;
+}
+
+// Whether one of rows from .. to - 1 (row(j): where it starts) has an element
+// that is not finite.
+template <class T, class Row>
+__device__ inline bool any_odd(Row row, int from, int to, int D, int lane)
+{
+    bool odd = false;
+    for (int j = from + lane; j < to; j += 64) {
+        const T *p = row(j);
+        for (int d = 0; d < D; d += 8) {
+            const Frag<T> x = load8(p + d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                odd = odd || !finite((float)x[e]);
+        }
+    }
+    return __any(odd);
+}
+
+// Whether every lane's share of a row has become NaN.
+__device__ inline bool all_nan(float a0, float a1, int D, int lane)
+{
+    return __all((lane >= D || a0 != a0) && (lane + 64 >= D || a1 != a1));
 }
 
 template <class T>
@@ -63,11 +91,12 @@ __device__ inline void put_row(T *row, float a0, float a1, int D, int lane)
 
 // o and lse of one query over keys 0 .. a - 1 and b .. c - 1 (a <= b) that
 // seen(j) lets through; key(j) and val(j) are their rows.  c2 = scale *
-// log2(e).  No key at all: 0 and -inf.
+// log2(e).  No key at all: 0 and -infinity.  have_lse: *lse is right already.
 template <class T, class Key, class Val, class SeenAt>
 __device__ inline void exact_row(const T *q, Key key, Val val, SeenAt seen, int a, int b, int c,
-                                 int D, float c2, T *o, float *lse, int lane)
+                                 int D, float c2, T *o, float *lse, bool have_lse, int lane)
 {
+    const float nan = __builtin_nanf("");
     float top = SDL_NEG_INF, total = 0.0f, a0 = 0.0f, a1 = 0.0f;
     bool any = false;
     for (int pass = 0; pass < 2; ++pass) {
@@ -78,20 +107,36 @@ __device__ inline void exact_row(const T *q, Key key, Val val, SeenAt seen, int 
             const bool in = j < c && (j < a || j >= b) && seen(j);
             const float x = in ? dot_row(q, key(j), D) * c2 : SDL_NEG_INF;
             if (pass == 0) {
+                if (__any(x != x)) {           // a score that is no number: nor is the softmax
+                    put_row(o, nan, nan, D, lane);
+                    if (lane == 0)
+                        *lse = nan;
+                    return;
+                }
                 top = fmaxf(top, x);
                 any = any || __any(in);
                 continue;
             }
-            const float base = top == SDL_NEG_INF ? 0.0f : top;
-            const float p = in ? __builtin_amdgcn_exp2f(x - base) : 0.0f;
+            const float p = in ? __builtin_amdgcn_exp2f(x - (top == SDL_NEG_INF ? 0.0f : top)) : 0.0f;
             total += p;
             for (uint64_t left = __ballot(in); left != 0; left &= left - 1) {
                 const int n = __ffsll((unsigned long long)left) - 1;
                 add_row(val(j0 + n), __shfl(p, n), D, lane, a0, a1);
             }
+            if (have_lse && all_nan(a0, a1, D, lane)) {
+                put_row(o, nan, nan, D, lane);
+                return;
+            }
         }
-        if (pass == 0)
+        if (pass == 0) {
             top = wave_max(top);
+            if (top == __builtin_inff()) {     // an infinite score: infinity over infinity
+                put_row(o, nan, nan, D, lane);
+                if (lane == 0)
+                    *lse = top;
+                return;
+            }
+        }
     }
     total = wave_sum(total);
     const float inv = 1.0f / total;
@@ -131,6 +176,8 @@ __device__ inline void exact_dq_row(const GradRows<T> &r, int i, float delta, Se
             const int n = __ffsll((unsigned long long)left) - 1;
             add_row(r.k + (int64_t)(j0 + n) * r.k_stride, __shfl(ds, n), D, lane, a0, a1);
         }
+        if (all_nan(a0, a1, D, lane))
+            break;
     }
     put_row(dq, a0 * scale, a1 * scale, D, lane);
 }
@@ -156,7 +203,27 @@ __device__ inline void exact_dkv_add(const GradRows<T> &r, int j, SeenAt seen, i
             add_row(r.q + (int64_t)(b + n) * r.q_stride, __shfl(ds, n), D, lane, dk[0], dk[1]);
             add_row(r.dout + (int64_t)(b + n) * r.dout_stride, __shfl(p, n), D, lane, dv[0], dv[1]);
         }
+        if (all_nan(dk[0], dk[1], D, lane) && all_nan(dv[0], dv[1], D, lane))
+            break;
     }
+}
+
+// Whether a key or value that the tiles of queries p0 .. p1 brought in behind
+// a mask is not finite.  Tiles of KT keys: those of the first `sinks` keys
+// (first_tiles of them) and from tile `band` on.
+template <class T, int KT, class Key, class Val>
+__device__ inline bool odd_masked_keys(const Seen &seen, Key key, Val val, int p0, int p1, int first_tiles,
+                                       int band, int lk, int D, int lane)
+{
+    auto odd = [&](int from, int to) {
+        to = to < lk ? to : lk;
+        return any_odd<T>(key, from, to, D, lane) || any_odd<T>(val, from, to, D, lane);
+    };
+    const int from = band * KT > seen.sinks ? band * KT : seen.sinks;
+    // past the queries, behind the window, behind the first keys (and the
+    // sequence's last key, which stands for those past its end)
+    return odd(p0 > 0 ? p0 : 0, (p1 / KT + 1) * KT) || odd(from, p1 - seen.window + 1) ||
+           odd(seen.sinks, first_tiles * KT) || odd(lk - 1, lk);
 }
 
 }  // namespace sdl

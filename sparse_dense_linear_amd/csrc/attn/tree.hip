@@ -96,6 +96,29 @@ __device__ inline int draft_place(int ctx, uint64_t mask)
     return ctx + (n > 1 ? n - 1 : 0);
 }
 
+// Row j of a pool, and whether a row that some draft does not see, but that
+// its tiles brought in, is not finite: keys at the lower end of the window,
+// and the drafts.
+template <class T>
+struct PoolRows {
+    const TreeArgs &a;
+    const int32_t *table;
+    const T *base;                    // at the key head
+    __device__ const T *operator()(int j) const
+    {
+        const int p = j / a.page;
+        return base + (int64_t)table[p] * a.page_stride + (int64_t)(j - p * a.page) * a.row_stride;
+    }
+};
+
+template <class T>
+__device__ bool odd_unseen(const Unit &u, const PoolRows<T> &k, const PoolRows<T> &v, int D, int lane)
+{
+    const int edge = u.low + u.drafts < u.ctx ? u.low + u.drafts : u.ctx;
+    return any_odd<T>(k, u.low, edge, D, lane) || any_odd<T>(v, u.low, edge, D, lane) ||
+           any_odd<T>(k, u.ctx, u.end, D, lane) || any_odd<T>(v, u.ctx, u.end, D, lane);
+}
+
 // The spans: `workers` of them (at most one for each tile), span w from
 // tile span_start(w) on.
 struct Spans {
@@ -408,29 +431,28 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
             }
             if (p == 0)
                 a.lse[hd * a.Tq + tk] = lse;
+            // 1: the output alone.  2: the sum too (no key was seen, or an
+            // infinite score, or one that is no number)
             if (!clean)
-                redo[lr] = 1;
+                atomicMax(&redo[lr], finite(lse) ? 1 : 2);
         }
         __syncthreads();
-        if (done)
+        if (done && __any(lane < RB && redo[lane]) | (RB > 64 && __any(redo[RB > 64 ? 64 + lane : 0]))) {
+            const PoolRows<T> key{a, table, kp}, val{a, table, vp};
+            const bool odd = odd_unseen<T>(u, key, val, a.D, lane);
             for (int lr = wave; lr < RB; lr += 4)
-                if (redo[lr]) {                // uniform over the wavefront
+                if (redo[lr] >= (odd ? 1 : 2)) {           // uniform over the wavefront
                     const int rr = block * RB + lr;
                     const int64_t tk = u.q_begin + rr / group;
                     const int hd = hk * group + rr % group;
                     DraftSeen one = seen;
                     one.mask = a.tree != nullptr ? draft_mask(a, u.q_begin, u.drafts, rr / group) : 0;
                     one.pos = a.tree != nullptr ? draft_place(u.ctx, one.mask) : u.ctx + rr / group;
-                    auto at_key = [&](const T *pool, int j) {
-                        const int p = j / a.page;
-                        return pool + (int64_t)table[p] * a.page_stride + (int64_t)(j - p * a.page) * a.row_stride;
-                    };
-                    exact_row<T>(
-                        (const T *)a.q + tk * a.q_row + hd * a.q_head,
-                        [&](int j) { return at_key(kp, j); }, [&](int j) { return at_key(vp, j); }, one,
-                        a.sinks < u.low ? a.sinks : u.low, u.low, u.end, a.D, c2,
-                        (T *)a.o + (tk * a.Hq + hd) * a.D, a.lse + hd * a.Tq + tk, lane);
+                    exact_row<T>((const T *)a.q + tk * a.q_row + hd * a.q_head, key, val, one,
+                                 a.sinks < u.low ? a.sinks : u.low, u.low, u.end, a.D, c2,
+                                 (T *)a.o + (tk * a.Hq + hd) * a.D, a.lse + hd * a.Tq + tk, redo[lr] == 1, lane);
                 }
+        }
         at += n1 - n0;
         ++piece_no;
     }
@@ -497,6 +519,15 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a)
             *lse_at = lse;
         return;
     }
+    const int32_t *table = a.table + (int64_t)seq * a.table_stride;
+    const PoolRows<T> key{a, table, (const T *)a.k_pages + hk * a.head_stride};
+    const PoolRows<T> val{a, table, (const T *)a.v_pages + hk * a.head_stride};
+    if (finite(lse) && !odd_unseen<T>(u, key, val, a.D, lane)) {
+        put_row(out, o0, o1, a.D, lane);
+        if (lane == 0)
+            *lse_at = lse;
+        return;
+    }
     // drafts' positions for the exact row: from their masks, one per lane
     __shared__ int places[4][64];
     int *place = places[threadIdx.x >> 6];
@@ -512,16 +543,11 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a)
     seen.mask = a.tree != nullptr ? draft_mask(a, u.q_begin, u.drafts, token) : 0;
     seen.pos = a.tree != nullptr ? draft_place(u.ctx, seen.mask) : u.ctx + token;
     seen.place = a.tree != nullptr ? place : nullptr;
-    const int32_t *table = a.table + (int64_t)seq * a.table_stride;
-    auto at_key = [&](const void *pool, int j) {
-        const int p = j / a.page;
-        return (const T *)pool + hk * a.head_stride + (int64_t)table[p] * a.page_stride +
-               (int64_t)(j - p * a.page) * a.row_stride;
-    };
-    exact_row<T>(
-        (const T *)a.q + tk * a.q_row + hd * a.q_head, [&](int j) { return at_key(a.k_pages, j); },
-        [&](int j) { return at_key(a.v_pages, j); }, seen, a.sinks < u.low ? a.sinks : u.low, u.low,
-        u.end, a.D, a.scale * kLog2e, out, lse_at, lane);
+    if (finite(lse) && lane == 0)
+        *lse_at = lse;
+    exact_row<T>((const T *)a.q + tk * a.q_row + hd * a.q_head, key, val, seen,
+                 a.sinks < u.low ? a.sinks : u.low, u.low, u.end, a.D, a.scale * kLog2e, out, lse_at,
+                 finite(lse), lane);
 }
 
 template <class T, int DP>

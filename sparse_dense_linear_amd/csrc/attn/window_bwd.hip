@@ -208,13 +208,21 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
                     store4(out + 32 * d + 8 * g + 4 * half, y[0], y[1], y[2], y[3]);
             }
     const uint64_t redo = __ballot(!clean && qi <= i1);
+    if (redo == 0)
+        return;
+    // (an infinity times the zeros past D is no number either)
+    if (a.D == DP &&
+        !odd_masked_keys<T, KT>(
+            seen, [&](int j) { return r.k + (int64_t)j * r.k_stride; },
+            [&](int j) { return r.v + (int64_t)j * r.v_stride; }, wp0, p1, first_tiles, band, lk, a.D, lane))
+        return;
     for (uint32_t left = (uint32_t)(redo | (redo >> 32)); left != 0; left &= left - 1) {
-        const int i = wi0 + __ffs(left) - 1, p = i + shift;
+        const int n = __ffs(left) - 1, i = wi0 + n, p = i + shift;
         const int lo = p - seen.window + 1 > 0 ? p - seen.window + 1 : 0;
         // delta of the row, stored above by this wavefront, is not read back:
         // the lane that holds it hands it out
         exact_dq_row<T>(
-            r, i, __shfl(delta, i - wi0), [&](int j) { return seen(p, j); },
+            r, i, __shfl(delta, n), [&](int j) { return seen(p, j); },
             seen.sinks < lo ? seen.sinks : lo, lo, p + 1, a.D, c2, a.scale,
             (T *)a.dq.base + (int64_t)(q_begin + i) * a.dq.row_stride + head * a.dq.head_stride, lane);
     }
@@ -245,6 +253,24 @@ __device__ inline StepRange window_steps(int j0, int j1, int window, int shift, 
 __device__ inline float *partial_at(const WindowArgs &a, int run, int hk, int key, int DP)
 {
     return a.partial + (((int64_t)run * a.Hkv + hk) * a.sinks + key) * 2 * DP;
+}
+
+// Whether one of queries from .. to - 1, of any head that shares key head hk,
+// has something that is not finite.
+template <class T>
+__device__ bool odd_queries(const WindowArgs &a, int q_begin, int k_begin, int hk, int from, int to, int lane)
+{
+    const int group = a.Hq / a.Hkv;
+    bool odd = false;
+    for (int g = 0; g < group && !odd; ++g) {
+        const GradRows<T> r = grad_rows<T>(a, q_begin, k_begin, hk * group + g, hk);
+        for (int i = from + lane; i < to; i += 64)
+            odd = odd || r.lse[i] != r.lse[i] || !finite(r.delta[i]);
+        odd = __any(odd) ||
+              any_odd<T>([&](int i) { return r.q + (int64_t)i * r.q_stride; }, from, to, a.D, lane) ||
+              any_odd<T>([&](int i) { return r.dout + (int64_t)i * r.dout_stride; }, from, to, a.D, lane);
+    }
+    return odd;
 }
 
 template <class T>
@@ -465,6 +491,17 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
                 }
     }
     const uint64_t redo = __ballot(!clean);
+    if (redo == 0)
+        return;
+    // queries of the steps that a key of this wavefront does not see: before
+    // the keys, and behind the window (a step's missing rows repeat the last)
+    const int before = wj1 - shift < lq ? wj1 - shift : lq;
+    int behind = wj0 + seen.window - shift < lq - 1 ? wj0 + seen.window - shift : lq - 1;
+    behind = behind > 0 ? behind : 0;
+    const int end = steps.to * QT < lq ? steps.to * QT : lq;
+    if (a.D == DP && !odd_queries<T>(a, q_begin, k_begin, hk, steps.from * QT, before, lane) &&
+        !odd_queries<T>(a, q_begin, k_begin, hk, behind, end, lane))
+        return;
     for (uint32_t left = (uint32_t)(redo | (redo >> 32)); left != 0; left &= left - 1)
         exact_dkv_row<T>(a, q_begin, k_begin, lq, lk, hk, wj0 + __ffs(left) - 1, lane);
 }
@@ -507,7 +544,9 @@ __global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slot
         if (lane + 64 * e < a.D)
             clean = clean && finite(sum[0][e]) && finite(sum[1][e]);
     }
-    if (!__all(clean)) {
+    // queries before the key are all that it does not see
+    const int before = j1 - (lk - lq) < lq ? j1 - (lk - lq) : lq;
+    if (!__all(clean) && (a.D != DP || odd_queries<T>(a, q_begin, k_begin, hk, 0, before, lane))) {
         exact_dkv_row<T>(a, q_begin, k_begin, lq, lk, hk, j, lane);
         return;
     }

@@ -210,18 +210,23 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_f
     if (qi <= i1 && half == 0)
         a.lse[(int64_t)head * a.Tq + q_begin + qi] = lse;
 
-    const uint64_t redo = __ballot(!clean && some && qi <= i1);
+    uint64_t redo = __ballot(!clean && some && qi <= i1);
+    if (redo == 0)
+        return;
+    auto key_row = [&](int j) { return K + (int64_t)j * a.k.row_stride; };
+    auto val_row = [&](int j) { return V + (int64_t)j * a.v.row_stride; };
+    // (a sum that is not finite says too little: an infinite score, a score
+    // that is no number, or an infinite key times the zeros past D)
+    if (!odd_masked_keys<T, KT>(seen, key_row, val_row, wp0, p1, first_tiles, band, lk, a.D, lane))
+        redo &= __ballot(!finite(lse));
     for (uint32_t left = (uint32_t)(redo | (redo >> 32)); left != 0; left &= left - 1) {
-        const int i = wi0 + __ffs(left) - 1, p = i + shift;
+        const int n = __ffs(left) - 1, i = wi0 + n, p = i + shift;
         const int lo = p - seen.window + 1 > 0 ? p - seen.window + 1 : 0;
-        const T *row = (const T *)a.q.base + (int64_t)(q_begin + i) * a.q.row_stride +
-                       head * a.q.head_stride;
         exact_row<T>(
-            row, [&](int j) { return K + (int64_t)j * a.k.row_stride; },
-            [&](int j) { return V + (int64_t)j * a.v.row_stride; },
-            [&](int j) { return seen(p, j); }, seen.sinks < lo ? seen.sinks : lo, lo, p + 1, a.D, c2,
+            (const T *)a.q.base + (int64_t)(q_begin + i) * a.q.row_stride + head * a.q.head_stride, key_row,
+            val_row, [&](int j) { return seen(p, j); }, seen.sinks < lo ? seen.sinks : lo, lo, p + 1, a.D, c2,
             (T *)a.o.base + (int64_t)(q_begin + i) * a.o.row_stride + head * a.o.head_stride,
-            a.lse + (int64_t)head * a.Tq + q_begin + i, lane);
+            a.lse + (int64_t)head * a.Tq + q_begin + i, finite(__shfl(lse, n)), lane);
     }
 }
 

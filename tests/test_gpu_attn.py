@@ -225,6 +225,44 @@ def test_seen_infinities_and_nan_go_where_arithmetic_sends_them(dtype):
     assert bool(torch.isfinite(o[:, :, :3]).all())
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [40, 64, 128])
+def test_infinite_keys(dtype, D):
+    """One element of a key is infinite: scores of the queries that see it are
+    -infinity (weight 0) or infinity (no number), by the sign of the query;
+    sizes of D that fill a tile and that do not."""
+    n, w, s = 150, 40, 2
+    for at in (60, 0):
+        q, k, v, do, qs, ks = operands([n], [n], 2, 1, D, dtype, seed=20)
+        k[at, 0, D - 1] = float("-inf")
+        want = window_ref(q, k, v, qs, ks, w, s)
+        o, lse = sdl.window_attention(q.cuda(), k.cuda(), v.cuda(), i32(qs), window=w, sinks=s)
+        assert_close(o, want["o"], want["o_tol"], "o")
+        assert_close(lse, want["lse"], want["lse_tol"], "lse")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [40, 128])
+def test_a_lost_training_step(dtype, D):
+    """Everything NaN, or one infinite value that every later query sees:
+    the gradients say so, in ordinary time."""
+    n = 3000
+    q, k, v, do, qs, ks = operands([n], [n], 4, 2, D, dtype, seed=21)
+    t = [x.cuda() for x in (q, k, v, do)]
+    nan = [torch.full_like(x, float("nan")) for x in t]
+    o, lse = sdl.window_attention(*nan[:3], i32(qs))
+    out = (o, lse) + sdl.window_attention_backward(nan[3], *nan[:3], o, lse, i32(qs))
+    assert all(bool(torch.isnan(x).all()) for x in out)
+    t[2][0, 0, 1] = float("inf")
+    o, lse = sdl.window_attention(*t[:3], i32(qs))
+    assert bool(torch.isposinf(o[:, :2, 1]).all())
+    assert bool(torch.isfinite(o[:, :2, 2:]).all()) and bool(torch.isfinite(o[:, 2:]).all())
+    assert bool(torch.isfinite(lse).all())
+    dq, dk, dv = sdl.window_attention_backward(t[3], *t[:3], o, lse, i32(qs))
+    assert not bool(torch.isfinite(dq[:, :2]).all(dim=2).any()) and bool(torch.isfinite(dq[:, 2:]).all())
+    assert bool(torch.isfinite(dv).all()) and bool(torch.isfinite(dk[:, 1]).all())
+
+
 def test_large_scores():
     """Scores far apart: weights of exactly 0 and 1, no overflow."""
     n = 100
