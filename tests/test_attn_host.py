@@ -16,6 +16,18 @@ INVALID, HIP, UNSUPPORTED = 1, 2, 4
 F32, BF16 = 0, 1
 
 
+class _Library:
+    """The library's functions, taking structures and numbers alike."""
+
+    def __getattr__(self, name):
+        f = getattr(_attn._lib(), name)
+        return lambda *a: f(*(ctypes.addressof(x) if isinstance(x, (ctypes.Structure, ctypes.c_int64)) else x
+                              for x in a))
+
+
+LIB = _Library()
+
+
 def header_functions():
     text = open(os.path.join(ROOT, "include", "attn.h")).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
@@ -51,14 +63,14 @@ def rows(heads=4, D=64, data=FAKE, **change):
 
 
 def fwd(w=None, dtype=F32, q=None, k=None, v=None, o=None, qp=FAKE, kp=FAKE, lse=FAKE):
-    return _attn._lib().window_attn_fwd(dtype, w or window(), q or rows(), k or rows(2), v or rows(2), qp, kp,
+    return LIB.window_attn_fwd(dtype, w or window(), q or rows(), k or rows(2), v or rows(2), qp, kp,
                                         o or rows(), lse, None)
 
 
 def bwd(w=None, dtype=F32, scratch=FAKE, size=1 << 30, lse=FAKE, **r):
     d = {n: rows() for n in ("dout", "q", "o", "dq")} | {n: rows(2) for n in ("k", "v", "dk", "dv")}
     d.update(r)
-    return _attn._lib().window_attn_bwd(dtype, w or window(), d["dout"], d["q"], d["k"], d["v"], d["o"], lse,
+    return LIB.window_attn_bwd(dtype, w or window(), d["dout"], d["q"], d["k"], d["v"], d["o"], lse,
                                         FAKE, FAKE, d["dq"], d["dk"], d["dv"], scratch, size, None)
 
 
@@ -78,7 +90,7 @@ def test_window_refuses_shapes(change, expect):
     assert bwd(window(**change)) == expect
     assert sdl.lib().spmm_last_error() != b""
     need = ctypes.c_int64(-1)
-    assert _attn._lib().window_attn_bwd_scratch(window(**change), ctypes.byref(need)) == expect
+    assert LIB.window_attn_bwd_scratch(window(**change), need) == expect
     assert need.value == -1
 
 
@@ -103,13 +115,13 @@ def test_window_refuses_the_rest():
     assert fwd(qp=None) == INVALID and fwd(kp=None) == INVALID and fwd(qp=FAKE + 2) == INVALID
     assert fwd(lse=None) == INVALID and fwd(lse=FAKE + 1) == INVALID and bwd(lse=None) == INVALID
     need = ctypes.c_int64()
-    assert _attn._lib().window_attn_bwd_scratch(window(), ctypes.byref(need)) == 0
+    assert LIB.window_attn_bwd_scratch(window(), need) == 0
     assert need.value > 0
     assert bwd(size=need.value - 1) == INVALID and bwd(scratch=None) == INVALID
     assert bwd(scratch=FAKE + 4) == INVALID
-    assert _attn._lib().window_attn_bwd_scratch(window(), None) == INVALID
-    assert _attn._lib().window_attn_fwd(F32, None, rows(), rows(), rows(), FAKE, FAKE, rows(), FAKE, None) == INVALID
-    assert _attn._lib().window_attn_fwd(F32, window(), None, rows(), rows(), FAKE, FAKE, rows(), FAKE,
+    assert LIB.window_attn_bwd_scratch(window(), None) == INVALID
+    assert LIB.window_attn_fwd(F32, None, rows(), rows(), rows(), FAKE, FAKE, rows(), FAKE, None) == INVALID
+    assert LIB.window_attn_fwd(F32, window(), None, rows(), rows(), FAKE, FAKE, rows(), FAKE,
                                         None) == INVALID
 
 
@@ -138,7 +150,7 @@ def tshape(**change):
 def tree(w=None, dtype=F32, q=None, scratch=FAKE, size=1 << 30, **p):
     a = dict(k=FAKE, v=FAKE, table=FAKE, ctx=FAKE, rp=FAKE, tree=None, o=FAKE, lse=FAKE)
     a.update(p)
-    return _attn._lib().tree_attn_paged(dtype, w or tshape(), q or rows(), a["k"], a["v"], a["table"], a["ctx"],
+    return LIB.tree_attn_paged(dtype, w or tshape(), q or rows(), a["k"], a["v"], a["table"], a["ctx"],
                                         a["rp"], a["tree"], a["o"], a["lse"], scratch, size, None)
 
 
@@ -151,7 +163,7 @@ def test_tree_refuses_shapes(change, expect):
     assert tree(tshape(**change)) == expect
     assert sdl.lib().spmm_last_error() != b""
     need = ctypes.c_int64(-1)
-    assert _attn._lib().tree_attn_scratch(F32, tshape(**change), ctypes.byref(need)) == expect
+    assert LIB.tree_attn_scratch(F32, tshape(**change), need) == expect
     assert need.value == -1
 
 
@@ -162,10 +174,10 @@ def test_tree_refuses_the_rest():
     assert tree(tree=FAKE + 4) == INVALID and tree(k=FAKE + 8) == INVALID and tree(dtype=7) == INVALID
     assert tree(q=rows(data=FAKE + 8)) == INVALID and tree(q=rows(row_stride=3)) == INVALID
     need = ctypes.c_int64()
-    assert _attn._lib().tree_attn_scratch(F32, tshape(), ctypes.byref(need)) == 0
+    assert LIB.tree_attn_scratch(F32, tshape(), need) == 0
     assert tree(size=need.value - 1) == INVALID and tree(scratch=None) == INVALID
     assert tree(scratch=FAKE + 8) == INVALID
-    assert _attn._lib().tree_attn_scratch(9, tshape(), ctypes.byref(need)) == INVALID
+    assert LIB.tree_attn_scratch(9, tshape(), need) == INVALID
 
 
 def pool(**change):
@@ -175,11 +187,11 @@ def pool(**change):
 
 
 def copy(p=None, src=FAKE, dst=FAKE, count=3):
-    return _attn._lib().pages_copy(p or pool(), src, dst, count, None)
+    return LIB.pages_copy(p or pool(), src, dst, count, None)
 
 
 def compact(p=None, table=FAKE, table_stride=4, ctx=FAKE, keep=FAKE, S=2, kept=3):
-    return _attn._lib().pages_compact(p or pool(), table, table_stride, ctx, keep, S, kept, None)
+    return LIB.pages_compact(p or pool(), table, table_stride, ctx, keep, S, kept, None)
 
 
 @pytest.mark.parametrize("change,expect", [
@@ -197,7 +209,7 @@ def test_pages_refuse_the_rest():
     assert compact(table=None) == INVALID and compact(ctx=None) == INVALID and compact(keep=FAKE + 2) == INVALID
     assert compact(S=-1) == INVALID and compact(kept=-1) == INVALID and compact(table_stride=-1) == INVALID
     assert compact(S=1 << 30) == INVALID and compact(kept=1 << 30) == INVALID
-    assert _attn._lib().pages_copy(None, FAKE, FAKE, 1, None) == INVALID
+    assert LIB.pages_copy(None, FAKE, FAKE, 1, None) == INVALID
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path")
