@@ -162,6 +162,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
     __shared__ int place[64];
     __shared__ float tops[4][32], totals[4][32];
     __shared__ int redo[RB];
+    __shared__ int64_t place_of[2][kTileKeys];     // of a tile's rows, in the pools
 
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
     const int group = a.Hq / a.Hkv;
@@ -278,34 +279,43 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
             O[d] = f32x16(0.0f);
         float top = SDL_NEG_INF, total = 0.0f;
 
-        // pages of a tile's rows, one tile ahead of the rows themselves
+        // Rows pass through registers: a tile's rows are under way while the
+        // tile before it is worked on, in both workgroups of a CU, which is
+        // what keeps HBM busy (LDS alone could not hold as much).  Where the
+        // rows lie is found two tiles ahead, once for each row.
         const int32_t *table = a.table + (int64_t)seq * a.table_stride;
         const T *kp = (const T *)a.k_pages + hk * a.head_stride, *vp = (const T *)a.v_pages + hk * a.head_stride;
-        int id[kPiecesPer], in_page[kPiecesPer];
         u32x4 pk[kPiecesPer], pv[kPiecesPer];
-        auto fetch_ids = [&](int n) {
-#pragma unroll
-            for (int i = 0; i < kPiecesPer; ++i) {
-                const int j = readable(a, u, n, first_key(u, n) + (t + i * kAttnThreads) / Tl::kPieces);
-                const int p = j / a.page;
-                in_page[i] = j - p * a.page;
-                id[i] = table[p];
-            }
+        int id = 0, in_page = 0;
+        auto find_row = [&](int n) {
+            const int j = readable(a, u, n, first_key(u, n) + t);
+            const int p = j / a.page;
+            in_page = j - p * a.page;
+            id = table[p];
         };
-        auto fetch_rows = [&]() {
+        auto keep_row = [&](int n) {
+            place_of[n & 1][t] = (int64_t)id * a.page_stride + (int64_t)in_page * a.row_stride;
+        };
+        auto fetch = [&](int n) {
 #pragma unroll
             for (int i = 0; i < kPiecesPer; ++i) {
-                const int p = (t + i * kAttnThreads) % Tl::kPieces;
+                const int m = t + i * kAttnThreads, p = m % Tl::kPieces;
                 const int d = p * Tl::kElems < a.D ? p * Tl::kElems : a.D - Tl::kElems;
-                const int64_t off = (int64_t)id[i] * a.page_stride + (int64_t)in_page[i] * a.row_stride + d;
+                const int64_t off = place_of[n & 1][m / Tl::kPieces] + d;
                 pk[i] = *(const u32x4 *)(kp + off);
                 pv[i] = *(const u32x4 *)(vp + off);
             }
         };
-        fetch_ids(n0);
-        fetch_rows();
-        if (n0 + 1 < n1)
-            fetch_ids(n0 + 1);
+        if (t < kTileKeys) {
+            find_row(n0);
+            keep_row(n0);
+            if (n0 + 1 < n1) {
+                find_row(n0 + 1);
+                keep_row(n0 + 1);
+            }
+        }
+        __syncthreads();
+        fetch(n0);
         for (int n = n0; n < n1; ++n) {
             char *kt = lds, *vt = lds + Tl::kBytes;
 #pragma unroll
@@ -314,56 +324,55 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
                 *(u32x4 *)(kt + Tl::at(m / Tl::kPieces, m % Tl::kPieces)) = pk[i];
                 *(u32x4 *)(vt + Tl::at(m / Tl::kPieces, m % Tl::kPieces)) = pv[i];
             }
+            const bool find = t < kTileKeys && n + 2 < n1;
+            if (find)
+                find_row(n + 2);
             __syncthreads();
-            if (n + 1 < n1) {
-                fetch_rows();
-                if (n + 2 < n1)
-                    fetch_ids(n + 2);
-            }
+            if (n + 1 < n1)
+                fetch(n + 1);
 #pragma unroll 1
             for (int b = ks; b < kTileKeys / 32; b += KS) {
                 const int j0 = first_key(u, n) + 32 * b;
-                if (j0 >= u.end || (j0 + 31 < u.low && j0 >= a.sinks))
+                if (j0 >= u.end || (j0 + 31 < u.low && j0 >= a.sinks) || block * RB + 32 * rg >= rows)
                     continue;
-                const int rows_at = renewed(Tl::row_base(lane)), cols_at = renewed(Tl::col_base(lane));
+                const int rows_at = renewed(Tl::row_base(lane) + 32 * b * Tl::kRowBytes);
+                const int cols_at = renewed(Tl::col_base(lane) + 32 * b * Tl::kRowBytes);
                 f32x16 x = f32x16(0.0f);
+                chain<STEPS, 4>([&](int i) { return Tl::row_frag(kt, rows_at, 0, i); },
+                                [&](int i, Frag<T> f) { x = mma(f, qf[i], x); });
+                if (!(j0 + 31 < u.ctx && (u.end - 1 - j0 < a.window || j0 + 31 < a.sinks))) {
+                    const int j = renewed(j0 + 4 * half);
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s)
-                    x = mma(Tl::row_frag(kt, rows_at, b, s), qf[s], x);
-                const bool whole = j0 + 31 < u.ctx && (u.end - 1 - j0 < a.window || j0 + 31 < a.sinks);
-                float most = SDL_NEG_INF;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float y = x[i] * c2;
-                    if (!whole && !seen(j0 + 8 * (i >> 2) + 4 * half + (i & 3)))
-                        y = SDL_NEG_INF;
-                    x[i] = y;
-                    most = fmaxf(most, y);
+                    for (int i = 0; i < 16; ++i)
+                        if (!seen(j + 8 * (i >> 2) + (i & 3)))
+                            x[i] = SDL_NEG_INF;
                 }
-                const float now = fmaxf(top, max_halves(most));
-                const float ref = now == SDL_NEG_INF ? 0.0f : now;
-                const float keep = __builtin_amdgcn_exp2f(top - ref);
-                top = now;
+                const float most = max_halves(max_of(x)) * c2;
+                if (__any(most > top + kLazy)) {
+                    const float now = fmaxf(top, most);
+                    const float keep = now == SDL_NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+                    top = now;
+                    total *= keep;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            O[d][i] *= keep;
+                }
+                const float ref = top == SDL_NEG_INF ? 0.0f : top;
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    x[i] = __builtin_amdgcn_exp2f(x[i] - ref);
+                    x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c2, -ref));
                     sum += x[i];
                 }
-                total = total * keep + sum;
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        O[d][i] *= keep;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const Frag<T> pf = result_frag<T>(x, s);
-#pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        O[d] = mma(Tl::col_frag(vt, cols_at, 2 * b + s, d), pf, O[d]);
-                }
+                total += sum;
+                const Frag<T> pf[2] = {result_frag<T>(x, 0), result_frag<T>(x, 1)};
+                chain<2 * DB, 4>([&](int i) { return Tl::col_frag(vt, cols_at, i / DB, i % DB); },
+                                 [&](int i, Frag<T> f) { O[i % DB] = mma(f, pf[i / DB], O[i % DB]); });
             }
+            if (find)
+                keep_row(n + 2);
             __syncthreads();
         }
 
@@ -373,12 +382,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
             tops[wave][lane] = top;
             totals[wave][lane] = total;
         }
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                store4((float *)(lds + wave * Out::kBytes + Out::at(lane & 31, 8 * d + 2 * g + half)),
-                       O[d][4 * g], O[d][4 * g + 1], O[d][4 * g + 2], O[d][4 * g + 3]);
+        Parked<DP>::put(lds + wave * Out::kBytes, lane, O);
         __syncthreads();
         const bool done = n0 == 0 && n1 == u.tiles;
         const int64_t slot = 2 * (int64_t)w + (piece_no == 0 ? 0 : 1);
