@@ -377,7 +377,7 @@ spmm_status_t tree_attn_paged(int32_t dtype, const attn_tree_t *shape, const att
     a.scale = shape->scale;
     a.partial = (float *)scratch;
     a.workers = sh.workers;
-    a.row_groups = sh.row_groups;
+    a.block_rows = sh.block_rows;
     return launched(launch_tree(dtype, a, (hipStream_t)stream), "tree attention");
 }
 

@@ -65,12 +65,12 @@ struct TreeArgs {
     int32_t window, sinks;
     float scale;
     float *partial;
-    int32_t workers, row_groups;   // launch shape (tree_shape)
+    int32_t workers, block_rows;   // launch shape (tree_shape)
 };
 
-// Workgroups of the split, 32-row groups of a workgroup, and the workspace.
+// Workgroups of the split, queries of a workgroup, and the workspace.
 struct TreeShape {
-    int32_t workers, row_groups;
+    int32_t workers, block_rows;
     int64_t bytes;
 };
 TreeShape tree_shape(int dtype, int64_t S, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D);

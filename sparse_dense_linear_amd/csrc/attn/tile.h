@@ -20,6 +20,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace sdl {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -75,6 +77,36 @@ __device__ inline Frag<T> zero_frag()
     return f;
 }
 
+// The 16 x 16 shape, for few columns: lane l holds row or column l % 16 and
+// terms 8 * (l / 16) .. + 7 of 32 (4 * (l / 16) .. + 3 of 16 for the shorter
+// step), and of the result column l % 16, rows 4 * (l / 16) + register.
+// Again a result is, as it lies, the second operand of the shorter step.
+__device__ inline f32x4 mma16(bf16x8 a, bf16x8 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ inline f32x4 mma16(f32x8 a, f32x8 b, f32x4 c)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+
+__device__ inline f32x4 mma16_short(s16x4 a, s16x4 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c, 0, 0, 0);
+}
+
+__device__ inline f32x4 mma16_short(f32x4 a, f32x4 b, f32x4 c)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+
 // x of this lane and of the lane 32 away.
 __device__ inline float max_halves(float x)
 {
@@ -86,6 +118,19 @@ __device__ inline float sum_halves(float x)
 {
     auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// x of the four lanes of a column of the 16 x 16 shape.
+__device__ inline float max_quarters(float x)
+{
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return max_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+
+__device__ inline float sum_quarters(float x)
+{
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
 __device__ inline float max_of(const f32x16 &x)
@@ -304,6 +349,95 @@ struct Stager {
             }
         }
     }
+};
+
+// One wavefront's share of attention with C = 32 or 16 queries as columns:
+// the shapes, fragments and reductions that depend on C.  A block of keys is
+// C keys; `part` is the lane's share of the terms, lane / C.
+template <class T, int DP, int ROWS, int C> struct Cols;
+
+template <class T, int DP, int ROWS>
+struct Cols<T, DP, ROWS, 32> {
+    typedef Tile<T, DP, ROWS> Tl;
+    typedef f32x16 Acc;
+    static constexpr int kAcc = 16, kSteps = DP / 16, kTerms = 16, kBlocks = DP / 32, kGroups = 2;
+    __device__ static int key_of(int r) { return 8 * (r >> 2) + (r & 3); }    // + 4 * part
+    __device__ static int row_base(int lane) { return Tl::row_base(lane); }
+    __device__ static int col_base(int lane) { return Tl::col_base(lane); }
+    __device__ static Frag<T> key_frag(const char *tile, int base, int step)
+    {
+        return Tl::row_frag(tile, base, 0, step);
+    }
+    __device__ static Acc mul(Frag<T> a, Frag<T> b, Acc c) { return mma(a, b, c); }
+    __device__ static float most(const Acc &x) { return max_halves(max_of(x)); }
+    __device__ static float sum(float x) { return sum_halves(x); }
+    typedef Frag<T> Weights;
+    __device__ static Weights weights(const Acc &x, int group) { return result_frag<T>(x, group); }
+    __device__ static Weights val_frag(const char *tile, int base, int group, int block)
+    {
+        return Tl::col_frag(tile, base, group, block);
+    }
+    __device__ static Acc apply(Weights v, Weights p, Acc o) { return mma(v, p, o); }
+};
+
+template <class T, int DP, int ROWS>
+struct Cols<T, DP, ROWS, 16> {
+    typedef Tile<T, DP, ROWS> Tl;
+    typedef f32x4 Acc;
+    static constexpr int kAcc = 4, kSteps = DP / 32, kTerms = 32, kBlocks = DP / 16, kGroups = 1;
+    __device__ static int key_of(int r) { return r; }                          // + 4 * part
+    __device__ static int row_base(int lane)
+    {
+        return Tl::at(lane & 15, (sizeof(T) == 2 ? 1 : 2) * (lane >> 4));
+    }
+    __device__ static int col_base(int lane)
+    {
+        const int i = lane & 15, part = lane >> 4;
+        if constexpr (sizeof(T) == 2)
+            return Tl::at(4 * part + (i >> 2), (i & 3) >> 1) + 8 * (i & 1);
+        else
+            return Tl::at(4 * part, i >> 2) + 4 * (i & 3);
+    }
+    __device__ static Frag<T> key_frag(const char *tile, int base, int step)
+    {
+        if constexpr (sizeof(T) == 2) {
+            return *(const bf16x8 *)(tile + (base ^ (step << 6)));
+        } else {
+            const f32x4 a = *(const f32x4 *)(tile + (base ^ (step << 7)));
+            const f32x4 b = *(const f32x4 *)(tile + (base ^ (step << 7 | 16)));
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    }
+    __device__ static Acc mul(Frag<T> a, Frag<T> b, Acc c) { return mma16(a, b, c); }
+    __device__ static float most(const Acc &x)
+    {
+        return max_quarters(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+    }
+    __device__ static float sum(float x) { return sum_quarters(x); }
+    typedef std::conditional_t<sizeof(T) == 2, s16x4, f32x4> Weights;
+    __device__ static Weights weights(const Acc &x, int)
+    {
+        if constexpr (sizeof(T) == 2) {
+            const bf16x4 p = {(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+            return __builtin_bit_cast(s16x4, p);
+        } else {
+            return x;
+        }
+    }
+    __device__ static Weights val_frag(const char *tile, int base, int, int block)
+    {
+        if constexpr (sizeof(T) == 2) {
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(tile + (base ^ (block << 5))));
+        } else {
+            f32x4 f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                f[e] = *(const float *)(tile + e * Tl::kRowBytes + (base ^ Tl::exchanged(e) ^ (block << 6)));
+            return f;
+        }
+    }
+    __device__ static Acc apply(Weights v, Weights p, Acc o) { return mma16_short(v, p, o); }
 };
 
 // A wavefront's 32 columns of DP results to LDS and back, for the wavefronts

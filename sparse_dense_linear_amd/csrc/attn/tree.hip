@@ -24,7 +24,10 @@ namespace sdl {
 
 namespace {
 
-constexpr int kTileKeys = 128;
+
+// Keys of a tile: with 16 queries to a block, four workgroups share a CU and
+// each has half a tile.
+__host__ __device__ constexpr int tile_keys(int block_rows) { return block_rows == 16 ? 64 : 128; }
 
 // What sequence s asks for.
 struct Unit {
@@ -32,9 +35,10 @@ struct Unit {
     int low;                         // first key of the window (any draft's)
     int first_tiles, band, tiles;    // key tiles [0, first_tiles) and [band, ..)
     int blocks;                      // blocks of queries
+    int tile_keys;
 };
 
-__device__ inline Unit unit_of(const TreeArgs &a, int s, int block_rows)
+__device__ inline Unit unit_of(const TreeArgs &a, int s)
 {
     Unit u;
     u.q_begin = a.q_rowptr[s];
@@ -42,17 +46,18 @@ __device__ inline Unit unit_of(const TreeArgs &a, int s, int block_rows)
     u.ctx = a.ctx[s];
     u.end = u.ctx + u.drafts;
     u.low = u.ctx - a.window + 1 > 0 ? u.ctx - a.window + 1 : 0;
-    u.band = u.low / kTileKeys;
-    u.first_tiles = (a.sinks + kTileKeys - 1) / kTileKeys;
+    u.tile_keys = tile_keys(a.block_rows);
+    u.band = u.low / u.tile_keys;
+    u.first_tiles = (a.sinks + u.tile_keys - 1) / u.tile_keys;
     u.first_tiles = u.first_tiles < u.band ? u.first_tiles : u.band;
-    u.tiles = u.first_tiles + (u.end + kTileKeys - 1) / kTileKeys - u.band;
-    u.blocks = (u.drafts * (a.Hq / a.Hkv) + block_rows - 1) / block_rows;
+    u.tiles = u.first_tiles + (u.end + u.tile_keys - 1) / u.tile_keys - u.band;
+    u.blocks = (u.drafts * (a.Hq / a.Hkv) + a.block_rows - 1) / a.block_rows;
     return u;
 }
 
 __device__ inline int first_key(const Unit &u, int n)
 {
-    return (n < u.first_tiles ? n : u.band + n - u.first_tiles) * kTileKeys;
+    return (n < u.first_tiles ? n : u.band + n - u.first_tiles) * u.tile_keys;
 }
 
 // A key of tile n that may be read: tiles reach over keys that no draft
@@ -137,38 +142,52 @@ struct Spans {
 struct Slots {
     int64_t *base;
     float *stat, *out;
-    __device__ Slots(const TreeArgs &a, int block_rows)
+    __device__ explicit Slots(const TreeArgs &a)
     {
         base = (int64_t *)a.partial;
         stat = a.partial + 2 * (((int64_t)a.S + 1 + 31) / 32 * 32);
-        out = stat + (int64_t)2 * a.workers * block_rows * 2;
+        out = stat + (int64_t)2 * a.workers * a.block_rows * 2;
     }
 };
 
-template <class T, int DP, int RG>
-__global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) void tree_attn(TreeArgs a)
+// Workgroups to a CU that registers and LDS allow.
+template <class T, int DP, int C>
+constexpr int per_cu()
+{
+    constexpr int tile = 2 * tile_keys(C) * DP * (int)sizeof(T);
+    return tile <= 16384 ? 4 : (tile <= 32768 && C == 16 ? 3 : (tile <= 65536 ? 2 : 1));
+}
+
+// RG groups of C queries; the 4 / RG wavefronts of a group share the keys of
+// a tile.
+template <class T, int DP, int C, int RG>
+__global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP, C>())) void tree_attn(TreeArgs a)
 {
     constexpr int KS = 4 / RG;                 // wavefronts that share a query group's keys
-    constexpr int RB = 32 * RG;                // queries of a block
-    constexpr int STEPS = DP / 16, DB = DP / 32;
+    constexpr int RB = C * RG;                 // queries of a block
+    constexpr int kTileKeys = tile_keys(RB);
+    typedef Cols<T, DP, kTileKeys, C> Co;
+    typedef typename Co::Acc Acc;
+    constexpr int STEPS = Co::kSteps, DB = Co::kBlocks;
     typedef Tile<T, DP, kTileKeys> Tl;
-    typedef Tile<float, DP, 32> Out;
+    typedef Tile<float, DP, C> Out;
     constexpr int kPiecesPer = kTileKeys * Tl::kPieces / kAttnThreads;
     constexpr int kBytes = 2 * Tl::kBytes > 4 * Out::kBytes ? 2 * Tl::kBytes : 4 * Out::kBytes;
     __shared__ __align__(16) char lds[kBytes];
-    __shared__ int64_t scan[8];
+    __shared__ int64_t scan[4];
     __shared__ int found;
     __shared__ int64_t found_base;
     __shared__ int place[64];
-    __shared__ float tops[4][32], totals[4][32];
+    __shared__ float tops[4][C], totals[4][C];
     __shared__ int redo[RB];
     __shared__ int64_t place_of[2][kTileKeys];     // of a tile's rows, in the pools
 
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
+    const int t = threadIdx.x, lane = t & 63, part = lane / C;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int group = a.Hq / a.Hkv;
     const int rg = wave % RG, ks = wave / RG;
     const float c2 = a.scale * kLog2e;
-    const Slots slots(a, RB);
+    const Slots slots(a);
 
     // ---- this workgroup's span: total of all tiles, then the sequence that
     // holds the span's first one
@@ -177,7 +196,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
     for (int s0 = 0; s0 < a.S; s0 += kAttnThreads) {
         int64_t n = 0;
         if (s0 + t < a.S) {
-            const Unit u = unit_of(a, s0 + t, RB);
+            const Unit u = unit_of(a, s0 + t);
             n = (int64_t)a.Hkv * u.blocks * u.tiles;
         }
         for (int d = 32; d > 0; d >>= 1)
@@ -200,7 +219,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
     for (int s0 = 0; s0 < a.S; s0 += kAttnThreads) {
         int64_t n = 0;
         if (s0 + t < a.S) {
-            const Unit u = unit_of(a, s0 + t, RB);
+            const Unit u = unit_of(a, s0 + t);
             n = (int64_t)a.Hkv * u.blocks * u.tiles;
         }
         int64_t upto = n;                      // inclusive sum over the wavefront
@@ -235,12 +254,12 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
     // ---- the units of the span, one piece after another
     int64_t piece_no = 0;
     while (at < stop) {
-        Unit u = unit_of(a, seq, RB);
+        Unit u = unit_of(a, seq);
         int64_t mine = (int64_t)a.Hkv * u.blocks * u.tiles;
         while (at >= base + mine) {            // the next sequence that has tiles
             base += mine;
             ++seq;
-            u = unit_of(a, seq, RB);
+            u = unit_of(a, seq);
             mine = (int64_t)a.Hkv * u.blocks * u.tiles;
         }
         const int unit = (int)((at - base) / u.tiles);
@@ -257,7 +276,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
             redo[t] = 0;
 
         // this lane's query
-        const int r = block * RB + 32 * rg + (lane & 31);
+        const int r = block * RB + C * rg + lane % C;
         const int token = (r < rows ? r : rows - 1) / group, head = hk * group + (r < rows ? r : rows - 1) % group;
         DraftSeen seen;
         seen.ctx = u.ctx;
@@ -271,12 +290,12 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
         Frag<T> qf[STEPS];
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
-            qf[s] = 16 * s + 8 * half < a.D ? load8(q + 16 * s + 8 * half) : zero_frag<T>();
+            qf[s] = Co::kTerms * s + 8 * part < a.D ? load8(q + Co::kTerms * s + 8 * part) : zero_frag<T>();
 
-        f32x16 O[DB];
+        Acc O[DB];
 #pragma unroll
         for (int d = 0; d < DB; ++d)
-            O[d] = f32x16(0.0f);
+            O[d] = Acc(0.0f);
         float top = SDL_NEG_INF, total = 0.0f;
 
         // Rows pass through registers: a tile's rows are under way while the
@@ -331,23 +350,23 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
             if (n + 1 < n1)
                 fetch(n + 1);
 #pragma unroll 1
-            for (int b = ks; b < kTileKeys / 32; b += KS) {
-                const int j0 = first_key(u, n) + 32 * b;
-                if (j0 >= u.end || (j0 + 31 < u.low && j0 >= a.sinks) || block * RB + 32 * rg >= rows)
+            for (int b = ks; b < kTileKeys / C; b += KS) {
+                const int j0 = first_key(u, n) + C * b, j1 = j0 + C - 1;
+                if (j0 >= u.end || (j1 < u.low && j0 >= a.sinks) || block * RB + C * rg >= rows)
                     continue;
-                const int rows_at = renewed(Tl::row_base(lane) + 32 * b * Tl::kRowBytes);
-                const int cols_at = renewed(Tl::col_base(lane) + 32 * b * Tl::kRowBytes);
-                f32x16 x = f32x16(0.0f);
-                chain<STEPS, 4>([&](int i) { return Tl::row_frag(kt, rows_at, 0, i); },
-                                [&](int i, Frag<T> f) { x = mma(f, qf[i], x); });
-                if (!(j0 + 31 < u.ctx && (u.end - 1 - j0 < a.window || j0 + 31 < a.sinks))) {
-                    const int j = renewed(j0 + 4 * half);
+                const int rows_at = renewed(Co::row_base(lane) + C * b * Tl::kRowBytes);
+                const int cols_at = renewed(Co::col_base(lane) + C * b * Tl::kRowBytes);
+                Acc x = Acc(0.0f);
+                chain<STEPS, 4>([&](int i) { return Co::key_frag(kt, rows_at, i); },
+                                [&](int i, Frag<T> f) { x = Co::mul(f, qf[i], x); });
+                if (!(j1 < u.ctx && (u.end - 1 - j0 < a.window || j1 < a.sinks))) {
+                    const int j = renewed(j0 + 4 * part);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!seen(j + 8 * (i >> 2) + (i & 3)))
+                    for (int i = 0; i < Co::kAcc; ++i)
+                        if (!seen(j + Co::key_of(i)))
                             x[i] = SDL_NEG_INF;
                 }
-                const float most = max_halves(max_of(x)) * c2;
+                const float most = Co::most(x) * c2;
                 if (__any(most > top + kLazy)) {
                     const float now = fmaxf(top, most);
                     const float keep = now == SDL_NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(top - now);
@@ -356,20 +375,24 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
 #pragma unroll
                     for (int d = 0; d < DB; ++d)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
+                        for (int i = 0; i < Co::kAcc; ++i)
                             O[d][i] *= keep;
                 }
                 const float ref = top == SDL_NEG_INF ? 0.0f : top;
                 float sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < Co::kAcc; ++i) {
                     x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c2, -ref));
                     sum += x[i];
                 }
                 total += sum;
-                const Frag<T> pf[2] = {result_frag<T>(x, 0), result_frag<T>(x, 1)};
-                chain<2 * DB, 4>([&](int i) { return Tl::col_frag(vt, cols_at, i / DB, i % DB); },
-                                 [&](int i, Frag<T> f) { O[i % DB] = mma(f, pf[i / DB], O[i % DB]); });
+                typename Co::Weights pf[Co::kGroups];
+#pragma unroll
+                for (int i = 0; i < Co::kGroups; ++i)
+                    pf[i] = Co::weights(x, i);
+                chain<Co::kGroups * DB, 4>(
+                    [&](int i) { return Co::val_frag(vt, cols_at, i / DB, i % DB); },
+                    [&](int i, typename Co::Weights f) { O[i % DB] = Co::apply(f, pf[i / DB], O[i % DB]); });
             }
             if (find)
                 keep_row(n + 2);
@@ -377,12 +400,18 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
         }
 
         // ---- join the wavefronts of a query group, and write
-        total = sum_halves(total);
-        if (half == 0) {
+        total = Co::sum(total);
+        if (part == 0) {
             tops[wave][lane] = top;
             totals[wave][lane] = total;
         }
-        Parked<DP>::put(lds + wave * Out::kBytes, lane, O);
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int g = 0; g < Co::kAcc / 4; ++g)
+                store4((float *)(lds + wave * Out::kBytes +
+                                 Out::at(lane % C, (C * d + Co::key_of(4 * g)) / 4 + part)),
+                       O[d][4 * g], O[d][4 * g + 1], O[d][4 * g + 2], O[d][4 * g + 3]);
         __syncthreads();
         const bool done = n0 == 0 && n1 == u.tiles;
         const int64_t slot = 2 * (int64_t)w + (piece_no == 0 ? 0 : 1);
@@ -395,16 +424,16 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 || DP == 64 ? 2 : 1) v
             float best = SDL_NEG_INF;
 #pragma unroll
             for (int k = 0; k < KS; ++k)
-                best = fmaxf(best, tops[k * RG + lr / 32][lr & 31]);
+                best = fmaxf(best, tops[k * RG + lr / C][lr % C]);
             const float ref = best == SDL_NEG_INF ? 0.0f : best;
             float sum = 0.0f;
             f32x4 o = f32x4(0.0f);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                const int wv = k * RG + lr / 32;
-                const float f = __builtin_amdgcn_exp2f(tops[wv][lr & 31] - ref);
-                sum = fmaf(f, totals[wv][lr & 31], sum);
-                const f32x4 x = *(const f32x4 *)(lds + wv * Out::kBytes + Out::at(lr & 31, p));
+                const int wv = k * RG + lr / C;
+                const float f = __builtin_amdgcn_exp2f(tops[wv][lr % C] - ref);
+                sum = fmaf(f, totals[wv][lr % C], sum);
+                const f32x4 x = *(const f32x4 *)(lds + wv * Out::kBytes + Out::at(lr % C, p));
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     o[e] = fmaf(f, x[e], o[e]);
@@ -469,7 +498,7 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a)
 {
     const int lane = threadIdx.x & 63;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int RB = 32 * a.row_groups, group = a.Hq / a.Hkv;
+    const int RB = a.block_rows, group = a.Hq / a.Hkv;
     const int64_t tk = row / a.Hq;
     const int hd = (int)(row % a.Hq), hk = hd / group;
     if (tk >= a.q_rowptr[a.S] || tk < a.q_rowptr[0])
@@ -483,10 +512,10 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a)
             hi = mid;
     }
     const int seq = lo;
-    const Unit u = unit_of(a, seq, RB);
+    const Unit u = unit_of(a, seq);
     const int token = (int)(tk - u.q_begin);
     const int r = token * group + hd % group;
-    const Slots slots(a, RB);
+    const Slots slots(a);
     Spans spans;
     spans.tiles = slots.base[a.S];
     spans.workers = spans.tiles < a.workers ? (int)spans.tiles : a.workers;
@@ -557,12 +586,14 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a)
 template <class T, int DP>
 hipError_t launch(const TreeArgs &a, hipStream_t stream)
 {
-    if (a.row_groups == 1)
-        tree_attn<T, DP, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
-    else if (a.row_groups == 2)
-        tree_attn<T, DP, 2><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    if (a.block_rows == 16)
+        tree_attn<T, DP, 16, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    else if (a.block_rows == 32)
+        tree_attn<T, DP, 32, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    else if (a.block_rows == 64)
+        tree_attn<T, DP, 32, 2><<<a.workers, kAttnThreads, 0, stream>>>(a);
     else
-        tree_attn<T, DP, 4><<<a.workers, kAttnThreads, 0, stream>>>(a);
+        tree_attn<T, DP, 32, 4><<<a.workers, kAttnThreads, 0, stream>>>(a);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess)
         return err;
@@ -576,13 +607,18 @@ TreeShape tree_shape(int dtype, int64_t S, int64_t Tq, int64_t Hq, int64_t Hkv, 
 {
     TreeShape sh;
     const int DP = D <= 64 ? 64 : 128;
-    // two workgroups to a CU where their tiles fit its LDS side by side
-    sh.workers = dtype == SPMM_DTYPE_BF16 || DP == 64 ? 512 : 256;
-    // groups of 32 queries that the mean sequence fills
+    // as many queries to a block as the mean sequence fills
     const int64_t rows = S > 0 ? (Tq + S - 1) / S * (Hq / Hkv) : 0;
-    sh.row_groups = rows <= 32 ? 1 : (rows <= 64 ? 2 : 4);
-    const int64_t block_rows = 32 * sh.row_groups;
-    sh.bytes = 4 * (2 * ((S + 1 + 31) / 32 * 32) + 2 * sh.workers * block_rows * (2 + DP));
+    sh.block_rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
+    // as many workgroups as the 256 CUs hold at once
+    const int C = sh.block_rows == 16 ? 16 : 32;
+    if (dtype == SPMM_DTYPE_BF16)
+        sh.workers = 256 * (DP == 64 ? (C == 16 ? per_cu<__bf16, 64, 16>() : per_cu<__bf16, 64, 32>())
+                                     : (C == 16 ? per_cu<__bf16, 128, 16>() : per_cu<__bf16, 128, 32>()));
+    else
+        sh.workers = 256 * (DP == 64 ? (C == 16 ? per_cu<float, 64, 16>() : per_cu<float, 64, 32>())
+                                     : (C == 16 ? per_cu<float, 128, 16>() : per_cu<float, 128, 32>()));
+    sh.bytes = 4 * (2 * ((S + 1 + 31) / 32 * 32) + 2 * (int64_t)sh.workers * sh.block_rows * (2 + DP));
     return sh;
 }
 
