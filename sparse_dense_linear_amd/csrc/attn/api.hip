@@ -171,8 +171,8 @@ spmm_status_t check_tree(int32_t dtype, const attn_tree_t *w)
         return bad("strides must be in 0 .. 2^32");
     if (w->page_stride % unit != 0 || w->row_stride % unit != 0 || w->head_stride % unit != 0)
         return bad("strides must be multiples of 16 bytes");
-    if (w->Tq * w->Hq > kMaxGrid)
-        return unsupported("too many queries: Tq * Hq must be below 2^31");
+    if (w->Tq * w->Hq + w->S * w->Hkv > kMaxGrid)
+        return unsupported("too many queries: Tq * Hq + S * Hkv must be below 2^31");
     return SPMM_SUCCESS;
 }
 

@@ -129,11 +129,16 @@ __device__ bool odd_unseen(const Unit &u, const PoolRows<T> &k, const PoolRows<T
 struct Spans {
     int64_t tiles;
     int workers;
-    __device__ int64_t start(int w) const { return w * tiles / workers; }
+    __device__ int64_t start(int w) const { return divide(w * tiles, workers); }
     // the span that holds a tile
     __device__ int of(int64_t tile) const
     {
-        return (int)(((tile + 1) * workers + tiles - 1) / tiles) - 1;
+        return (int)divide((tile + 1) * workers + tiles - 1, tiles) - 1;
+    }
+    // of non-negative numbers; 64 bits cost some hundred instructions
+    __device__ static int64_t divide(int64_t x, int64_t y)
+    {
+        return (x | y) >> 32 == 0 ? (uint32_t)x / (uint32_t)y : x / y;
     }
 };
 
@@ -149,6 +154,69 @@ struct Slots {
         out = stat + (int64_t)2 * a.workers * a.block_rows * 2;
     }
 };
+
+// A finished row lr of a block: four elements of its output from the sum of
+// weights and the unnormalised values.  redo[lr]: 1, the output is to be
+// computed again if a row that is masked is not finite; 2, the sum too (no
+// key was seen, or a score is infinite or no number).
+template <class T>
+__device__ inline void finish(const TreeArgs &a, int64_t token, int head, int p, float best, float sum,
+                              const f32x4 &o, int *redo)
+{
+    const float lse = kLn2 * (best + __builtin_amdgcn_logf(sum));
+    const float inv = 1.0f / sum;
+    bool clean = finite(lse);
+    if (4 * p < a.D) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[e] = o[e] * inv;
+            clean = clean && finite(y[e]);
+        }
+        store4((T *)a.o + (token * a.Hq + head) * a.D + 4 * p, y[0], y[1], y[2], y[3]);
+    }
+    if (p == 0)
+        a.lse[head * a.Tq + token] = lse;
+    if (!clean)
+        atomicMax(redo, finite(lse) ? 1 : 2);
+}
+
+// What finish() left to do in rows first .. first + count - 1 of a sequence's
+// query rows, by the four wavefronts of a workgroup; place: the drafts'
+// positions.
+template <class T>
+__device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, int hk, int first, int count,
+                                    const int *redo, const int *place, int wave, int lane)
+{
+    const int group = a.Hq / a.Hkv;
+    bool some = false;
+    for (int lr = lane; lr < count; lr += 64)
+        some = some || redo[lr] != 0;
+    if (!__any(some))
+        return;
+    const int32_t *table = a.table + (int64_t)seq * a.table_stride;
+    const PoolRows<T> key{a, table, (const T *)a.k_pages + hk * a.head_stride};
+    const PoolRows<T> val{a, table, (const T *)a.v_pages + hk * a.head_stride};
+    const bool odd = odd_unseen<T>(u, key, val, a.D, lane);
+    for (int lr = wave; lr < count; lr += 4) {
+        const int why = redo[lr];
+        if (why < (odd ? 1 : 2))               // uniform over the wavefront
+            continue;
+        const int r = first + lr, t = r / group, head = hk * group + r % group;
+        const int64_t token = u.q_begin + t;
+        DraftSeen seen;
+        seen.ctx = u.ctx;
+        seen.drafts = u.drafts;
+        seen.window = a.window;
+        seen.sinks = a.sinks;
+        seen.mask = a.tree != nullptr ? draft_mask(a, u.q_begin, u.drafts, t) : 0;
+        seen.pos = a.tree != nullptr ? draft_place(u.ctx, seen.mask) : u.ctx + t;
+        seen.place = a.tree != nullptr ? place : nullptr;
+        exact_row<T>((const T *)a.q + token * a.q_row + head * a.q_head, key, val, seen,
+                     a.sinks < u.low ? a.sinks : u.low, u.low, u.end, a.D, a.scale * kLog2e,
+                     (T *)a.o + (token * a.Hq + head) * a.D, a.lse + head * a.Tq + token, why == 1, lane);
+    }
+}
 
 // Workgroups to a CU that registers and LDS allow.
 template <class T, int DP, int C>
@@ -262,9 +330,9 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP, C>())) void tree_attn(
             u = unit_of(a, seq);
             mine = (int64_t)a.Hkv * u.blocks * u.tiles;
         }
-        const int unit = (int)((at - base) / u.tiles);
+        const int unit = (int)Spans::divide(at - base, u.tiles);
         const int hk = unit / u.blocks, block = unit % u.blocks;
-        const int n0 = (int)((at - base) % u.tiles);
+        const int n0 = (int)(at - base - (int64_t)unit * u.tiles);
         const int n1 = stop - at < u.tiles - n0 ? n0 + (int)(stop - at) : u.tiles;
         const int rows = u.drafts * group;
 
@@ -447,140 +515,89 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP, C>())) void tree_attn(
                 }
                 continue;
             }
-            const int64_t tk = u.q_begin + rr / group;
-            const int hd = hk * group + rr % group;
-            const float lse = kLn2 * (best + __builtin_amdgcn_logf(sum));
-            // nothing seen: the maximum of no score at all
-            const float inv = 1.0f / sum;
-            bool clean = finite(lse);
-            if (4 * p < a.D) {
-                float y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    y[e] = o[e] * inv;
-                    clean = clean && finite(y[e]);
-                }
-                store4((T *)a.o + (tk * a.Hq + hd) * a.D + 4 * p, y[0], y[1], y[2], y[3]);
-            }
-            if (p == 0)
-                a.lse[hd * a.Tq + tk] = lse;
-            // 1: the output alone.  2: the sum too (no key was seen, or an
-            // infinite score, or one that is no number)
-            if (!clean)
-                atomicMax(&redo[lr], finite(lse) ? 1 : 2);
+            finish<T>(a, u.q_begin + rr / group, hk * group + rr % group, p, best, sum, o, redo + lr);
         }
         __syncthreads();
-        if (done && __any(lane < RB && redo[lane]) | (RB > 64 && __any(redo[RB > 64 ? 64 + lane : 0]))) {
-            const PoolRows<T> key{a, table, kp}, val{a, table, vp};
-            const bool odd = odd_unseen<T>(u, key, val, a.D, lane);
-            for (int lr = wave; lr < RB; lr += 4)
-                if (redo[lr] >= (odd ? 1 : 2)) {           // uniform over the wavefront
-                    const int rr = block * RB + lr;
-                    const int64_t tk = u.q_begin + rr / group;
-                    const int hd = hk * group + rr % group;
-                    DraftSeen one = seen;
-                    one.mask = a.tree != nullptr ? draft_mask(a, u.q_begin, u.drafts, rr / group) : 0;
-                    one.pos = a.tree != nullptr ? draft_place(u.ctx, one.mask) : u.ctx + rr / group;
-                    exact_row<T>((const T *)a.q + tk * a.q_row + hd * a.q_head, key, val, one,
-                                 a.sinks < u.low ? a.sinks : u.low, u.low, u.end, a.D, c2,
-                                 (T *)a.o + (tk * a.Hq + hd) * a.D, a.lse + hd * a.Tq + tk, redo[lr] == 1, lane);
-                }
-        }
+        if (done)
+            finish_again<T>(a, u, seq, hk, block * RB, RB, redo, place, wave, lane);
         at += n1 - n0;
         ++piece_no;
     }
 }
 
-// One wavefront for each query row: joins the slots of the spans that its
-// unit was cut over (units within one span are written already).
+constexpr int kJoinRows = 16;      // query rows of a joining workgroup
+
+// Joins the slots of the spans that a unit was cut over (units within one
+// span are written already), kJoinRows of its rows to a workgroup.  Units are numbered
+// without a list, as find_seq_tile does: the rows of sequence s, in blocks,
+// have the numbers from rowptr[s] * group / rows + s on.
 template <class T, int DP>
-__global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a)
+__global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int numbers)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    __shared__ int redo[kJoinRows], place[64];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int RB = a.block_rows, group = a.Hq / a.Hkv;
-    const int64_t tk = row / a.Hq;
-    const int hd = (int)(row % a.Hq), hk = hd / group;
-    if (tk >= a.q_rowptr[a.S] || tk < a.q_rowptr[0])
-        return;
-    int lo = 0, hi = a.S;                      // the last sequence that begins at or before tk
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.q_rowptr[mid] <= tk)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    const int seq = lo;
-    const Unit u = unit_of(a, seq);
-    const int token = (int)(tk - u.q_begin);
-    const int r = token * group + hd % group;
+    const int hk = blockIdx.x / numbers, number = blockIdx.x % numbers;
     const Slots slots(a);
+    const int64_t tiles = slots.base[a.S];
+    int seq = 0, left = a.S;                   // the last sequence whose first number is <= number
+    while (left > 1) {
+        const int step = (left + 63) / 64, s = seq + lane * step;
+        const bool at = lane * step < left && (int64_t)a.q_rowptr[s] * group / RB + s <= number;
+        const int n = __popcll(__ballot(at)) - 1;
+        if (n < 0)
+            return;
+        seq += n * step;
+        left = left - n * step < step ? left - n * step : step;
+    }
+    const Unit u = unit_of(a, seq);
+    const int block = number - (int)((int64_t)u.q_begin * group / RB + seq);
+    const int rows = u.drafts * group;
+    const int row0 = blockIdx.y * kJoinRows;
+    if (block < 0 || block >= u.blocks || block * RB + row0 >= rows)
+        return;
     Spans spans;
-    spans.tiles = slots.base[a.S];
-    spans.workers = spans.tiles < a.workers ? (int)spans.tiles : a.workers;
-    const int64_t from = slots.base[seq] + (int64_t)(hk * u.blocks + r / RB) * u.tiles;
+    spans.tiles = tiles;
+    spans.workers = tiles < a.workers ? (int)tiles : a.workers;
+    const int64_t from = slots.base[seq] + (int64_t)(hk * u.blocks + block) * u.tiles;
     const int w0 = spans.of(from), w1 = spans.of(from + u.tiles - 1);
     if (w0 == w1)
         return;
+    const int64_t slot0 = 2 * (int64_t)w0 + (spans.start(w0) >= from ? 0 : 1);
 
-    float best = SDL_NEG_INF;
-    for (int w = w0; w <= w1; ++w) {
-        const int64_t slot = 2 * (int64_t)w + (spans.start(w) >= from ? 0 : 1);
-        best = fmaxf(best, slots.stat[(slot * RB + r % RB) * 2]);
+    if (t < kJoinRows)
+        redo[t] = 0;
+    if (a.tree != nullptr && t < 64 && t < u.drafts)
+        place[t] = draft_place(u.ctx, draft_mask(a, u.q_begin, u.drafts, t));
+    __syncthreads();
+    constexpr int kOutPieces = DP / 4;
+    for (int m = t; m < kJoinRows * kOutPieces; m += kAttnThreads) {
+        const int lr = m / kOutPieces, p = m % kOutPieces;
+        const int r = block * RB + row0 + lr;
+        if (r >= rows)
+            break;
+        float best = SDL_NEG_INF, sum = 0.0f;
+        f32x4 o = f32x4(0.0f);
+        auto add = [&](int64_t slot) {
+            const int64_t row = slot * RB + row0 + lr;
+            const float top = slots.stat[2 * row], total = slots.stat[2 * row + 1];
+            const f32x4 x = *(const f32x4 *)(slots.out + row * DP + 4 * p);
+            const float now = fmaxf(best, top), ref = now == SDL_NEG_INF ? 0.0f : now;
+            const float mine = __builtin_amdgcn_exp2f(best - ref), theirs = __builtin_amdgcn_exp2f(top - ref);
+            best = now;
+            sum = fmaf(theirs, total, mine * sum);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = fmaf(theirs, x[e], mine * o[e]);
+        };
+        add(slot0);
+#pragma unroll 4
+        for (int w = w0 + 1; w <= w1; ++w)     // a unit that goes on is a span's first
+            add(2 * (int64_t)w);
+        finish<T>(a, u.q_begin + r / group, hk * group + r % group, p, best, sum, o, redo + lr);
     }
-    const float ref = best == SDL_NEG_INF ? 0.0f : best;
-    float sum = 0.0f, o0 = 0.0f, o1 = 0.0f;
-    for (int w = w0; w <= w1; ++w) {
-        const int64_t slot = 2 * (int64_t)w + (spans.start(w) >= from ? 0 : 1);
-        const float f = __builtin_amdgcn_exp2f(slots.stat[(slot * RB + r % RB) * 2] - ref);
-        sum = fmaf(f, slots.stat[(slot * RB + r % RB) * 2 + 1], sum);
-        const float *o = slots.out + (slot * RB + r % RB) * DP;
-        o0 = fmaf(f, o[lane], o0);
-        if (DP > 64)
-            o1 = fmaf(f, o[64 + lane], o1);
-    }
-    const float inv = 1.0f / sum;
-    o0 *= inv;
-    o1 *= inv;
-    const float lse = kLn2 * (best + __builtin_amdgcn_logf(sum));
-    T *out = (T *)a.o + (tk * a.Hq + hd) * a.D;
-    float *lse_at = a.lse + hd * a.Tq + tk;
-    if (__all(finite(lse) && (lane >= a.D || finite(o0)) && (lane + 64 >= a.D || finite(o1)))) {
-        put_row(out, o0, o1, a.D, lane);
-        if (lane == 0)
-            *lse_at = lse;
-        return;
-    }
-    const int32_t *table = a.table + (int64_t)seq * a.table_stride;
-    const PoolRows<T> key{a, table, (const T *)a.k_pages + hk * a.head_stride};
-    const PoolRows<T> val{a, table, (const T *)a.v_pages + hk * a.head_stride};
-    if (finite(lse) && !odd_unseen<T>(u, key, val, a.D, lane)) {
-        put_row(out, o0, o1, a.D, lane);
-        if (lane == 0)
-            *lse_at = lse;
-        return;
-    }
-    // drafts' positions for the exact row: from their masks, one per lane
-    __shared__ int places[4][64];
-    int *place = places[threadIdx.x >> 6];
-    if (a.tree != nullptr && lane < u.drafts)
-        place[lane] = draft_place(u.ctx, draft_mask(a, u.q_begin, u.drafts, lane));
-    __threadfence_block();
-    __builtin_amdgcn_wave_barrier();
-    DraftSeen seen;
-    seen.ctx = u.ctx;
-    seen.drafts = u.drafts;
-    seen.window = a.window;
-    seen.sinks = a.sinks;
-    seen.mask = a.tree != nullptr ? draft_mask(a, u.q_begin, u.drafts, token) : 0;
-    seen.pos = a.tree != nullptr ? draft_place(u.ctx, seen.mask) : u.ctx + token;
-    seen.place = a.tree != nullptr ? place : nullptr;
-    if (finite(lse) && lane == 0)
-        *lse_at = lse;
-    exact_row<T>((const T *)a.q + tk * a.q_row + hd * a.q_head, key, val, seen,
-                 a.sinks < u.low ? a.sinks : u.low, u.low, u.end, a.D, a.scale * kLog2e, out, lse_at,
-                 finite(lse), lane);
+    __syncthreads();
+    finish_again<T>(a, u, seq, hk, block * RB + row0, kJoinRows, redo, place, wave, lane);
 }
 
 template <class T, int DP>
@@ -597,7 +614,9 @@ hipError_t launch(const TreeArgs &a, hipStream_t stream)
     hipError_t err = hipGetLastError();
     if (err != hipSuccess)
         return err;
-    tree_join<T, DP><<<dim3((uint32_t)((a.Tq * a.Hq + 3) / 4)), kAttnThreads, 0, stream>>>(a);
+    const int64_t numbers = a.Tq * (a.Hq / a.Hkv) / a.block_rows + a.S;
+    tree_join<T, DP><<<dim3((uint32_t)(numbers * a.Hkv), a.block_rows / kJoinRows), kAttnThreads, 0, stream>>>(
+        a, (int)numbers);
     return hipGetLastError();
 }
 
