@@ -218,6 +218,16 @@ __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, i
     }
 }
 
+// Sequences whose queries fill no more than one block read their keys once:
+// keeping them in the caches would only push out what is read again.  (64
+// answers: 231 us against 255; trees of drafts, several blocks each, 83
+// against 76 the other way round.)
+template <bool ONCE>
+__device__ inline u32x4 load_once(const u32x4 *p)
+{
+    return ONCE ? __builtin_nontemporal_load(p) : *p;
+}
+
 // Workgroups to a CU that registers and LDS allow.
 template <class T, int DP, int C>
 constexpr int per_cu()
@@ -389,8 +399,8 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP, C>())) void tree_attn(
                 const int m = t + i * kAttnThreads, p = m % Tl::kPieces;
                 const int d = p * Tl::kElems < a.D ? p * Tl::kElems : a.D - Tl::kElems;
                 const int64_t off = place_of[n & 1][m / Tl::kPieces] + d;
-                pk[i] = *(const u32x4 *)(kp + off);
-                pv[i] = *(const u32x4 *)(vp + off);
+                pk[i] = load_once<C == 16>((const u32x4 *)(kp + off));
+                pv[i] = load_once<C == 16>((const u32x4 *)(vp + off));
             }
         };
         if (t < kTileKeys) {
@@ -414,9 +424,9 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP, C>())) void tree_attn(
             const bool find = t < kTileKeys && n + 2 < n1;
             if (find)
                 find_row(n + 2);
-            __syncthreads();
             if (n + 1 < n1)
                 fetch(n + 1);
+            __syncthreads();
 #pragma unroll 1
             for (int b = ks; b < kTileKeys / C; b += KS) {
                 const int j0 = first_key(u, n) + C * b, j1 = j0 + C - 1;

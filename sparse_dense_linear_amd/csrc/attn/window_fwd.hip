@@ -24,10 +24,16 @@ namespace {
 
 // RG groups of 32 queries; the 4 / RG wavefronts of a group share the keys
 // of each tile and join their results at the end.
+//
+// What bounds it is the issue of instructions: matrix instructions take about
+// as long as the softmax between them, and overlap only between wavefronts
+// of a SIMD.  In bf16, 128 queries to a workgroup, tiles of 32 keys leave
+// room for a third workgroup on a CU (16384 tokens, 32 heads of 128 on 8,
+// window 1024: 300 us, against 326 with tiles of 64 and two).
 template <class T, int DP, int RG>
-__global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_fwd(WindowArgs a, int slots)
+__global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? (RG == 4 ? 3 : 2) : 1) void window_fwd(WindowArgs a, int slots)
 {
-    constexpr int KT = 64;                       // keys of a tile
+    constexpr int KT = RG == 4 && sizeof(T) == 2 ? 32 : 64;   // keys of a tile
     constexpr int KS = 4 / RG;                   // wavefronts of a group
     constexpr int NB = KT / 32 / KS;             // 32-key blocks of a wavefront
     constexpr int STEPS = DP / 16, DB = DP / 32;
