@@ -46,25 +46,32 @@ __global__ __launch_bounds__(kAttnThreads) void copy_kernel(PagesArgs a, int par
 // column through all kept rows, so rows never wait for other threads.
 __global__ __launch_bounds__(kAttnThreads) void compact_kernel(PagesArgs a)
 {
+    // (32-bit division where the numbers allow it: the 64-bit one costs more
+    // than the rest of the kernel)
+    auto divide = [](int64_t x, int64_t y) {
+        return ((uint64_t)x | (uint64_t)y) >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+    };
     const int64_t cols = a.row_bytes / 16;
     const int64_t n = (int64_t)blockIdx.x * kAttnThreads + threadIdx.x;
-    const int64_t col = n % cols, item = n / cols;
-    const int64_t seq = item % a.count, layer = item / a.count % a.layers;
-    if (item >= 2 * a.layers * a.count)
+    const int64_t item = divide(n, cols), col = n - item * cols;
+    const int64_t outer = divide(item, a.count), seq = item - outer * a.count;
+    if (outer >= 2 * a.layers)
         return;
-    char *base = (item / a.count / a.layers == 0 ? a.k : a.v) +
-                 layer * a.pages * a.page * a.row_bytes + 16 * col;
+    const int64_t layer = outer < a.layers ? outer : outer - a.layers;
+    char *base = (outer < a.layers ? a.k : a.v) + layer * a.pages * a.page * a.row_bytes + 16 * col;
     const int32_t *table = a.table + seq * a.table_stride, *keep = a.keep + seq * a.kept;
     const int64_t ctx = a.ctx[seq];
     // byte offset of a position's row, -1 if it has none
     auto row_at = [&](int64_t pos) -> int64_t {
-        const int64_t p = pos / a.page;
-        if (pos < 0 || p >= a.table_stride)
+        if (pos < 0)
+            return -1;
+        const int64_t p = divide(pos, a.page);
+        if (p >= a.table_stride)
             return -1;
         const int64_t number = table[p];
         if (number < 0 || number >= a.pages)
             return -1;
-        return (number * a.page + pos % a.page) * a.row_bytes;
+        return (number * a.page + pos - p * a.page) * a.row_bytes;
     };
     bool more = true;
     for (int64_t t0 = 0; t0 < a.kept && more; t0 += kKeepBatch) {

@@ -196,7 +196,9 @@ __device__ inline int renewed(int x)
     return x;
 }
 
-// A tile of ROWS rows of DP elements.  The 16-byte pieces of a row are
+// A tile of ROWS rows of DP elements, of which the kernels work on the first
+// DU (D of 65 .. 96 lies in rows of 128 and costs three quarters of them:
+// a training step in fp32 with D = 80 took 249 us with all of them).  The 16-byte pieces of a row are
 // exchanged among themselves by its row number: neighbouring rows differ by
 // a pair of pieces and every eighth one by the order within the pair, so
 // that 8 lanes that read one piece of 8 consecutive rows, 16 lanes that read
@@ -354,13 +356,13 @@ struct Stager {
 // One wavefront's share of attention with C = 32 or 16 queries as columns:
 // the shapes, fragments and reductions that depend on C.  A block of keys is
 // C keys; `part` is the lane's share of the terms, lane / C.
-template <class T, int DP, int ROWS, int C> struct Cols;
+template <class T, int DP, int DU, int ROWS, int C> struct Cols;
 
-template <class T, int DP, int ROWS>
-struct Cols<T, DP, ROWS, 32> {
+template <class T, int DP, int DU, int ROWS>
+struct Cols<T, DP, DU, ROWS, 32> {
     typedef Tile<T, DP, ROWS> Tl;
     typedef f32x16 Acc;
-    static constexpr int kAcc = 16, kSteps = DP / 16, kTerms = 16, kBlocks = DP / 32, kGroups = 2;
+    static constexpr int kAcc = 16, kSteps = DU / 16, kTerms = 16, kBlocks = DU / 32, kGroups = 2;
     __device__ static int key_of(int r) { return 8 * (r >> 2) + (r & 3); }    // + 4 * part
     __device__ static int row_base(int lane) { return Tl::row_base(lane); }
     __device__ static int col_base(int lane) { return Tl::col_base(lane); }
@@ -380,11 +382,11 @@ struct Cols<T, DP, ROWS, 32> {
     __device__ static Acc apply(Weights v, Weights p, Acc o) { return mma(v, p, o); }
 };
 
-template <class T, int DP, int ROWS>
-struct Cols<T, DP, ROWS, 16> {
+template <class T, int DP, int DU, int ROWS>
+struct Cols<T, DP, DU, ROWS, 16> {
     typedef Tile<T, DP, ROWS> Tl;
     typedef f32x4 Acc;
-    static constexpr int kAcc = 4, kSteps = DP / 32, kTerms = 32, kBlocks = DP / 16, kGroups = 1;
+    static constexpr int kAcc = 4, kSteps = DU / 32, kTerms = 32, kBlocks = DU / 16, kGroups = 1;
     __device__ static int key_of(int r) { return r; }                          // + 4 * part
     __device__ static int row_base(int lane)
     {
@@ -440,16 +442,16 @@ struct Cols<T, DP, ROWS, 16> {
     __device__ static Acc apply(Weights v, Weights p, Acc o) { return mma16_short(v, p, o); }
 };
 
-// A wavefront's 32 columns of DP results to LDS and back, for the wavefronts
+// A wavefront's 32 columns of DU results to LDS and back, for the wavefronts
 // that share them: `block` of the results is rows 32 * block .. of D.
-template <int DP>
+template <int DP, int DU>
 struct Parked {
     typedef Tile<float, DP, 32> Tl;
     static constexpr int kBytes = Tl::kBytes;
-    __device__ static void put(char *to, int lane, const f32x16 (&x)[DP / 32])
+    __device__ static void put(char *to, int lane, const f32x16 (&x)[DU / 32])
     {
 #pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
+        for (int d = 0; d < DU / 32; ++d)
 #pragma unroll
             for (int g = 0; g < 4; ++g)
                 store4((float *)(to + Tl::at(lane & 31, 8 * d + 2 * g + (lane >> 5))), x[d][4 * g],
@@ -457,10 +459,10 @@ struct Parked {
     }
     // x = mine * x + theirs * what was put
     __device__ static void add(const char *from, int lane, float mine, float theirs,
-                               f32x16 (&x)[DP / 32])
+                               f32x16 (&x)[DU / 32])
     {
 #pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
+        for (int d = 0; d < DU / 32; ++d)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const f32x4 y =

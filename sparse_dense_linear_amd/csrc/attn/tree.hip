@@ -238,13 +238,13 @@ constexpr int per_cu()
 
 // RG groups of C queries; the 4 / RG wavefronts of a group share the keys of
 // a tile.
-template <class T, int DP, int C, int RG>
+template <class T, int DP, int DU, int C, int RG>
 __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP, C>())) void tree_attn(TreeArgs a)
 {
     constexpr int KS = 4 / RG;                 // wavefronts that share a query group's keys
     constexpr int RB = C * RG;                 // queries of a block
     constexpr int kTileKeys = tile_keys(RB);
-    typedef Cols<T, DP, kTileKeys, C> Co;
+    typedef Cols<T, DP, DU, kTileKeys, C> Co;
     typedef typename Co::Acc Acc;
     constexpr int STEPS = Co::kSteps, DB = Co::kBlocks;
     typedef Tile<T, DP, kTileKeys> Tl;
@@ -493,7 +493,7 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP, C>())) void tree_attn(
         __syncthreads();
         const bool done = n0 == 0 && n1 == u.tiles;
         const int64_t slot = 2 * (int64_t)w + (piece_no == 0 ? 0 : 1);
-        constexpr int kOutPieces = DP / 4;
+        constexpr int kOutPieces = DU / 4;
         for (int m = t; m < RB * kOutPieces; m += kAttnThreads) {
             const int lr = m / kOutPieces, p = m % kOutPieces;
             const int rr = block * RB + lr;
@@ -541,7 +541,7 @@ constexpr int kJoinRows = 16;      // query rows of a joining workgroup
 // span are written already), kJoinRows of its rows to a workgroup.  Units are numbered
 // without a list, as find_seq_tile does: the rows of sequence s, in blocks,
 // have the numbers from rowptr[s] * group / rows + s on.
-template <class T, int DP>
+template <class T, int DP, int DU>
 __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int numbers)
 {
     __shared__ int redo[kJoinRows], place[64];
@@ -580,7 +580,7 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int number
     if (a.tree != nullptr && t < 64 && t < u.drafts)
         place[t] = draft_place(u.ctx, draft_mask(a, u.q_begin, u.drafts, t));
     __syncthreads();
-    constexpr int kOutPieces = DP / 4;
+    constexpr int kOutPieces = DU / 4;
     for (int m = t; m < kJoinRows * kOutPieces; m += kAttnThreads) {
         const int lr = m / kOutPieces, p = m % kOutPieces;
         const int r = block * RB + row0 + lr;
@@ -610,22 +610,22 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int number
     finish_again<T>(a, u, seq, hk, block * RB + row0, kJoinRows, redo, place, wave, lane);
 }
 
-template <class T, int DP>
+template <class T, int DP, int DU>
 hipError_t launch(const TreeArgs &a, hipStream_t stream)
 {
     if (a.block_rows == 16)
-        tree_attn<T, DP, 16, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
+        tree_attn<T, DP, DU, 16, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
     else if (a.block_rows == 32)
-        tree_attn<T, DP, 32, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
+        tree_attn<T, DP, DU, 32, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
     else if (a.block_rows == 64)
-        tree_attn<T, DP, 32, 2><<<a.workers, kAttnThreads, 0, stream>>>(a);
+        tree_attn<T, DP, DU, 32, 2><<<a.workers, kAttnThreads, 0, stream>>>(a);
     else
-        tree_attn<T, DP, 32, 4><<<a.workers, kAttnThreads, 0, stream>>>(a);
+        tree_attn<T, DP, DU, 32, 4><<<a.workers, kAttnThreads, 0, stream>>>(a);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess)
         return err;
     const int64_t numbers = a.Tq * (a.Hq / a.Hkv) / a.block_rows + a.S;
-    tree_join<T, DP><<<dim3((uint32_t)(numbers * a.Hkv), a.block_rows / kJoinRows), kAttnThreads, 0, stream>>>(
+    tree_join<T, DP, DU><<<dim3((uint32_t)(numbers * a.Hkv), a.block_rows / kJoinRows), kAttnThreads, 0, stream>>>(
         a, (int)numbers);
     return hipGetLastError();
 }
@@ -654,8 +654,10 @@ TreeShape tree_shape(int dtype, int64_t S, int64_t Tq, int64_t Hq, int64_t Hkv, 
 hipError_t launch_tree(int dtype, const TreeArgs &a, hipStream_t stream)
 {
     if (dtype == SPMM_DTYPE_BF16)
-        return a.D <= 64 ? launch<__bf16, 64>(a, stream) : launch<__bf16, 128>(a, stream);
-    return a.D <= 64 ? launch<float, 64>(a, stream) : launch<float, 128>(a, stream);
+        return a.D <= 64 ? launch<__bf16, 64, 64>(a, stream)
+                         : (a.D <= 96 ? launch<__bf16, 128, 96>(a, stream) : launch<__bf16, 128, 128>(a, stream));
+    return a.D <= 64 ? launch<float, 64, 64>(a, stream)
+                     : (a.D <= 96 ? launch<float, 128, 96>(a, stream) : launch<float, 128, 128>(a, stream));
 }
 
 }  // namespace sdl

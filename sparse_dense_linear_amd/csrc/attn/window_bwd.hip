@@ -53,13 +53,13 @@ __device__ inline float base2(float lse) { return lse == SDL_NEG_INF ? 0.0f : ls
 
 // ------------------------------------------------------------------- dq
 
-template <class T, int DP, int RG>
+template <class T, int DP, int DU, int RG>
 __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_dq(WindowArgs a, int slots)
 {
     constexpr int KT = 64;                       // keys of a tile
     constexpr int KS = 4 / RG;                   // wavefronts that share a group's keys
     constexpr int NB = KT / 32 / KS;             // 32-key blocks of a wavefront
-    constexpr int STEPS = DP / 16, DB = DP / 32;
+    constexpr int STEPS = DU / 16, DB = DU / 32;
     constexpr int kRows = 32 * RG;
     constexpr int kAhead = sizeof(T) == 2 ? 6 : 2;
     typedef Tile<T, DP, KT> Tl;
@@ -179,14 +179,14 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     }
 
     if constexpr (KS == 2) {
-        static_assert(RG == 2 && Parked<DP>::kBytes <= Tl::kBytes, "a buffer for each group");
+        static_assert(RG == 2 && Parked<DP, DU>::kBytes <= Tl::kBytes, "a buffer for each group");
         char *room = wave % RG == 0 ? k_even : k_odd;
         if (ks == 1)
-            Parked<DP>::put(room, lane, dQ);
+            Parked<DP, DU>::put(room, lane, dQ);
         __syncthreads();
         if (ks == 1)
             return;
-        Parked<DP>::add(room, lane, 1.0f, 1.0f, dQ);
+        Parked<DP, DU>::add(room, lane, 1.0f, 1.0f, dQ);
     }
     if (wi0 > i1)
         return;
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     if (redo == 0)
         return;
     // (an infinity times the zeros past D is no number either)
-    if (a.D == DP &&
+    if (a.D == DU &&
         !odd_masked_keys<T, KT>(
             seen, [&](int j) { return r.k + (int64_t)j * r.k_stride; },
             [&](int j) { return r.v + (int64_t)j * r.v_stride; }, wp0, p1, first_tiles, band, lk, a.D, lane))
@@ -295,12 +295,12 @@ __device__ void exact_dkv_row(const WindowArgs &a, int q_begin, int k_begin, int
 
 // Two wavefronts share 32 keys and take the halves of each step's queries;
 // their sums are joined at the end.
-template <class T, int DP>
+template <class T, int DP, int DU>
 __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_dkv(WindowArgs a, int key_slots,
                                                                                    int far_slots, int far_tiles)
 {
-    constexpr int QT = kStepRows, STEPS = DP / 16, DB = DP / 32;
-    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+    constexpr int QT = kStepRows, STEPS = DU / 16, DB = DU / 32;
+    constexpr int kAhead = sizeof(T) == 2 ? 3 : 2;   // 317 us of a training step; 4: 358, 2: 319
     typedef Tile<T, DP, QT> Tl;
     __shared__ __align__(16) char q_even[Tl::kBytes], g_even[Tl::kBytes], q_odd[Tl::kBytes], g_odd[Tl::kBytes];
     __shared__ __align__(16) float stat_even[2 * QT], stat_odd[2 * QT];    // lse, delta
@@ -446,16 +446,16 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
         arrive(stat_even);
     }
 
-    static_assert(Parked<DP>::kBytes <= Tl::kBytes, "a buffer for each sum");
+    static_assert(Parked<DP, DU>::kBytes <= Tl::kBytes, "a buffer for each sum");
     if (qw == 1) {
-        Parked<DP>::put(kw == 0 ? q_even : q_odd, lane, dK);
-        Parked<DP>::put(kw == 0 ? g_even : g_odd, lane, dV);
+        Parked<DP, DU>::put(kw == 0 ? q_even : q_odd, lane, dK);
+        Parked<DP, DU>::put(kw == 0 ? g_even : g_odd, lane, dV);
     }
     __syncthreads();
     if (qw == 1)
         return;
-    Parked<DP>::add(kw == 0 ? q_even : q_odd, lane, 1.0f, 1.0f, dK);
-    Parked<DP>::add(kw == 0 ? g_even : g_odd, lane, 1.0f, 1.0f, dV);
+    Parked<DP, DU>::add(kw == 0 ? q_even : q_odd, lane, 1.0f, 1.0f, dK);
+    Parked<DP, DU>::add(kw == 0 ? g_even : g_odd, lane, 1.0f, 1.0f, dV);
     if (!working)
         return;
     bool clean = true;
@@ -499,7 +499,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     int behind = wj0 + seen.window - shift < lq - 1 ? wj0 + seen.window - shift : lq - 1;
     behind = behind > 0 ? behind : 0;
     const int end = steps.to * QT < lq ? steps.to * QT : lq;
-    if (a.D == DP && !odd_queries<T>(a, q_begin, k_begin, hk, steps.from * QT, before, lane) &&
+    if (a.D == DU && !odd_queries<T>(a, q_begin, k_begin, hk, steps.from * QT, before, lane) &&
         !odd_queries<T>(a, q_begin, k_begin, hk, behind, end, lane))
         return;
     for (uint32_t left = (uint32_t)(redo | (redo >> 32)); left != 0; left &= left - 1)
@@ -507,7 +507,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
 }
 
 // One wavefront for each first key of each sequence and key head.
-template <class T, int DP>
+template <class T, int DP, int DU>
 __global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slots)
 {
     const int lane = threadIdx.x;
@@ -546,7 +546,7 @@ __global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slot
     }
     // queries before the key are all that it does not see
     const int before = j1 - (lk - lq) < lq ? j1 - (lk - lq) : lq;
-    if (!__all(clean) && (a.D != DP || odd_queries<T>(a, q_begin, k_begin, hk, 0, before, lane))) {
+    if (!__all(clean) && (a.D != DU || odd_queries<T>(a, q_begin, k_begin, hk, 0, before, lane))) {
         exact_dkv_row<T>(a, q_begin, k_begin, lq, lk, hk, j, lane);
         return;
     }
@@ -563,15 +563,15 @@ int64_t far_runs(int64_t S, int64_t Tq, int64_t Tk, int64_t window, int64_t sink
     return sinks > 0 && window < Tk ? Tq / kFarRows + S : 0;
 }
 
-template <class T, int DP, int RG>
+template <class T, int DP, int DU, int RG>
 hipError_t launch_dq(const WindowArgs &a, hipStream_t stream)
 {
     const int64_t slots = a.Tq / (32 * RG) + a.S;
-    window_dq<T, DP, RG><<<dim3((uint32_t)(slots * a.Hq)), kAttnThreads, 0, stream>>>(a, (int)slots);
+    window_dq<T, DP, DU, RG><<<dim3((uint32_t)(slots * a.Hq)), kAttnThreads, 0, stream>>>(a, (int)slots);
     return hipGetLastError();
 }
 
-template <class T, int DP>
+template <class T, int DP, int DU>
 hipError_t launch(const WindowArgs &a, hipStream_t stream)
 {
     const int64_t key_slots = a.Tk / kKeyRows + a.S;
@@ -579,17 +579,17 @@ hipError_t launch(const WindowArgs &a, hipStream_t stream)
     const int64_t far_tiles = far > 0 ? (a.sinks + kKeyRows - 1) / kKeyRows : 0;
     hipError_t err;
     if (a.Tq > 0) {
-        err = few_tiles(a) ? launch_dq<T, DP, 2>(a, stream) : launch_dq<T, DP, 4>(a, stream);
+        err = few_tiles(a) ? launch_dq<T, DP, DU, 2>(a, stream) : launch_dq<T, DP, DU, 4>(a, stream);
         if (err != hipSuccess)
             return err;
     }
     if (a.Tk > 0) {
-        window_dkv<T, DP><<<dim3((uint32_t)((key_slots + far * far_tiles) * a.Hkv)), kAttnThreads, 0, stream>>>(
+        window_dkv<T, DP, DU><<<dim3((uint32_t)((key_slots + far * far_tiles) * a.Hkv)), kAttnThreads, 0, stream>>>(
             a, (int)key_slots, (int)far, (int)far_tiles);
         if ((err = hipGetLastError()) != hipSuccess)
             return err;
         if (far > 0) {
-            window_dkv_join<T, DP><<<dim3((uint32_t)(a.S * a.Hkv * a.sinks)), 64, 0, stream>>>(a, (int)far);
+            window_dkv_join<T, DP, DU><<<dim3((uint32_t)(a.S * a.Hkv * a.sinks)), 64, 0, stream>>>(a, (int)far);
             if ((err = hipGetLastError()) != hipSuccess)
                 return err;
         }
@@ -611,8 +611,10 @@ int64_t window_bwd_partial_bytes(int64_t S, int64_t Tq, int64_t Tk, int64_t Hkv,
 hipError_t launch_window_bwd(int dtype, const WindowArgs &a, hipStream_t stream)
 {
     if (dtype == SPMM_DTYPE_BF16)
-        return a.D <= 64 ? launch<__bf16, 64>(a, stream) : launch<__bf16, 128>(a, stream);
-    return a.D <= 64 ? launch<float, 64>(a, stream) : launch<float, 128>(a, stream);
+        return a.D <= 64 ? launch<__bf16, 64, 64>(a, stream)
+                         : (a.D <= 96 ? launch<__bf16, 128, 96>(a, stream) : launch<__bf16, 128, 128>(a, stream));
+    return a.D <= 64 ? launch<float, 64, 64>(a, stream)
+                     : (a.D <= 96 ? launch<float, 128, 96>(a, stream) : launch<float, 128, 128>(a, stream));
 }
 
 }  // namespace sdl

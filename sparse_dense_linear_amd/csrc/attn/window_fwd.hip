@@ -30,13 +30,13 @@ namespace {
 // of a SIMD.  In bf16, 128 queries to a workgroup, tiles of 32 keys leave
 // room for a third workgroup on a CU (16384 tokens, 32 heads of 128 on 8,
 // window 1024: 300 us, against 326 with tiles of 64 and two).
-template <class T, int DP, int RG>
+template <class T, int DP, int DU, int RG>
 __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? (RG == 4 ? 3 : 2) : 1) void window_fwd(WindowArgs a, int slots)
 {
     constexpr int KT = RG == 4 && sizeof(T) == 2 ? 32 : 64;   // keys of a tile
     constexpr int KS = 4 / RG;                   // wavefronts of a group
     constexpr int NB = KT / 32 / KS;             // 32-key blocks of a wavefront
-    constexpr int STEPS = DP / 16, DB = DP / 32;
+    constexpr int STEPS = DU / 16, DB = DU / 32;
     constexpr int kRows = 32 * RG;
     constexpr int kAhead = sizeof(T) == 2 ? 6 : 2;
     typedef Tile<T, DP, KT> Tl;
@@ -173,10 +173,10 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? (RG == 4 ? 3 : 2) : 
 
     total = sum_halves(total);
     if constexpr (KS == 2) {
-        static_assert(RG == 2 && Parked<DP>::kBytes <= Tl::kBytes, "a buffer for each group");
+        static_assert(RG == 2 && Parked<DP, DU>::kBytes <= Tl::kBytes, "a buffer for each group");
         char *room = wave % RG == 0 ? k_even : k_odd;
         if (ks == 1) {
-            Parked<DP>::put(room, lane, O);
+            Parked<DP, DU>::put(room, lane, O);
             if (half == 0) {
                 parked_top[wave % RG][lane] = top;
                 parked_total[wave % RG][lane] = total;
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? (RG == 4 ? 3 : 2) : 
         const float other = parked_top[wave % RG][lane & 31];
         const float now = fmaxf(top, other), base = now == SDL_NEG_INF ? 0.0f : now;
         const float mine = __builtin_amdgcn_exp2f(top - base), theirs = __builtin_amdgcn_exp2f(other - base);
-        Parked<DP>::add(room, lane, mine, theirs, O);
+        Parked<DP, DU>::add(room, lane, mine, theirs, O);
         total = fmaf(theirs, parked_total[wave % RG][lane & 31], mine * total);
         top = now;
     }
@@ -236,18 +236,18 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? (RG == 4 ? 3 : 2) : 
     }
 }
 
-template <class T, int DP, int RG>
+template <class T, int DP, int DU, int RG>
 hipError_t launch(const WindowArgs &a, hipStream_t stream)
 {
     const int64_t slots = a.Tq / (32 * RG) + a.S;
-    window_fwd<T, DP, RG><<<dim3((uint32_t)(slots * a.Hq)), kAttnThreads, 0, stream>>>(a, (int)slots);
+    window_fwd<T, DP, DU, RG><<<dim3((uint32_t)(slots * a.Hq)), kAttnThreads, 0, stream>>>(a, (int)slots);
     return hipGetLastError();
 }
 
-template <class T, int DP>
+template <class T, int DP, int DU>
 hipError_t launch_rows(const WindowArgs &a, hipStream_t stream)
 {
-    return few_tiles(a) ? launch<T, DP, 2>(a, stream) : launch<T, DP, 4>(a, stream);
+    return few_tiles(a) ? launch<T, DP, DU, 2>(a, stream) : launch<T, DP, DU, 4>(a, stream);
 }
 
 }  // namespace
@@ -255,8 +255,10 @@ hipError_t launch_rows(const WindowArgs &a, hipStream_t stream)
 hipError_t launch_window_fwd(int dtype, const WindowArgs &a, hipStream_t stream)
 {
     if (dtype == SPMM_DTYPE_BF16)
-        return a.D <= 64 ? launch_rows<__bf16, 64>(a, stream) : launch_rows<__bf16, 128>(a, stream);
-    return a.D <= 64 ? launch_rows<float, 64>(a, stream) : launch_rows<float, 128>(a, stream);
+        return a.D <= 64 ? launch_rows<__bf16, 64, 64>(a, stream)
+                         : (a.D <= 96 ? launch_rows<__bf16, 128, 96>(a, stream) : launch_rows<__bf16, 128, 128>(a, stream));
+    return a.D <= 64 ? launch_rows<float, 64, 64>(a, stream)
+                     : (a.D <= 96 ? launch_rows<float, 128, 96>(a, stream) : launch_rows<float, 128, 128>(a, stream));
 }
 
 }  // namespace sdl
