@@ -16,6 +16,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;      // positions and windows fit 31 bits
 constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxGridY = 65535;
 constexpr int64_t kMaxSinks = 128;                  // a few first tokens
 constexpr int64_t kMaxStride = (int64_t)1 << 32;
 
@@ -423,8 +424,8 @@ spmm_status_t pages_compact(const attn_pool_t *pool, const int32_t *table, int64
         return bad("table, ctx or keep is null or not 4-byte aligned");
     if (S >= kMaxRows || kept >= kMaxRows || table_stride >= kMaxRows)
         return bad("S, kept and table_stride must be below 2^30");
-    if (too_many(pool->layers, S, pool->row_bytes / 4096 + 1))
-        return unsupported("too many rows for one call");
+    if (pool->layers > 4 * kMaxGridY || pool->row_bytes > kMaxRows / 16)
+        return unsupported("at most 262140 layers, and 64 MiB to a row");
     PagesArgs a = pages_args(pool);
     a.table = table;
     a.table_stride = table_stride;

@@ -12,6 +12,7 @@ namespace {
 constexpr int kCopyPieces = 4;                                  // 16-byte pieces per thread
 constexpr int kCopyBytes = kAttnThreads * kCopyPieces * 16;     // per workgroup
 constexpr int kKeepBatch = 8;                                   // rows a thread holds at once
+constexpr int kItems = 8;                                       // layers and pools of a workgroup
 
 // Workgroup: `parts` of them to a page of one pair, layer and pool.
 __global__ __launch_bounds__(kAttnThreads) void copy_kernel(PagesArgs a, int parts)
@@ -42,57 +43,65 @@ __global__ __launch_bounds__(kAttnThreads) void copy_kernel(PagesArgs a, int par
     }
 }
 
-// Thread: one 16-byte column of one sequence, layer and pool.  It takes the
-// column through all kept rows, so rows never wait for other threads.
+// Workgroup: one sequence, kItems of its (layer, pool) pairs.  Where the kept
+// rows lie is found once, kKeepBatch of them at a time; a thread then takes
+// a 16-byte column through them, all reads before its writes, so rows never
+// wait for other threads.  (Finding them anew in every thread, with a column
+// each, took 35 us for 128 sequences, 32 layers and up to 8 rows of 2 KB; this
+// takes 21.)
 __global__ __launch_bounds__(kAttnThreads) void compact_kernel(PagesArgs a)
 {
-    // (32-bit division where the numbers allow it: the 64-bit one costs more
-    // than the rest of the kernel)
-    auto divide = [](int64_t x, int64_t y) {
-        return ((uint64_t)x | (uint64_t)y) >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
-    };
-    const int64_t cols = a.row_bytes / 16;
-    const int64_t n = (int64_t)blockIdx.x * kAttnThreads + threadIdx.x;
-    const int64_t item = divide(n, cols), col = n - item * cols;
-    const int64_t outer = divide(item, a.count), seq = item - outer * a.count;
-    if (outer >= 2 * a.layers)
-        return;
-    const int64_t layer = outer < a.layers ? outer : outer - a.layers;
-    char *base = (outer < a.layers ? a.k : a.v) + layer * a.pages * a.page * a.row_bytes + 16 * col;
+    __shared__ int64_t from[kKeepBatch], to[kKeepBatch];      // byte offsets in a layer; -1: nothing
+    __shared__ int stop;
+    const int t = threadIdx.x;
+    const int64_t seq = blockIdx.x, first = (int64_t)blockIdx.y * kItems;
+    const int items = (int)(2 * a.layers - first < kItems ? 2 * a.layers - first : kItems);
+    const uint32_t cols = (uint32_t)(a.row_bytes / 16);
+    const int64_t layer_bytes = a.pages * a.page * a.row_bytes;
     const int32_t *table = a.table + seq * a.table_stride, *keep = a.keep + seq * a.kept;
     const int64_t ctx = a.ctx[seq];
     // byte offset of a position's row, -1 if it has none
     auto row_at = [&](int64_t pos) -> int64_t {
-        if (pos < 0)
+        if (pos < 0 || pos / a.page >= a.table_stride)
             return -1;
-        const int64_t p = divide(pos, a.page);
-        if (p >= a.table_stride)
-            return -1;
-        const int64_t number = table[p];
+        const int64_t number = table[pos / a.page];
         if (number < 0 || number >= a.pages)
             return -1;
-        return (number * a.page + pos - p * a.page) * a.row_bytes;
+        return (number * a.page + pos % a.page) * a.row_bytes;
     };
-    bool more = true;
-    for (int64_t t0 = 0; t0 < a.kept && more; t0 += kKeepBatch) {
-        u32x4 piece[kKeepBatch];
-        int64_t to[kKeepBatch];
-#pragma unroll
-        for (int i = 0; i < kKeepBatch; ++i) {
-            to[i] = -1;
-            const int64_t of = more && t0 + i < a.kept ? keep[t0 + i] : -1;
-            more = more && of >= 0;
-            if (more && of != t0 + i) {
-                const int64_t from = row_at(ctx + of);
-                to[i] = from < 0 ? -1 : row_at(ctx + t0 + i);
-                if (to[i] >= 0)
-                    piece[i] = *(const u32x4 *)(base + from);
+    for (int64_t t0 = 0; t0 < a.kept; t0 += kKeepBatch) {
+        if (t < 64) {
+            const int64_t i = t0 + t;
+            const bool mine = t < kKeepBatch && i < a.kept;
+            const int64_t of = mine ? keep[i] : 0;
+            const uint64_t ends = __ballot(mine && of < 0);    // nothing counts from the first on
+            if (t < kKeepBatch) {
+                const bool moves = mine && (ends & (((uint64_t)2 << t) - 1)) == 0 && of != i;
+                const int64_t f = moves ? row_at(ctx + of) : -1;
+                from[t] = f;
+                to[t] = f < 0 ? -1 : row_at(ctx + i);
             }
+            if (t == 0)
+                stop = ends != 0;
         }
+        __syncthreads();
+        for (uint32_t m = t; m < cols * items; m += kAttnThreads) {
+            const uint32_t item = m / cols, col = m - item * cols;
+            const int64_t n = first + item;
+            char *base = (n < a.layers ? a.k + n * layer_bytes : a.v + (n - a.layers) * layer_bytes) + 16 * (int64_t)col;
+            u32x4 piece[kKeepBatch];
 #pragma unroll
-        for (int i = 0; i < kKeepBatch; ++i)
-            if (to[i] >= 0)
-                *(u32x4 *)(base + to[i]) = piece[i];
+            for (int i = 0; i < kKeepBatch; ++i)
+                if (to[i] >= 0)
+                    piece[i] = *(const u32x4 *)(base + from[i]);
+#pragma unroll
+            for (int i = 0; i < kKeepBatch; ++i)
+                if (to[i] >= 0)
+                    *(u32x4 *)(base + to[i]) = piece[i];
+        }
+        if (stop)
+            return;                            // the same for the whole workgroup
+        __syncthreads();
     }
 }
 
@@ -107,8 +116,8 @@ hipError_t launch_pages_copy(const PagesArgs &a, hipStream_t stream)
 
 hipError_t launch_pages_compact(const PagesArgs &a, hipStream_t stream)
 {
-    const int64_t threads = 2 * a.layers * a.count * (a.row_bytes / 16);
-    compact_kernel<<<dim3((uint32_t)((threads + kAttnThreads - 1) / kAttnThreads)), kAttnThreads, 0, stream>>>(a);
+    const dim3 grid((uint32_t)a.count, (uint32_t)((2 * a.layers + kItems - 1) / kItems));
+    compact_kernel<<<grid, kAttnThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
