@@ -35,7 +35,7 @@
  * path: row pointers non-decreasing and within the row counts, page numbers
  * (of what a draft may see) within the pool, tables long enough.
  *
- * Memory: calls allocate nothing.  Two of them take scratch memory from the
+ * Memory: calls allocate nothing.  Some take scratch memory from the
  * caller (device, 16-byte aligned, the size told by a host-only call); its
  * contents need no preparation and mean nothing afterwards.  Calls that may
  * run at the same time, or graphs that may be replayed at the same time,
@@ -87,7 +87,13 @@ spmm_status_t window_attn_fwd(int32_t dtype, const attn_window_t *shape,
                               const attn_rows_t *q, const attn_rows_t *k,
                               const attn_rows_t *v, const int32_t *q_rowptr,
                               const int32_t *k_rowptr, const attn_rows_t *o,
-                              float *lse, void *stream);
+                              float *lse, void *scratch, int64_t scratch_bytes,
+                              void *stream);
+
+/* Host only: scratch bytes of window_attn_fwd for this shape (0: none). */
+spmm_status_t window_attn_fwd_scratch(int32_t dtype,
+                                      const attn_window_t *shape,
+                                      int64_t *bytes);
 
 /*
  * Gradients of window_attn_fwd: with p as there,

@@ -48,14 +48,15 @@ def _lib():
         torch = _torch()
         L = lib()
         P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
-        L.window_attn_fwd.argtypes = [I32] + [P] * 9
+        L.window_attn_fwd.argtypes = [I32] + [P] * 9 + [I64, P]
+        L.window_attn_fwd_scratch.argtypes = [I32, P, P]
         L.window_attn_bwd.argtypes = [I32] + [P] * 13 + [I64, P]
         L.window_attn_bwd_scratch.argtypes = [P, P]
         L.tree_attn_paged.argtypes = [I32] + [P] * 11 + [I64, P]
         L.tree_attn_scratch.argtypes = [I32, P, P]
         L.pages_copy.argtypes = [P, P, P, I64, P]
         L.pages_compact.argtypes = [P, P, I64, P, P, I64, I64, P]
-        for name in ("window_attn_fwd", "window_attn_bwd", "window_attn_bwd_scratch",
+        for name in ("window_attn_fwd", "window_attn_fwd_scratch", "window_attn_bwd", "window_attn_bwd_scratch",
                      "tree_attn_paged", "tree_attn_scratch", "pages_copy", "pages_compact"):
             getattr(L, name).restype = I32
         _ready = L
@@ -193,9 +194,14 @@ def _fwd(q, k, v, q_rowptr, k_rowptr, o, lse, window, sinks, scale, device, hand
     _rows(r, v, "v", device, e, k.shape)
     _rows(r, o, "o", device, e, q.shape)
     r = array("q", r)
-    at = r.buffer_info()[0]
-    st = _ready.window_attn_fwd(dt, ctypes.addressof(w), at, at + _ROWS, at + 2 * _ROWS, qp, kp,
-                                at + 3 * _ROWS, lp, handle)
+    at, shape = r.buffer_info()[0], ctypes.addressof(w)
+    need = ctypes.c_int64()
+    st = _ready.window_attn_fwd_scratch(dt, shape, ctypes.addressof(need))
+    if st:
+        _check(st, "window_attn_fwd_scratch")
+    scratch = torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
+    st = _ready.window_attn_fwd(dt, shape, at, at + _ROWS, at + 2 * _ROWS, qp, kp, at + 3 * _ROWS, lp,
+                                scratch.data_ptr() if need.value else None, need.value, handle)
     if st:
         _check(st, "window_attn_fwd")
 
@@ -236,7 +242,8 @@ def window_attn_fwd(q, k, v, q_rowptr, k_rowptr, o, lse, window=None, sinks: int
     """o and lse of window attention (window_attn_fwd); enqueued on `stream`
     (default: torch's current stream of q's device).  q and o [Tq, Hq, D], k
     and v [Tk, Hkv, D] with any row and head strides, lse [Hq, Tq] float32.
-    window None: no window; scale None: 1 / sqrt(D)."""
+    window None: no window; scale None: 1 / sqrt(D).  The scratch memory, if
+    the call needs any, is taken from torch for this call alone."""
     device = _first(q, "q", 3, "three dimensions: rows, heads, D")
     with _On(device, stream) as handle:
         _fwd(q, k, v, q_rowptr, k_rowptr, o, lse, window, sinks, scale, device, handle)

@@ -225,7 +225,8 @@ extern "C" {
 
 spmm_status_t window_attn_fwd(int32_t dtype, const attn_window_t *shape, const attn_rows_t *q,
                               const attn_rows_t *k, const attn_rows_t *v, const int32_t *q_rowptr,
-                              const int32_t *k_rowptr, const attn_rows_t *o, float *lse, void *stream)
+                              const int32_t *k_rowptr, const attn_rows_t *o, float *lse, void *scratch,
+                              int64_t scratch_bytes, void *stream)
 {
     spmm_status_t st = check_window(dtype, shape);
     if (st != SPMM_SUCCESS)
@@ -250,7 +251,26 @@ spmm_status_t window_attn_fwd(int32_t dtype, const attn_window_t *shape, const a
     a.k_rowptr = k_rowptr;
     a.o = out_rows(o);
     a.lse = lse;
+    a.partial = (float *)scratch;
+    const int64_t need = window_fwd_scratch_bytes(dtype, a);
+    if (scratch_bytes < need)
+        return bad("scratch is smaller than window_attn_fwd_scratch says");
+    if (need > 0 && (scratch == nullptr || !aligned(scratch, 16)))
+        return bad("scratch is null or not 16-byte aligned");
     return launched(launch_window_fwd(dtype, a, (hipStream_t)stream), "window attention");
+}
+
+spmm_status_t window_attn_fwd_scratch(int32_t dtype, const attn_window_t *shape, int64_t *bytes)
+{
+    const spmm_status_t st = check_window(dtype, shape);
+    if (st != SPMM_SUCCESS)
+        return st;
+    if (bytes == nullptr)
+        return bad("bytes is null");
+    WindowArgs a = {};
+    fill_window(a, shape);
+    *bytes = shape->S == 0 || shape->Tq == 0 ? 0 : window_fwd_scratch_bytes(dtype, a);
+    return SPMM_SUCCESS;
 }
 
 spmm_status_t window_attn_bwd_scratch(const attn_window_t *shape, int64_t *bytes)

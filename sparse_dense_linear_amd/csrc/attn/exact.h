@@ -211,9 +211,9 @@ __device__ inline void exact_dkv_add(const GradRows<T> &r, int j, SeenAt seen, i
 // Whether a key or value that the tiles of queries p0 .. p1 brought in behind
 // a mask is not finite.  Tiles of KT keys: those of the first `sinks` keys
 // (first_tiles of them) and from tile `band` on.
-template <class T, int KT, class Key, class Val>
+template <class T, class Key, class Val>
 __device__ inline bool odd_masked_keys(const Seen &seen, Key key, Val val, int p0, int p1, int first_tiles,
-                                       int band, int lk, int D, int lane)
+                                       int band, int KT, int lk, int D, int lane)
 {
     auto odd = [&](int from, int to) {
         to = to < lk ? to : lk;

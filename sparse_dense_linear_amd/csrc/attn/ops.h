@@ -34,7 +34,16 @@ struct WindowArgs {
     Rows dout, out;           // do and o
     OutRows dq, dk, dv;
     float *delta;             // [Hq, Tq]
-    float *partial;           // see window_bwd.hip
+    float *partial;           // scratch: parts of split walks (forward), see
+                              // window_bwd.hip (backward)
+};
+
+// Queries of a forward workgroup; the parts of `tiles` key tiles that its walk
+// is split into, at most `parts`; and where they leave maximum and sum, and
+// unnormalised output.
+struct SplitShape {
+    int32_t rows, tiles, parts;
+    float *stat, *out;
 };
 
 // Whether workgroups of 128 queries are too few to fill the 512 places that
@@ -43,6 +52,7 @@ inline bool few_tiles(const WindowArgs &a) { return (a.Tq / 128 + a.S) * a.Hq < 
 
 hipError_t launch_window_fwd(int dtype, const WindowArgs &a, hipStream_t stream);
 hipError_t launch_window_bwd(int dtype, const WindowArgs &a, hipStream_t stream);
+int64_t window_fwd_scratch_bytes(int dtype, const WindowArgs &a);
 // Bytes of delta and of the partial sums (0: none) of a backward call.
 int64_t window_bwd_delta_bytes(int64_t Tq, int64_t Hq);
 int64_t window_bwd_partial_bytes(int64_t S, int64_t Tq, int64_t Tk, int64_t Hkv, int64_t D,

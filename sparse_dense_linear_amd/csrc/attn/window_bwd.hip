@@ -212,9 +212,9 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
         return;
     // (an infinity times the zeros past D is no number either)
     if (a.D == DU &&
-        !odd_masked_keys<T, KT>(
+        !odd_masked_keys<T>(
             seen, [&](int j) { return r.k + (int64_t)j * r.k_stride; },
-            [&](int j) { return r.v + (int64_t)j * r.v_stride; }, wp0, p1, first_tiles, band, lk, a.D, lane))
+            [&](int j) { return r.v + (int64_t)j * r.v_stride; }, wp0, p1, first_tiles, band, KT, lk, a.D, lane))
         return;
     for (uint32_t left = (uint32_t)(redo | (redo >> 32)); left != 0; left &= left - 1) {
         const int n = __ffs(left) - 1, i = wi0 + n, p = i + shift;

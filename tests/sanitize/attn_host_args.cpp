@@ -47,7 +47,10 @@ void windows()
                     const spmm_status_t st = window_attn_bwd_scratch(&w, &bytes);
                     EXPECT(st == SPMM_SUCCESS ? bytes >= 0 : bytes == -1);
                     // no scratch, an unknown type, a misaligned lse: refused, or nothing to do
-                    EXPECT(window_attn_fwd(7, &w, &r, &r, &r, p, p, &r, f, nullptr) != SPMM_SUCCESS);
+                    EXPECT(window_attn_fwd(7, &w, &r, &r, &r, p, p, &r, f, nullptr, 0, nullptr) != SPMM_SUCCESS);
+                    int64_t forward = -1;
+                    EXPECT(window_attn_fwd_scratch(SPMM_DTYPE_BF16, &w, &forward) == st);
+                    EXPECT(st == SPMM_SUCCESS ? forward >= 0 : forward == -1);
                     const spmm_status_t back = window_attn_bwd(SPMM_DTYPE_F32, &w, &r, &r, &r, &r, &r, f, p, p,
                                                                &r, &r, &r, nullptr, 0, nullptr);
                     EXPECT(back != SPMM_SUCCESS || w.S == 0 || (w.Tq == 0 && w.Tk == 0));
@@ -55,7 +58,7 @@ void windows()
     for (int64_t x : kExtremes)
         for (int64_t y : kExtremes) {
             const attn_rows_t odd = {fake(), x, y};
-            EXPECT(window_attn_fwd(SPMM_DTYPE_F32, &good, &odd, &r, &r, nullptr, p, &odd, f, nullptr) !=
+            EXPECT(window_attn_fwd(SPMM_DTYPE_F32, &good, &odd, &r, &r, nullptr, p, &odd, f, nullptr, 0, nullptr) !=
                    SPMM_SUCCESS);
         }
 }

@@ -37,7 +37,8 @@ def header_functions():
 def test_library_exports_every_declared_symbol():
     names = header_functions()
     assert names == ["pages_compact", "pages_copy", "tree_attn_paged", "tree_attn_scratch",
-                     "window_attn_bwd", "window_attn_bwd_scratch", "window_attn_fwd"]
+                     "window_attn_bwd", "window_attn_bwd_scratch", "window_attn_fwd",
+                     "window_attn_fwd_scratch"]
     lib = ctypes.CDLL(sdl.lib_path())
     assert not [n for n in names if not hasattr(lib, n)]
 
@@ -62,9 +63,9 @@ def rows(heads=4, D=64, data=FAKE, **change):
     return _attn._Rows(**a)
 
 
-def fwd(w=None, dtype=F32, q=None, k=None, v=None, o=None, qp=FAKE, kp=FAKE, lse=FAKE):
+def fwd(w=None, dtype=F32, q=None, k=None, v=None, o=None, qp=FAKE, kp=FAKE, lse=FAKE, scratch=FAKE, size=1 << 40):
     return LIB.window_attn_fwd(dtype, w or window(), q or rows(), k or rows(2), v or rows(2), qp, kp,
-                                        o or rows(), lse, None)
+                               o or rows(), lse, scratch, size, None)
 
 
 def bwd(w=None, dtype=F32, scratch=FAKE, size=1 << 30, lse=FAKE, **r):
@@ -91,6 +92,7 @@ def test_window_refuses_shapes(change, expect):
     assert sdl.lib().spmm_last_error() != b""
     need = ctypes.c_int64(-1)
     assert LIB.window_attn_bwd_scratch(window(**change), need) == expect
+    assert LIB.window_attn_fwd_scratch(F32, window(**change), need) == expect
     assert need.value == -1
 
 
@@ -120,9 +122,16 @@ def test_window_refuses_the_rest():
     assert bwd(size=need.value - 1) == INVALID and bwd(scratch=None) == INVALID
     assert bwd(scratch=FAKE + 4) == INVALID
     assert LIB.window_attn_bwd_scratch(window(), None) == INVALID
-    assert LIB.window_attn_fwd(F32, None, rows(), rows(), rows(), FAKE, FAKE, rows(), FAKE, None) == INVALID
-    assert LIB.window_attn_fwd(F32, window(), None, rows(), rows(), FAKE, FAKE, rows(), FAKE,
-                                        None) == INVALID
+    assert LIB.window_attn_fwd_scratch(F32, window(), None) == INVALID
+    assert LIB.window_attn_fwd(F32, None, rows(), rows(), rows(), FAKE, FAKE, rows(), FAKE, FAKE, 1, None) == INVALID
+    assert LIB.window_attn_fwd(F32, window(), None, rows(), rows(), FAKE, FAKE, rows(), FAKE, FAKE, 1,
+                               None) == INVALID
+    # few queries behind many keys: the walks are split, and need room
+    long = window(Tk=1 << 20, window=1 << 20)
+    assert LIB.window_attn_fwd_scratch(F32, long, need) == 0 and need.value > 0
+    assert fwd(long, size=need.value - 1) == INVALID and fwd(long, scratch=None) == INVALID
+    assert fwd(long, scratch=FAKE + 8) == INVALID
+    assert LIB.window_attn_fwd_scratch(F32, window(), need) == 0 and need.value == 0
 
 
 def test_nothing_to_do():

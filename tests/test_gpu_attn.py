@@ -100,6 +100,26 @@ def test_many_far_runs(dtype):
     check([1100], [2100], 2, 2, 128, dtype, 100, 128, seed=9)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (3000, 70), (700, 4)])
+def test_long_walks_are_split_and_joined(dtype, window, sinks):
+    """Few queries behind many keys, beside short sequences; what a masked
+    place holds stays out of the joined results too."""
+    check([300, 60], [5000, 60], 2, 1, 64, dtype, window, sinks, seed=24, grad=False)   # 128 to a workgroup
+    ql, kl = [70, 1, 5, 0], [5000, 3000, 40, 7]                                         # 64
+    check(ql, kl, 2, 1, 72, dtype, window, sinks, seed=22)
+    q, k, v, do, qs, ks = operands(ql, kl, 2, 1, 128, dtype, seed=23)
+    w = sdl.NO_WINDOW if window is None else window
+    want = window_ref(q, k, v, qs, ks, w, sinks)
+    k2, v2 = k.clone(), v.clone()
+    k2[4990], v2[4990] = float("nan"), float("inf")    # queries 60 and later of the first sequence see it
+    o, lse = sdl.window_attention(q.cuda(), k2.cuda(), v2.cuda(), i32(qs), i32(ks), window=window, sinks=sinks)
+    keep = torch.tensor([i for i in range(qs[-1]) if not 60 <= i < 70])
+    assert_close(o.cpu()[keep], want["o"][keep], want["o_tol"][keep], "o")
+    assert_close(lse.cpu()[:, keep], want["lse"][:, keep], want["lse_tol"][:, keep], "lse")
+    assert bool(torch.isnan(o[60:70]).all()) and bool(torch.isnan(lse[:, 60:70]).all())
+
+
 def test_scale():
     check([90], [90], 2, 1, 64, F32, 33, 1, seed=2, scale=0.7)
     check([90], [90], 2, 1, 64, BF16, 33, 1, seed=2, scale=0.05)
