@@ -8,7 +8,7 @@
 // matrix product with its keys, so each cached row is read once for all of
 // them (for up to 32 * RG of them; more take another turn over L2).
 //
-// Work is counted in tiles of 128 keys over (sequence, key head, block of
+// Work is counted in tiles of keys over (sequence, key head, block of
 // queries) and cut into equal spans, one per workgroup, so that ragged
 // batches and single long sequences fill the GPU alike.  A unit that lies
 // within one span is finished there; one that is cut leaves its running
@@ -25,7 +25,7 @@ namespace sdl {
 namespace {
 
 
-// Keys of a tile: with 16 queries to a block, four workgroups share a CU and
+// Keys of a tile: with 16 queries to a block, three workgroups share a CU and
 // each has half a tile.
 __host__ __device__ constexpr int tile_keys(int block_rows) { return block_rows == 16 ? 64 : 128; }
 
@@ -155,6 +155,81 @@ struct Slots {
     }
 };
 
+// A workgroup's span, and the sequence that holds its first tile.
+struct Span {
+    int w, seq;
+    int64_t at, stop;      // tiles
+    int64_t base;          // first tile of the sequence
+
+    // By all threads of the workgroup; false: it has none.
+    __device__ bool begin(const TreeArgs &a, const Slots &slots)
+    {
+        __shared__ int64_t scan[4];
+        __shared__ int found;
+        __shared__ int64_t found_base;
+        const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+        // the total of all tiles, then the sequence
+        Spans spans;
+        spans.tiles = 0;
+        for (int s0 = 0; s0 < a.S; s0 += kAttnThreads) {
+            int64_t n = 0;
+            if (s0 + t < a.S) {
+                const Unit u = unit_of(a, s0 + t);
+                n = (int64_t)a.Hkv * u.blocks * u.tiles;
+            }
+            for (int d = 32; d > 0; d >>= 1)
+                n += __shfl_xor(n, d);
+            if (lane == 0)
+                scan[wave] = n;
+            __syncthreads();
+            spans.tiles += scan[0] + scan[1] + scan[2] + scan[3];
+            __syncthreads();
+        }
+        spans.workers = spans.tiles < a.workers ? (int)spans.tiles : a.workers;
+        if ((int)blockIdx.x >= spans.workers)
+            return false;
+        w = xcd_order(blockIdx.x, spans.workers);
+        at = spans.start(w);
+        stop = spans.start(w + 1);
+        int64_t sum = 0;
+        for (int s0 = 0; s0 < a.S; s0 += kAttnThreads) {
+            int64_t n = 0;
+            if (s0 + t < a.S) {
+                const Unit u = unit_of(a, s0 + t);
+                n = (int64_t)a.Hkv * u.blocks * u.tiles;
+            }
+            int64_t upto = n;                  // inclusive sum over the wavefront
+            for (int d = 1; d < 64; d <<= 1) {
+                const int64_t y = __shfl_up(upto, d);
+                if (lane >= d)
+                    upto += y;
+            }
+            if (lane == 63)
+                scan[wave] = upto;
+            __syncthreads();
+            for (int i = 0; i < wave; ++i)
+                upto += scan[i];
+            upto += sum;
+            if (s0 + t < a.S) {
+                if (upto - n <= at && at < upto) {
+                    found = s0 + t;
+                    found_base = upto - n;
+                }
+                if (w == 0) {
+                    slots.base[s0 + t] = upto - n;
+                    if (s0 + t == a.S - 1)
+                        slots.base[a.S] = upto;
+                }
+            }
+            sum += scan[0] + scan[1] + scan[2] + scan[3];
+            __syncthreads();
+        }
+        seq = found;
+        base = found_base;
+        return true;
+    }
+};
+
 // A finished row lr of a block: four elements of its output from the sum of
 // weights and the unnormalised values.  redo[lr]: 1, the output is to be
 // computed again if a row that is masked is not finite; 2, the sum too (no
@@ -229,17 +304,17 @@ __device__ inline u32x4 load_once(const u32x4 *p)
 }
 
 // Workgroups to a CU that registers and LDS allow.
-template <class T, int DP, int C>
-constexpr int per_cu()
+template <class T, int DP>
+constexpr int per_cu(int block_rows)
 {
-    constexpr int tile = 2 * tile_keys(C) * DP * (int)sizeof(T);
-    return tile <= 16384 ? 4 : (tile <= 32768 && C == 16 ? 3 : (tile <= 65536 ? 2 : 1));
+    const int tile = 2 * tile_keys(block_rows) * DP * (int)sizeof(T);
+    return tile <= 16384 ? 4 : (tile <= 32768 && block_rows == 16 ? 3 : (tile <= 65536 ? 2 : 1));
 }
 
 // RG groups of C queries; the 4 / RG wavefronts of a group share the keys of
 // a tile.
 template <class T, int DP, int DU, int C, int RG>
-__global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP, C>())) void tree_attn(TreeArgs a)
+__global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_attn(TreeArgs a)
 {
     constexpr int KS = 4 / RG;                 // wavefronts that share a query group's keys
     constexpr int RB = C * RG;                 // queries of a block
@@ -252,9 +327,6 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP, C>())) void tree_attn(
     constexpr int kPiecesPer = kTileKeys * Tl::kPieces / kAttnThreads;
     constexpr int kBytes = 2 * Tl::kBytes > 4 * Out::kBytes ? 2 * Tl::kBytes : 4 * Out::kBytes;
     __shared__ __align__(16) char lds[kBytes];
-    __shared__ int64_t scan[4];
-    __shared__ int found;
-    __shared__ int64_t found_base;
     __shared__ int place[64];
     __shared__ float tops[4][C], totals[4][C];
     __shared__ int redo[RB];
@@ -267,67 +339,13 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP, C>())) void tree_attn(
     const float c2 = a.scale * kLog2e;
     const Slots slots(a);
 
-    // ---- this workgroup's span: total of all tiles, then the sequence that
-    // holds the span's first one
-    Spans spans;
-    spans.tiles = 0;
-    for (int s0 = 0; s0 < a.S; s0 += kAttnThreads) {
-        int64_t n = 0;
-        if (s0 + t < a.S) {
-            const Unit u = unit_of(a, s0 + t);
-            n = (int64_t)a.Hkv * u.blocks * u.tiles;
-        }
-        for (int d = 32; d > 0; d >>= 1)
-            n += __shfl_xor(n, d);
-        if (lane == 0)
-            scan[wave] = n;
-        __syncthreads();
-        spans.tiles += scan[0] + scan[1] + scan[2] + scan[3];
-        __syncthreads();
-    }
-    if (spans.tiles == 0)
+    Span span;
+    if (!span.begin(a, slots))
         return;
-    spans.workers = spans.tiles < a.workers ? (int)spans.tiles : a.workers;
-    const int w = xcd_order(blockIdx.x, gridDim.x);
-    if (w >= spans.workers)
-        return;
-    int64_t at = spans.start(w);
-    const int64_t stop = spans.start(w + 1);
-    int64_t base = 0;
-    for (int s0 = 0; s0 < a.S; s0 += kAttnThreads) {
-        int64_t n = 0;
-        if (s0 + t < a.S) {
-            const Unit u = unit_of(a, s0 + t);
-            n = (int64_t)a.Hkv * u.blocks * u.tiles;
-        }
-        int64_t upto = n;                      // inclusive sum over the wavefront
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t y = __shfl_up(upto, d);
-            if (lane >= d)
-                upto += y;
-        }
-        if (lane == 63)
-            scan[wave] = upto;
-        __syncthreads();
-        for (int i = 0; i < wave; ++i)
-            upto += scan[i];
-        upto += base;
-        if (s0 + t < a.S) {
-            if (upto - n <= at && at < upto) {
-                found = s0 + t;
-                found_base = upto - n;
-            }
-            if (w == 0) {
-                slots.base[s0 + t] = upto - n;
-                if (s0 + t == a.S - 1)
-                    slots.base[a.S] = upto;
-            }
-        }
-        base += scan[0] + scan[1] + scan[2] + scan[3];
-        __syncthreads();
-    }
-    int seq = found;
-    base = found_base;
+    const int w = span.w;
+    int64_t at = span.at, base = span.base;
+    const int64_t stop = span.stop;
+    int seq = span.seq;
 
     // ---- the units of the span, one piece after another
     int64_t piece_no = 0;
@@ -640,13 +658,10 @@ TreeShape tree_shape(int dtype, int64_t S, int64_t Tq, int64_t Hq, int64_t Hkv, 
     const int64_t rows = S > 0 ? (Tq + S - 1) / S * (Hq / Hkv) : 0;
     sh.block_rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
     // as many workgroups as the 256 CUs hold at once
-    const int C = sh.block_rows == 16 ? 16 : 32;
     if (dtype == SPMM_DTYPE_BF16)
-        sh.workers = 256 * (DP == 64 ? (C == 16 ? per_cu<__bf16, 64, 16>() : per_cu<__bf16, 64, 32>())
-                                     : (C == 16 ? per_cu<__bf16, 128, 16>() : per_cu<__bf16, 128, 32>()));
+        sh.workers = 256 * (DP == 64 ? per_cu<__bf16, 64>(sh.block_rows) : per_cu<__bf16, 128>(sh.block_rows));
     else
-        sh.workers = 256 * (DP == 64 ? (C == 16 ? per_cu<float, 64, 16>() : per_cu<float, 64, 32>())
-                                     : (C == 16 ? per_cu<float, 128, 16>() : per_cu<float, 128, 32>()));
+        sh.workers = 256 * (DP == 64 ? per_cu<float, 64>(sh.block_rows) : per_cu<float, 128>(sh.block_rows));
     sh.bytes = 4 * (2 * ((S + 1 + 31) / 32 * 32) + 2 * (int64_t)sh.workers * sh.block_rows * (2 + DP));
     return sh;
 }
