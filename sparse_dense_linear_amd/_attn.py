@@ -5,6 +5,7 @@ from __future__ import annotations
 import ctypes
 import math
 from array import array
+from operator import index
 
 from ._binding import DTYPE_BF16, DTYPE_F32, _check, _torch, lib
 
@@ -159,7 +160,7 @@ def _scale(scale, d) -> float:
 
 
 def _window_size(window) -> int:
-    return NO_WINDOW if window is None else int(window)
+    return NO_WINDOW if window is None else index(window)
 
 
 def _window_shape(q, k, v, q_rowptr, window, sinks, scale, device):
@@ -175,7 +176,7 @@ def _window_shape(q, k, v, q_rowptr, window, sinks, scale, device):
         raise ValueError("q_rowptr must hold S+1 entries")
     Tq, Hq, D = q.shape
     Tk, Hkv, _ = k.shape
-    return _Window(S, Tq, Tk, Hq, Hkv, D, _window_size(window), int(sinks), _scale(scale, D), 0), S
+    return _Window(S, Tq, Tk, Hq, Hkv, D, _window_size(window), index(sinks), _scale(scale, D), 0), S
 
 
 # ----------------------------------------------------------------- window
@@ -333,7 +334,7 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
     hs = hs if Hkv > 1 else D
     rs = rs if page > 1 else Hkv * D
     ps = ps if pages > 1 else page * Hkv * D
-    w = _Tree(S, Tq, Hq, Hkv, D, page, ps, rs, hs, table.shape[1], _window_size(window), int(sinks),
+    w = _Tree(S, Tq, Hq, Hkv, D, page, ps, rs, hs, table.shape[1], _window_size(window), index(sinks),
               _scale(scale, D), 0)
     r = []
     _rows(r, q, "q", device, q.dtype, q.shape)

@@ -451,6 +451,8 @@ def test_binding_refusals():
     bad(sdl.SpmmError, q=q[:, :, :60], k=k[:, :, :60], v=k[:, :, :60])
     bad(sdl.SpmmError, q=torch.zeros(10, 4, 66, device="cuda")[:, :, :64])   # strides
     bad(sdl.SpmmError, window=0)
+    bad(TypeError, window=2.5)
+    bad(TypeError, sinks=1.0)
     bad(sdl.SpmmError, sinks=200)
     bad(sdl.SpmmError, scale=-1.0)
     o, lse = sdl.window_attention(**ok)
