@@ -46,8 +46,9 @@ struct SplitShape {
     float *stat, *out;
 };
 
-// Whether workgroups of 128 queries are too few to fill the 512 places that
-// the GPU has for them (two to a CU): then 64 queries each.
+// Whether workgroups of 128 queries make less than two rounds of the 512
+// places that the GPU has for them (two to a CU): then 64 queries each, or
+// split walks.
 inline bool few_tiles(const WindowArgs &a) { return (a.Tq / 128 + a.S) * a.Hq < 1024; }
 
 hipError_t launch_window_fwd(int dtype, const WindowArgs &a, hipStream_t stream);

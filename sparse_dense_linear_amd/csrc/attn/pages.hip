@@ -15,7 +15,7 @@ constexpr int kKeepBatch = 8;                                   // rows a thread
 constexpr int kItems = 8;                                       // layers and pools of a workgroup
 
 // Workgroup: `parts` of them to a page of one pair, layer and pool.  Stores
-// past the caches: 250 pages of 32 KB in 32 layers, 184 us (5.7 TB/s read and
+// past the caches: 250 pages of 32 KB in 32 layers, 182 us (5.8 TB/s read and
 // written; a large copy reaches 5.1) against 194.
 __global__ __launch_bounds__(kAttnThreads) void copy_kernel(PagesArgs a, int parts)
 {

