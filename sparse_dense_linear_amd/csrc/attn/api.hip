@@ -148,7 +148,7 @@ struct BwdScratch {
 BwdScratch bwd_scratch(const attn_window_t *w)
 {
     return {window_bwd_delta_bytes(w->Tq, w->Hq),
-            window_bwd_partial_bytes(w->S, w->Tq, w->Tk, w->Hkv, w->D, clamp_window(w->window),
+            window_bwd_partial_bytes(w->S, w->Tq, w->Tk, w->Hq, w->Hkv, w->D, clamp_window(w->window),
                                      w->sinks)};
 }
 

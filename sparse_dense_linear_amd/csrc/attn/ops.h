@@ -56,7 +56,7 @@ hipError_t launch_window_bwd(int dtype, const WindowArgs &a, hipStream_t stream)
 int64_t window_fwd_scratch_bytes(int dtype, const WindowArgs &a);
 // Bytes of delta and of the partial sums (0: none) of a backward call.
 int64_t window_bwd_delta_bytes(int64_t Tq, int64_t Hq);
-int64_t window_bwd_partial_bytes(int64_t S, int64_t Tq, int64_t Tk, int64_t Hkv, int64_t D,
+int64_t window_bwd_partial_bytes(int64_t S, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
                                  int64_t window, int64_t sinks);
 
 struct TreeArgs {

@@ -13,14 +13,15 @@
 //
 // The first `sinks` keys are seen by every later query.  Their workgroup
 // would walk the whole sequence while the others walk one window, so what
-// lies past its window is cut into runs of kFarRows queries with a workgroup
-// each; those and the window's part leave fp32 partial sums, which a last
-// small launch adds in a fixed order.
+// lies past its window is cut into runs of queries with a workgroup each;
+// those and the window's part leave fp32 partial sums, which a last small
+// launch adds in a fixed order.  Where key tiles are few, their windows are
+// taken in parts too (dkv_parts).
 //
 // 8192 tokens, 32 heads of 128 on 8, window 1024, bf16 (forward 145 us): dq
-// 200 us, dk and dv 313, the join 5.  dq keeps the matrix cores busy 41 % of the cycles, as
-// the forward does; dk and dv, with 128 accumulator registers a lane for two
-// gradients, have two workgroups on a CU and 37 %.  fp32 is nearer to its
+// 200 us, dk and dv 313, the join 5.  dq keeps the matrix cores busy 41 % of
+// the cycles, as the forward does; dk and dv, with 128 accumulator registers
+// a lane for two gradients, have two workgroups on a CU and 37 %.  fp32 is nearer to its
 // bound (60 % in dk and dv): its matrix instructions are 16 times slower, so
 // everything else hides behind them.
 #include "ops.h"
@@ -35,7 +36,6 @@ namespace {
 
 constexpr int kKeyRows = 64;      // keys of a dk/dv workgroup
 constexpr int kStepRows = 64;     // queries of one step of it
-constexpr int kFarRows = 512;     // queries of a far run
 
 template <class T>
 __device__ GradRows<T> grad_rows(const WindowArgs &a, int q_begin, int k_begin, int head, int hk)
@@ -300,11 +300,45 @@ __device__ void exact_dkv_row(const WindowArgs &a, int q_begin, int k_begin, int
     put_row(v, dv[0], dv[1], a.D, lane);
 }
 
+// Where part `part` of key tile `unit` leaves 32 of its keys' sums (keys 32 * kw
+// on): registers in turn, a lane's four elements behind each other.
+template <int DU>
+__device__ inline float *sums_at(float *sums, int unit, int parts, int part, int kw)
+{
+    return sums + (((int64_t)unit * parts + part) * 2 + kw) * (2 * DU * 32);
+}
+
+// Computes rows of keys again that came out non-finite, where that is called
+// for: bits 0 .. 31 (and the same again from 32) of `redo` are keys wj0 .. wj1;
+// steps: the queries that the tile met.
+template <class T, int DU>
+__device__ inline void again_dkv(const WindowArgs &a, const Seen &seen, uint64_t redo, const StepRange &steps,
+                                 int wj0, int wj1, int q_begin, int k_begin, int lq, int lk, int hk, int lane)
+{
+    if (redo == 0)
+        return;
+    // queries of the steps that a key of this wavefront does not see: before
+    // the keys, and behind the window (a step's missing rows repeat the last)
+    const int shift = lk - lq;
+    const int before = wj1 - shift < lq ? wj1 - shift : lq;
+    int behind = wj0 + seen.window - shift < lq - 1 ? wj0 + seen.window - shift : lq - 1;
+    behind = behind > 0 ? behind : 0;
+    const int end = steps.to * kStepRows < lq ? steps.to * kStepRows : lq;
+    if (a.D == DU && !odd_queries<T>(a, q_begin, k_begin, hk, steps.from * kStepRows, before, lane) &&
+        !odd_queries<T>(a, q_begin, k_begin, hk, behind, end, lane))
+        return;
+    for (uint32_t left = (uint32_t)(redo | (redo >> 32)); left != 0; left &= left - 1)
+        exact_dkv_row<T>(a, q_begin, k_begin, lq, lk, hk, wj0 + __ffs(left) - 1, lane);
+}
+
 // Two wavefronts share 32 keys and take the halves of each step's queries;
-// their sums are joined at the end.
+// their sums are joined at the end.  Where there are few key tiles, the
+// queries of a tile are taken in gridDim.y parts (dkv_parts), which leave
+// their sums for window_dkv_parts.
 template <class T, int DP, int DU>
 __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_dkv(WindowArgs a, int key_slots,
-                                                                                   int far_slots, int far_tiles)
+                                                                                   int far_slots, int far_tiles,
+                                                                                   int far_rows, float *sums)
 {
     constexpr int QT = kStepRows, STEPS = DU / 16, DB = DU / 32;
     constexpr int kAhead = sizeof(T) == 2 ? 3 : 2;   // 317 us of a training step; 4: 358, 2: 319
@@ -318,7 +352,10 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     const int idx = xcd_order(blockIdx.x, gridDim.x);
     const int hk = idx / per_head, rest = idx % per_head;
     const bool far = rest < far_items;
-    const SeqTile st = far ? find_seq_tile(a.q_rowptr, a.S, kFarRows, rest / far_tiles)
+    const int parts = gridDim.y, part_no = blockIdx.y;
+    if (far && part_no > 0)
+        return;
+    const SeqTile st = far ? find_seq_tile(a.q_rowptr, a.S, far_rows, rest / far_tiles)
                            : find_seq_tile(a.k_rowptr, a.S, kKeyRows, rest - far_items);
     if (st.seq < 0)
         return;
@@ -341,7 +378,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     const int all_steps = (lq + QT - 1) / QT;
     const bool has_far = j0 < seen.sinks && steps.to < all_steps;
     if (far) {
-        const int b = st.tile * (kFarRows / QT), e = b + kFarRows / QT;
+        const int b = st.tile * (far_rows / QT), e = b + far_rows / QT;
         steps.from = b > steps.to ? b : steps.to;
         steps.to = e < all_steps ? e : all_steps;
         if (steps.from >= steps.to)
@@ -350,10 +387,20 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     const bool working = wj0 <= j1 && (!far || wj0 < seen.sinks);
 
     // items: head of the group, then step
-    const int count = group * (steps.to - steps.from);
+    const int length = steps.to - steps.from;
+    int begin = 0, count = group * length;
+    if (parts > 1 && !far) {
+        begin = (int)((int64_t)count * part_no / parts);
+        count = (int)((int64_t)count * (part_no + 1) / parts) - begin;
+    }
     float carried = 0.0f;            // lse or delta of one row on its way to LDS
     const Stager<T, DP, QT, 4> q_in(a.q.row_stride, a.D), g_in(a.dout.row_stride, a.D);
-    int next_head = hk * group, next_step = steps.from;     // of the next fetch
+    // of the next fetch
+    int next_head = hk * group, next_step = steps.from;
+    if (begin > 0) {
+        next_head += begin / length;
+        next_step += begin % length;
+    }
     auto fetch = [&](char *qt, char *gt) {
         const int first = next_step * QT;
         const GradRows<T> r = grad_rows<T>(a, q_begin, k_begin, next_head, hk);
@@ -374,6 +421,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
             stat[t] = carried;
         __syncthreads();
     };
+    const int next_step0 = next_step;
     if (count > 0)
         fetch(q_even, g_even);
 
@@ -396,7 +444,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
         dV[d] = f32x16(0.0f);
     }
 
-    int this_step = steps.from;
+    int this_step = next_step0;
     auto compute = [&](const char *qt, const char *gt, const float *stat) {
         const int first = this_step * QT + 32 * qw;          // the wavefront's rows
         const int last = (first + 32 < lq ? first + 32 : lq) - 1;
@@ -465,6 +513,18 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
     Parked<DP, DU>::add(kw == 0 ? g_even : g_odd, lane, 1.0f, 1.0f, dV);
     if (!working)
         return;
+    if (parts > 1 && !far) {
+        float *to = sums_at<DU>(sums, hk * key_slots + rest - far_items, parts, part_no, kw) + 4 * lane;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                store4(to + 256 * (4 * d + g), dK[d][4 * g], dK[d][4 * g + 1], dK[d][4 * g + 2], dK[d][4 * g + 3]);
+                store4(to + 256 * (4 * (DB + d) + g), dV[d][4 * g], dV[d][4 * g + 1], dV[d][4 * g + 2],
+                       dV[d][4 * g + 3]);
+            }
+        return;
+    }
     bool clean = true;
     const bool part = has_far && key < seen.sinks;    // summed by the last launch
     if (part && key <= j1) {
@@ -497,25 +557,71 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
                     store4(v + at, z[0], z[1], z[2], z[3]);
                 }
     }
-    const uint64_t redo = __ballot(!clean);
-    if (redo == 0)
+    again_dkv<T, DU>(a, seen, __ballot(!clean), steps, wj0, wj1, q_begin, k_begin, lq, lk, hk, lane);
+}
+
+constexpr int kPartThreads = 512;
+
+// Adds the parts of half a key tile in order, and for first keys their far
+// runs.
+template <class T, int DP, int DU>
+__global__ __launch_bounds__(kPartThreads) void window_dkv_parts(WindowArgs a, int key_slots, int far_rows,
+                                                                 int parts, float *sums)
+{
+    constexpr int DB = DU / 32;
+    __shared__ int odd[32];
+    const int unit = blockIdx.x, hk = unit / key_slots, kw = blockIdx.y;
+    const SeqTile st = find_seq_tile(a.k_rowptr, a.S, kKeyRows, unit % key_slots);
+    if (st.seq < 0)
         return;
-    // queries of the steps that a key of this wavefront does not see: before
-    // the keys, and behind the window (a step's missing rows repeat the last)
-    const int before = wj1 - shift < lq ? wj1 - shift : lq;
-    int behind = wj0 + seen.window - shift < lq - 1 ? wj0 + seen.window - shift : lq - 1;
-    behind = behind > 0 ? behind : 0;
-    const int end = steps.to * QT < lq ? steps.to * QT : lq;
-    if (a.D == DU && !odd_queries<T>(a, q_begin, k_begin, hk, steps.from * QT, before, lane) &&
-        !odd_queries<T>(a, q_begin, k_begin, hk, behind, end, lane))
+    const int q_begin = a.q_rowptr[st.seq], lq = a.q_rowptr[st.seq + 1] - q_begin;
+    const int k_begin = a.k_rowptr[st.seq], lk = a.k_rowptr[st.seq + 1] - k_begin;
+    const int j0 = st.tile * kKeyRows, wj0 = j0 + 32 * kw;
+    if (wj0 >= lk)
         return;
-    for (uint32_t left = (uint32_t)(redo | (redo >> 32)); left != 0; left &= left - 1)
-        exact_dkv_row<T>(a, q_begin, k_begin, lq, lk, hk, wj0 + __ffs(left) - 1, lane);
+    const int j1 = (j0 + kKeyRows < lk ? j0 + kKeyRows : lk) - 1;
+    const int wj1 = wj0 + 31 < j1 ? wj0 + 31 : j1;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, key = wj0 + (lane & 31);
+    const StepRange steps = window_steps(j0, j1, a.window, lk - lq, lq);
+    const bool has_far = j0 < a.sinks && steps.to < (lq + kStepRows - 1) / kStepRows;
+    const bool first = has_far && key < a.sinks;
+    const int base = q_begin / far_rows + st.seq;      // the sequence's first far run
+    const int run0 = steps.to / (far_rows / kStepRows), run1 = (lq + far_rows - 1) / far_rows;
+    if (t < 32)
+        odd[t] = 0;
+    __syncthreads();
+    bool clean = true;
+    for (int n = wave; n < 8 * DB; n += kPartThreads / 64) {      // dk's registers, then dv's
+        const bool of_v = n >= 4 * DB;
+        const int at = 8 * (of_v ? n - 4 * DB : n) + 4 * (lane >> 5);
+        f32x4 x = f32x4(0.0f);
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p)
+            x += *(const f32x4 *)(sums_at<DU>(sums, unit, parts, p, kw) + 256 * n + 4 * lane);
+        if (first)
+#pragma unroll 4
+            for (int r = run0; r < run1; ++r)
+                x += *(const f32x4 *)(partial_at(a, base + r, hk, key, DP) + (of_v ? DP : 0) + at);
+        if (key > j1 || at >= a.D)
+            continue;
+        if (!of_v)
+            x *= a.scale;
+        const OutRows &out = of_v ? a.dv : a.dk;
+        store4((T *)out.base + (int64_t)(k_begin + key) * out.row_stride + hk * out.head_stride + at, x[0], x[1],
+               x[2], x[3]);
+        clean = clean && finite(x[0]) && finite(x[1]) && finite(x[2]) && finite(x[3]);
+    }
+    if (!clean)
+        atomicOr(&odd[lane & 31], 1);
+    __syncthreads();
+    if (wave == 0)
+        again_dkv<T, DU>(a, Seen{a.window, a.sinks}, __ballot(odd[lane & 31] != 0), steps, wj0, wj1, q_begin, k_begin,
+                         lq, lk, hk, lane);
 }
 
 // One wavefront for each first key of each sequence and key head.
 template <class T, int DP, int DU>
-__global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slots)
+__global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slots, int far_rows)
 {
     const int lane = threadIdx.x;
     const int j = blockIdx.x % a.sinks, hk = blockIdx.x / a.sinks % a.Hkv;
@@ -529,8 +635,8 @@ __global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slot
     const StepRange steps = window_steps(j0, j1, a.window, lk - lq, lq);
     if (steps.to >= (lq + kStepRows - 1) / kStepRows)
         return;                                        // no far part: written already
-    const int base = q_begin / kFarRows + seq;         // the sequence's first far run
-    const int from = steps.to / (kFarRows / kStepRows), to = (lq + kFarRows - 1) / kFarRows;
+    const int base = q_begin / far_rows + seq;         // the sequence's first far run
+    const int from = steps.to / (far_rows / kStepRows), to = (lq + far_rows - 1) / far_rows;
     float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
     auto add = [&](int run) {
         const float *p = partial_at(a, run, hk, j, DP);
@@ -542,6 +648,7 @@ __global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slot
         }
     };
     add(far_slots + seq);
+#pragma unroll 4
     for (int r = from; r < to; ++r)
         add(base + r);
     bool clean = true;
@@ -563,11 +670,53 @@ __global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slot
             sum[1][0], sum[1][1], a.D, lane);
 }
 
+// Whether there are fewer key tiles than twice the CUs.
+bool few_key_tiles(int64_t S, int64_t Tk, int64_t Hkv) { return (Tk / kKeyRows + S) * Hkv < 512; }
+
+// Parts that a key tile's queries are taken in: where there are few tiles, as
+// many as make about two workgroups to a CU, of at least 8 steps each (6 of
+// fp32's longer ones), which pay for the launch that adds them.  (2900 tokens,
+// 16 heads of 128 on 2, all keys seen, bf16: the backward pass 306 us in parts,
+// 730 whole; 2025 tokens, 8 heads of 80 on 4, window 300, fp32: dk and dv 78
+// us with the adding, 99 whole.  In bf16, parts of 6 steps cost 8000 pairs
+// of a window of 64 60 us against 45 whole.)
+int64_t dkv_parts(bool f32, int64_t S, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t window)
+{
+    const int64_t units = (Tk / kKeyRows + S) * Hkv;
+    if (units == 0 || !few_key_tiles(S, Tk, Hkv))
+        return 1;
+    const int64_t reach = window + kKeyRows < Tq ? window + kKeyRows : Tq;
+    const int64_t most = Hq / Hkv * (reach / kStepRows + 1) / (f32 ? 6 : 8);
+    const int64_t parts = (512 + units / 2) / units;
+    return most < 1 ? 1 : (parts < most ? parts : most);
+}
+
+// Queries of a far run: shorter ones where there are few workgroups otherwise.
+// (Dk and dv of the fp32 example: 68 us with 256, 80 with 128, 122 with 512.  990
+// tokens, 4 heads of 64 on 1, window 100, bf16: the backward pass 40 us with 256,
+// 30 with 128, 43 with 512.)
+int64_t far_run_rows(bool f32, int64_t S, int64_t Tk, int64_t Hkv)
+{
+    return few_key_tiles(S, Tk, Hkv) ? (f32 ? 256 : 128) : 512;
+}
+
 // Far runs of a call: none without first keys, or where no position can lie
 // past the window of the first key.
-int64_t far_runs(int64_t S, int64_t Tq, int64_t Tk, int64_t window, int64_t sinks)
+int64_t far_runs(bool f32, int64_t S, int64_t Tq, int64_t Tk, int64_t Hkv, int64_t window, int64_t sinks)
 {
-    return sinks > 0 && window < Tk ? Tq / kFarRows + S : 0;
+    return sinks > 0 && window < Tk ? Tq / far_run_rows(f32, S, Tk, Hkv) + S : 0;
+}
+
+// Floats of the first keys' partial sums, and of the parts' sums.
+int64_t far_floats(int64_t S, int64_t Hkv, int64_t D, int64_t sinks, int64_t runs)
+{
+    return runs == 0 ? 0 : (runs + S) * Hkv * sinks * 2 * (D <= 64 ? 64 : 128);
+}
+
+int64_t parts_floats(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, int64_t parts)
+{
+    const int64_t DU = D <= 64 ? 64 : (D <= 96 ? 96 : 128);
+    return parts == 1 ? 0 : (Tk / kKeyRows + S) * Hkv * parts * kKeyRows * 2 * DU;
 }
 
 template <class T, int DP, int DU, int RG>
@@ -581,8 +730,10 @@ hipError_t launch_dq(const WindowArgs &a, hipStream_t stream)
 template <class T, int DP, int DU>
 hipError_t launch(const WindowArgs &a, hipStream_t stream)
 {
+    constexpr bool f32 = sizeof(T) == 4;
     const int64_t key_slots = a.Tk / kKeyRows + a.S;
-    const int64_t far = far_runs(a.S, a.Tq, a.Tk, a.window, a.sinks);
+    const int64_t far = far_runs(f32, a.S, a.Tq, a.Tk, a.Hkv, a.window, a.sinks);
+    const int far_rows = (int)far_run_rows(f32, a.S, a.Tk, a.Hkv);
     const int64_t far_tiles = far > 0 ? (a.sinks + kKeyRows - 1) / kKeyRows : 0;
     hipError_t err;
     if (a.Tq > 0) {
@@ -591,12 +742,19 @@ hipError_t launch(const WindowArgs &a, hipStream_t stream)
             return err;
     }
     if (a.Tk > 0) {
-        window_dkv<T, DP, DU><<<dim3((uint32_t)((key_slots + far * far_tiles) * a.Hkv)), kAttnThreads, 0, stream>>>(
-            a, (int)key_slots, (int)far, (int)far_tiles);
+        const int64_t parts = dkv_parts(f32, a.S, a.Tq, a.Tk, a.Hq, a.Hkv, a.window);
+        float *sums = a.partial + far_floats(a.S, a.Hkv, a.D, a.sinks, far);
+        window_dkv<T, DP, DU><<<dim3((uint32_t)((key_slots + far * far_tiles) * a.Hkv), (uint32_t)parts), kAttnThreads,
+                                0, stream>>>(a, (int)key_slots, (int)far, (int)far_tiles, far_rows, sums);
         if ((err = hipGetLastError()) != hipSuccess)
             return err;
+        if (parts > 1) {
+            window_dkv_parts<T, DP, DU><<<dim3((uint32_t)(key_slots * a.Hkv), 2), kPartThreads, 0, stream>>>(
+                a, (int)key_slots, far_rows, (int)parts, sums);
+            return hipGetLastError();
+        }
         if (far > 0) {
-            window_dkv_join<T, DP, DU><<<dim3((uint32_t)(a.S * a.Hkv * a.sinks)), 64, 0, stream>>>(a, (int)far);
+            window_dkv_join<T, DP, DU><<<dim3((uint32_t)(a.S * a.Hkv * a.sinks)), 64, 0, stream>>>(a, (int)far, far_rows);
             if ((err = hipGetLastError()) != hipSuccess)
                 return err;
         }
@@ -608,11 +766,12 @@ hipError_t launch(const WindowArgs &a, hipStream_t stream)
 
 int64_t window_bwd_delta_bytes(int64_t Tq, int64_t Hq) { return (Tq * Hq * 4 + 255) / 256 * 256; }
 
-int64_t window_bwd_partial_bytes(int64_t S, int64_t Tq, int64_t Tk, int64_t Hkv, int64_t D,
+int64_t window_bwd_partial_bytes(int64_t S, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
                                  int64_t window, int64_t sinks)
 {
-    const int64_t runs = far_runs(S, Tq, Tk, window, sinks);
-    return runs == 0 ? 0 : (runs + S) * Hkv * sinks * 2 * (D <= 64 ? 64 : 128) * 4;
+    // enough for both types: bf16 has more runs, fp32 more parts
+    return 4 * (far_floats(S, Hkv, D, sinks, far_runs(false, S, Tq, Tk, Hkv, window, sinks)) +
+                parts_floats(S, Tk, Hkv, D, dkv_parts(true, S, Tq, Tk, Hq, Hkv, window)));
 }
 
 hipError_t launch_window_bwd(int dtype, const WindowArgs &a, hipStream_t stream)

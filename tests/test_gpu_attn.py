@@ -101,6 +101,34 @@ def test_many_far_runs(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 72, 128])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (300, 70), (100, 4)])
+def test_few_key_tiles_are_taken_in_parts(dtype, D, window, sinks):
+    """Many queries on few keys: what parts of the queries add to dk and dv is
+    joined, with the far runs of first keys; a query that is no number reaches
+    the keys it sees alone."""
+    check([500, 130, 0, 1], [500, 130, 5, 1], 16, 2, D, dtype, window, sinks, seed=25)
+    check([300, 20], [64, 700], 16, 1, D, dtype, window, sinks, seed=26)
+    ql, at = [500, 130], 400
+    q, k, v, do, qs, ks = operands(ql, ql, 16, 2, D, dtype, seed=27)
+    w = sdl.NO_WINDOW if window is None else window
+    do[at] = 0
+    want = window_ref(q, k, v, qs, ks, w, sinks, None, do)
+    q[at], do[at] = float("nan"), float("nan")
+    a = dict(window=window, sinks=sinks)
+    t = [x.cuda() for x in (q, k, v, do)]
+    o, lse = sdl.window_attention(*t[:3], i32(qs), **a)
+    first = sdl.window_attention_backward(t[3], *t[:3], o, lse, i32(qs), **a)
+    again = sdl.window_attention_backward(t[3], *t[:3], o, lse, i32(qs), **a)
+    for x, y in zip(first, again):
+        assert torch.equal(torch.nan_to_num(x, nan=9.0), torch.nan_to_num(y, nan=9.0))
+    sees = torch.tensor([j <= at and (at - j < w or j < sinks) for j in range(qs[-1])])
+    for n, x in zip(("dk", "dv"), first[1:]):
+        assert bool(torch.isnan(x.cpu()[sees]).all()), n
+        assert_close(x.cpu()[~sees], want[n][~sees], want[n + "_tol"][~sees], n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("window,sinks", [(None, 0), (3000, 70), (700, 4)])
 def test_long_walks_are_split_and_joined(dtype, window, sinks):
     """Few queries behind many keys, beside short sequences; what a masked
