@@ -197,8 +197,8 @@ __device__ inline int renewed(int x)
 }
 
 // A tile of ROWS rows of DP elements, of which the kernels work on the first
-// DU (D of 65 .. 96 lies in rows of 128 and costs three quarters of them: a
-// training step in fp32 with D = 80 takes 201 us, and 249 with all of them).
+// DU (D of 65 .. 96 lies in rows of 128 and costs three quarters of them: of
+// a training step in fp32 with D = 80 that saved 48 of 249 us).
 // The 16-byte pieces of a row are exchanged among themselves by its row number: neighbouring rows differ by
 // a pair of pieces and every eighth one by the order within the pair, so
 // that 8 lanes that read one piece of 8 consecutive rows, 16 lanes that read
