@@ -129,6 +129,45 @@ def test_few_key_tiles_are_taken_in_parts(dtype, D, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_parts_in_a_graph_into_slices(dtype):
+    """The joined gradients as slices of one fused tensor with rows of no
+    sequence around them, in a captured call whose lengths change between
+    replays."""
+    Hq, Hkv, D, ql = 16, 2, 72, [400, 150]
+    q, k, v, do, qs, ks = operands(ql, ql, Hq, Hkv, D, dtype, seed=28, first=6, behind=9)
+    a = dict(window=250, sinks=5)
+    t = [x.cuda() for x in (q, k, v, do)]
+    rp = i32(qs)
+    fused = torch.full((q.shape[0], Hq + 2 * Hkv, D), 7.0, dtype=dtype, device="cuda")
+    grads = fused[:, :Hq], fused[:, Hq:Hq + Hkv], fused[:, Hq + Hkv:]
+    o = torch.full_like(t[0], 7.0)
+    lse = torch.zeros((Hq, q.shape[0]), device="cuda")
+
+    def run():
+        sdl.window_attn_fwd(*t[:3], rp, rp, o, lse, **a)
+        sdl.window_attn_bwd(t[3], *t[:3], o, lse, rp, rp, *grads, **a)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for lengths in (ql, [120, 430], [550, 0], ql):
+        rows = starts(lengths, 6)
+        want = window_ref(q, k, v, rows, rows, 250, 5, None, do)
+        rp.copy_(i32(rows))
+        fused.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, x in zip(("dq", "dk", "dv"), grads):
+            assert_close(x[6:rows[-1]], want[n][6:rows[-1]], want[n + "_tol"][6:rows[-1]], n)
+        assert bool((fused[:6] == 7.0).all()) and bool((fused[rows[-1]:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("window,sinks", [(None, 0), (3000, 70), (700, 4)])
 def test_long_walks_are_split_and_joined(dtype, window, sinks):
     """Few queries behind many keys, beside short sequences; what a masked
