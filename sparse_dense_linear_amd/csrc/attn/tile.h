@@ -474,24 +474,34 @@ struct Parked {
     }
 };
 
-// COUNT matrix instructions in a row, use(i, read(i)), with the LDS reads of
-// the next AHEAD of them under way.  Left to itself the compiler keeps one
-// operand's registers and waits out the latency of LDS before every
-// instruction, where registers are scarce; the order here is therefore fixed.
-template <int COUNT, int AHEAD, class Read, class Use>
-__device__ inline void chain(Read read, Use use)
+// The compiler moves no instruction across this point.
+__host__ __device__ inline void keep_order()
 {
-    decltype(read(0)) f[AHEAD];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-        f[i] = read(i);
+#ifdef __HIP_DEVICE_COMPILE__
     __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+// COUNT matrix instructions in a row, use(i, read(i)), with the LDS reads of
+// the next AHEAD of them under way (of all of them, where they are no more).
+// Left to itself the compiler keeps one operand's registers and waits out the
+// latency of LDS before every instruction, where registers are scarce; the
+// order here is therefore fixed.
+template <int COUNT, int AHEAD, class Read, class Use>
+__host__ __device__ inline void chain(Read read, Use use)
+{
+    constexpr int kAhead = AHEAD < COUNT ? AHEAD : COUNT;
+    decltype(read(0)) f[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        f[i] = read(i);
+    keep_order();
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
-        use(i, f[i % AHEAD]);
-        if (i + AHEAD < COUNT)
-            f[i % AHEAD] = read(i + AHEAD);
-        __builtin_amdgcn_sched_barrier(0);
+        use(i, f[i % kAhead]);
+        if (i + kAhead < COUNT)
+            f[i % kAhead] = read(i + kAhead);
+        keep_order();
     }
 }
 
