@@ -64,16 +64,19 @@ __device__ inline int first_key(const Unit &u, int n)
     return (n < u.first_tiles ? n : u.band + n - u.first_tiles) * u.tile_keys;
 }
 
-// A key of tile n that may be read: tiles reach over keys that no draft
-// sees (behind the window their pages may have been given away), which
-// repeat the nearest key that is seen.
-__device__ inline int readable(const TreeArgs &a, const Unit &u, int n, int j)
+// Whether a key may be read: tiles reach over keys that no draft sees (behind
+// the window their pages may have been given away).  Their rows are zero in
+// LDS: what a masked pair multiplies by its weight of 0 is then no row that is
+// seen elsewhere and may be infinite.
+__device__ inline bool readable(const TreeArgs &a, const Unit &u, int j)
 {
-    if (j >= u.end)
-        return u.end - 1;
-    if (j < u.low && j >= a.sinks)
-        return n < u.first_tiles ? a.sinks - 1 : u.low;
-    return j;
+    return j < u.end && (j >= u.low || j < a.sinks);
+}
+
+// Every key of j0 .. j1 may be read.
+__device__ inline bool all_readable(const TreeArgs &a, const Unit &u, int j0, int j1)
+{
+    return j1 < u.end && (j0 >= u.low || j1 < a.sinks);
 }
 
 // Which keys draft t sees, and from where.
@@ -405,25 +408,41 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_at
         const int32_t *table = a.table + (int64_t)seq * a.table_stride;
         const T *kp = (const T *)a.k_pages + hk * a.head_stride, *vp = (const T *)a.v_pages + hk * a.head_stride;
         u32x4 pk[kPiecesPer], pv[kPiecesPer];
-        int id = 0, in_page = 0;
+        int id = 0, in_page = 0;               // in_page < 0: a row that may not be read
         auto find_row = [&](int n) {
-            const int j = readable(a, u, n, first_key(u, n) + t);
-            const int p = j / a.page;
-            in_page = j - p * a.page;
-            id = table[p];
+            const int j = first_key(u, n) + t;
+            in_page = -1;
+            if (readable(a, u, j)) {
+                const int p = j / a.page;
+                in_page = j - p * a.page;
+                id = table[p];
+            }
         };
         auto keep_row = [&](int n) {
-            place_of[n & 1][t] = (int64_t)id * a.page_stride + (int64_t)in_page * a.row_stride;
+            place_of[n & 1][t] = in_page < 0 ? -1 : (int64_t)id * a.page_stride + (int64_t)in_page * a.row_stride;
         };
         auto fetch = [&](int n) {
+            const int j0 = first_key(u, n);
+            auto load = [&](bool whole) {
 #pragma unroll
-            for (int i = 0; i < kPiecesPer; ++i) {
-                const int m = t + i * kAttnThreads, p = m % Tl::kPieces;
-                const int d = p * Tl::kElems < a.D ? p * Tl::kElems : a.D - Tl::kElems;
-                const int64_t off = place_of[n & 1][m / Tl::kPieces] + d;
-                pk[i] = load_once<C == 16>((const u32x4 *)(kp + off));
-                pv[i] = load_once<C == 16>((const u32x4 *)(vp + off));
-            }
+                for (int i = 0; i < kPiecesPer; ++i) {
+                    const int m = t + i * kAttnThreads, p = m % Tl::kPieces;
+                    const int d = p * Tl::kElems < a.D ? p * Tl::kElems : a.D - Tl::kElems;
+                    const int64_t at = place_of[n & 1][m / Tl::kPieces];
+                    if (!whole) {
+                        pk[i] = u32x4(0);
+                        pv[i] = u32x4(0);
+                    }
+                    if (whole || at >= 0) {
+                        pk[i] = load_once<C == 16>((const u32x4 *)(kp + at + d));
+                        pv[i] = load_once<C == 16>((const u32x4 *)(vp + at + d));
+                    }
+                }
+            };
+            if (all_readable(a, u, j0, j0 + kTileKeys - 1))
+                load(true);
+            else
+                load(false);
         };
         if (t < kTileKeys) {
             find_row(n0);

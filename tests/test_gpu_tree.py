@@ -200,6 +200,32 @@ def test_masked_places_may_hold_anything(dtype):
         assert not bool(torch.isfinite(o[2]).all())
 
 
+@BOTH
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("drafts", [1, 40])
+def test_an_infinite_value_beside_masked_keys(dtype, D, drafts):
+    """The last first key, and the first and last key of the window, hold an
+    infinite value: its element of the output is infinite for the drafts that
+    see it, and no masked key of the same tile makes it no number."""
+    ctx, window, sinks, page, d = 700, 41, 3, 16, 5
+    for at in (sinks - 1, ctx + drafts - window, ctx + drafts - 1):
+        cache = Cache([ctx + drafts], page, 1, D, dtype, 31)
+        cache.rows_v[0][at, 0, d] = float("inf")
+        cache.v[cache.table[0][at // page], at % page, 0, d] = float("inf")
+        q = torch.randn(drafts, 4, D, generator=torch.Generator().manual_seed(32)).to(dtype)
+        k, v, table = cache.on_gpu()
+        o, lse = sdl.tree_attention(q.cuda(), k, v, table, i32([ctx]), i32([0, drafts]), window=window, sinks=sinks)
+        seen = chain_seen(ctx, drafts, window, sinks)
+        sees = seen[:, at]
+        finite = cache.rows_v[0][:, 0].double()
+        finite[at, d] = 0
+        for h in range(4):
+            f = head_forward(q[:, h].double(), cache.rows_k[0][:, 0].double(), finite, seen, D ** -0.5, dtype)
+            f["o"][sees, d] = float("inf")
+            assert_close(o[:, h], f["o"], 2 * f["o_tol"], f"o, key {at}")
+            assert_close(lse[h], f["lse"], 2 * f["lse_tol"], "lse")
+
+
 def test_strided_pools_and_queries():
     """Pools that are one layer of a larger tensor, queries cut from a fused
     tensor."""
