@@ -33,13 +33,15 @@ __device__ inline float wave_sum(float x)
     return x;
 }
 
-// Whether one of rows from .. to - 1 (row(j): where it starts) has an element
-// that is not finite.
-template <class T, class Row>
-__device__ inline bool any_odd(Row row, int from, int to, int D, int lane)
+// Whether one of rows from .. to - 1 (row(j): where it starts) that counts(j)
+// lets through has an element that is not finite.
+template <class T, class Row, class Counts>
+__device__ inline bool any_odd(Row row, Counts counts, int from, int to, int D, int lane)
 {
     bool odd = false;
     for (int j = from + lane; j < to; j += 64) {
+        if (!counts(j))
+            continue;
         const T *p = row(j);
         for (int d = 0; d < D; d += 8) {
             const Frag<T> x = load8(p + d);
@@ -49,6 +51,12 @@ __device__ inline bool any_odd(Row row, int from, int to, int D, int lane)
         }
     }
     return __any(odd);
+}
+
+template <class T, class Row>
+__device__ inline bool any_odd(Row row, int from, int to, int D, int lane)
+{
+    return any_odd<T>(row, [](int) { return true; }, from, to, D, lane);
 }
 
 // Whether every lane's share of a row has become NaN.

@@ -21,6 +21,7 @@
 // for the join.  Drafts of up to 64 tokens with 8 heads on one are bound by
 // latency, two workgroups to a CU: 23 GFLOP in 76 us and 12 for the join.
 #include "ops.h"
+#include "draft.h"
 #include "exact.h"
 #include "tile.h"
 #include "spmm.h"
@@ -64,48 +65,64 @@ __device__ inline int first_key(const Unit &u, int n)
     return (n < u.first_tiles ? n : u.band + n - u.first_tiles) * u.tile_keys;
 }
 
-// Whether a key may be read: tiles reach over keys that no draft sees (behind
-// the window their pages may have been given away).  Their rows are zero in
-// LDS: what a masked pair multiplies by its weight of 0 is then no row that is
-// seen elsewhere and may be infinite.
-__device__ inline bool readable(const TreeArgs &a, const Unit &u, int j)
+// f of all lanes' x, in each lane; f takes them in any order, f(x, x) is x.
+template <class F>
+__device__ inline int wave_of(int x, F f)
 {
-    return j < u.end && (j >= u.low || j < a.sinks);
+    // within a row of 16 lanes, turned by 8, 4, 2 and 1
+    x = f(x, __builtin_amdgcn_mov_dpp(x, 0x128, 15, 15, true));
+    x = f(x, __builtin_amdgcn_mov_dpp(x, 0x124, 15, 15, true));
+    x = f(x, __builtin_amdgcn_mov_dpp(x, 0x122, 15, 15, true));
+    x = f(x, __builtin_amdgcn_mov_dpp(x, 0x121, 15, 15, true));
+    auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = f((int)r[0], (int)r[1]);
+    r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return f((int)r[0], (int)r[1]);
 }
 
-// Every key of j0 .. j1 may be read.
-__device__ inline bool all_readable(const TreeArgs &a, const Unit &u, int j0, int j1)
-{
-    return j1 < u.end && (j0 >= u.low || j1 < a.sinks);
-}
-
-// Which keys draft t sees, and from where.
-struct DraftSeen {
-    int ctx, drafts, window, sinks;
-    int pos;              // of the draft
-    uint64_t mask;
-    const int *place;     // positions of the drafts' keys (null: a chain)
-    __device__ bool operator()(int j) const
-    {
-        if (j < ctx || place == nullptr)
-            return j <= pos && (pos - j < window || j < sinks);
-        const int d = j - ctx;
-        if (d >= drafts || d >= 64 || !(mask >> d & 1))
-            return false;
-        return pos - place[d] < window || place[d] < sinks;
-    }
+// What all drafts of a sequence see together, and where each of them stands
+// (in LDS).
+struct Drafts {
+    int place[64], named[64], low;
 };
 
-__device__ inline uint64_t draft_mask(const TreeArgs &a, int q_begin, int drafts, int t)
+// By one wavefront; a.tree is not null.
+__device__ inline void find_drafts(const TreeArgs &a, const Unit &u, int lane, Drafts &to)
 {
-    const uint64_t m = a.tree[q_begin + t];
-    return drafts < 64 ? m & (((uint64_t)1 << drafts) - 1) : m;
+    const uint64_t *masks = a.tree + u.q_begin;
+    int low = u.ctx;
+    uint64_t named = 0;
+    int place = 0;
+    for (int t = lane; t < u.drafts; t += 64) {
+        const int at = count_draft(masks, u.ctx, u.drafts, a.window, a.sinks, t, low, named);
+        place = t < 64 ? at : place;
+    }
+    low = wave_of(low, [](int x, int y) { return x < y ? x : y; });
+    auto either = [](int x, int y) { return x | y; };
+    const uint32_t named0 = wave_of((int)named, either), named1 = wave_of((int)(named >> 32), either);
+    if (lane < u.drafts)
+        to.place[lane] = place;
+    to.named[lane] = (lane < 32 ? named0 : named1) >> (lane & 31) & 1;
+    if (lane == 0)
+        to.low = low;
 }
 
-__device__ inline int draft_place(int ctx, uint64_t mask)
+// Tiles reach over keys that no draft sees.  Those are zero in LDS: what a
+// masked pair multiplies by its weight of 0 is then no row that is seen
+// elsewhere and may be infinite.
+__device__ inline SeenRows seen_rows(const TreeArgs &a, const Unit &u, const Drafts &drafts)
 {
-    const int n = __popcll(mask);
-    return ctx + (n > 1 ? n - 1 : 0);
+    if (a.tree == nullptr)
+        return {u.ctx, u.end, u.low, a.sinks, nullptr};
+    return {u.ctx, u.end, drafts.low, a.sinks, drafts.named};
+}
+
+// Whether that need not be asked, as every key of j0 .. j1 is seen whatever the
+// masks are: no draft stands further than 63 behind the context.
+__device__ inline bool all_seen(const TreeArgs &a, const Unit &u, int j0, int j1)
+{
+    return a.tree == nullptr ? j1 < u.end && (j0 >= u.low || j1 < a.sinks)
+                             : j1 < u.ctx && (j0 >= u.low + 63 || j1 < a.sinks);
 }
 
 // Row j of a pool, and whether a row that some draft does not see, but that
@@ -124,11 +141,14 @@ struct PoolRows {
 };
 
 template <class T>
-__device__ bool odd_unseen(const Unit &u, const PoolRows<T> &k, const PoolRows<T> &v, int D, int lane)
+__device__ bool odd_unseen(const Unit &u, const SeenRows &rows, const PoolRows<T> &k, const PoolRows<T> &v, int D,
+                           int lane)
 {
     const int edge = u.low + u.drafts < u.ctx ? u.low + u.drafts : u.ctx;
-    return any_odd<T>(k, u.low, edge, D, lane) || any_odd<T>(v, u.low, edge, D, lane) ||
-           any_odd<T>(k, u.ctx, u.end, D, lane) || any_odd<T>(v, u.ctx, u.end, D, lane);
+    auto odd = [&](const PoolRows<T> &x) {
+        return any_odd<T>(x, rows.low, edge, D, lane) || any_odd<T>(x, rows, u.ctx, u.end, D, lane);
+    };
+    return odd(k) || odd(v);
 }
 
 // The spans: `workers` of them (at most one for each tile), span w from
@@ -268,7 +288,7 @@ __device__ inline void finish(const TreeArgs &a, int64_t token, int head, int p,
 // positions.
 template <class T>
 __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, int hk, int first, int count,
-                                    const int *redo, const int *place, int wave, int lane)
+                                    const int *redo, const Drafts &drafts, int wave, int lane)
 {
     const int group = a.Hq / a.Hkv;
     bool some = false;
@@ -279,7 +299,7 @@ __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, i
     const int32_t *table = a.table + (int64_t)seq * a.table_stride;
     const PoolRows<T> key{a, table, (const T *)a.k_pages + hk * a.head_stride};
     const PoolRows<T> val{a, table, (const T *)a.v_pages + hk * a.head_stride};
-    const bool odd = odd_unseen<T>(u, key, val, a.D, lane);
+    const bool odd = odd_unseen<T>(u, seen_rows(a, u, drafts), key, val, a.D, lane);
     for (int lr = wave; lr < count; lr += 4) {
         const int why = redo[lr];
         if (why < (odd ? 1 : 2))               // uniform over the wavefront
@@ -291,9 +311,9 @@ __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, i
         seen.drafts = u.drafts;
         seen.window = a.window;
         seen.sinks = a.sinks;
-        seen.mask = a.tree != nullptr ? draft_mask(a, u.q_begin, u.drafts, t) : 0;
+        seen.mask = a.tree != nullptr ? draft_mask(a.tree[u.q_begin + t], u.drafts) : 0;
         seen.pos = a.tree != nullptr ? draft_place(u.ctx, seen.mask) : u.ctx + t;
-        seen.place = a.tree != nullptr ? place : nullptr;
+        seen.place = a.tree != nullptr ? drafts.place : nullptr;
         exact_row<T>((const T *)a.q + token * a.q_row + head * a.q_head, key, val, seen,
                      a.sinks < u.low ? a.sinks : u.low, u.low, u.end, a.D, a.scale * kLog2e,
                      (T *)a.o + (token * a.Hq + head) * a.D, a.lse + head * a.Tq + token, why == 1, lane);
@@ -334,7 +354,7 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_at
     constexpr int kPiecesPer = kTileKeys * Tl::kPieces / kAttnThreads;
     constexpr int kBytes = 2 * Tl::kBytes > 4 * Out::kBytes ? 2 * Tl::kBytes : 4 * Out::kBytes;
     __shared__ __align__(16) char lds[kBytes];
-    __shared__ int place[64];
+    __shared__ Drafts drafts;
     __shared__ float tops[4][C], totals[4][C];
     __shared__ int redo[RB];
     __shared__ int64_t place_of[2][kTileKeys];     // of a tile's rows, in the pools
@@ -371,12 +391,12 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_at
         const int n1 = stop - at < u.tiles - n0 ? n0 + (int)(stop - at) : u.tiles;
         const int rows = u.drafts * group;
 
-        // the drafts' positions, for the tiles that reach past the context
+        // the drafts' positions, and what they see together
         __syncthreads();
-        if (a.tree != nullptr && t < 64 && t < u.drafts)
-            place[t] = draft_place(u.ctx, draft_mask(a, u.q_begin, u.drafts, t));
         if (t < RB)
             redo[t] = 0;
+        if (wave == 3 && a.tree != nullptr)    // (the first ones find the rows)
+            find_drafts(a, u, lane, drafts);
 
         // this lane's query
         const int r = block * RB + C * rg + lane % C;
@@ -386,9 +406,9 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_at
         seen.drafts = u.drafts;
         seen.window = a.window;
         seen.sinks = a.sinks;
-        seen.mask = a.tree != nullptr ? draft_mask(a, u.q_begin, u.drafts, token) : 0;
+        seen.mask = a.tree != nullptr ? draft_mask(a.tree[u.q_begin + token], u.drafts) : 0;
         seen.pos = a.tree != nullptr ? draft_place(u.ctx, seen.mask) : u.ctx + token;
-        seen.place = a.tree != nullptr ? place : nullptr;
+        seen.place = a.tree != nullptr ? drafts.place : nullptr;
         const T *q = (const T *)a.q + (int64_t)(u.q_begin + token) * a.q_row + head * a.q_head;
         Frag<T> qf[STEPS];
 #pragma unroll
@@ -408,11 +428,12 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_at
         const int32_t *table = a.table + (int64_t)seq * a.table_stride;
         const T *kp = (const T *)a.k_pages + hk * a.head_stride, *vp = (const T *)a.v_pages + hk * a.head_stride;
         u32x4 pk[kPiecesPer], pv[kPiecesPer];
-        int id = 0, in_page = 0;               // in_page < 0: a row that may not be read
+        int id = 0, in_page = 0;               // in_page < 0: a row that is not read
+        auto whole = [&](int n) { return all_seen(a, u, first_key(u, n), first_key(u, n) + kTileKeys - 1); };
         auto find_row = [&](int n) {
             const int j = first_key(u, n) + t;
             in_page = -1;
-            if (readable(a, u, j)) {
+            if (whole(n) || seen_rows(a, u, drafts)(j)) {
                 const int p = j / a.page;
                 in_page = j - p * a.page;
                 id = table[p];
@@ -422,28 +443,33 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_at
             place_of[n & 1][t] = in_page < 0 ? -1 : (int64_t)id * a.page_stride + (int64_t)in_page * a.row_stride;
         };
         auto fetch = [&](int n) {
-            const int j0 = first_key(u, n);
-            auto load = [&](bool whole) {
+            const int tt = renewed(t);
+            int64_t at[kPiecesPer];            // all of them before the loads, which then go out together
+#pragma unroll
+            for (int i = 0; i < kPiecesPer; ++i)
+                at[i] = place_of[n & 1][(tt + i * kAttnThreads) / Tl::kPieces];
+            auto load = [&](bool all) {
 #pragma unroll
                 for (int i = 0; i < kPiecesPer; ++i) {
-                    const int m = t + i * kAttnThreads, p = m % Tl::kPieces;
+                    const int p = (tt + i * kAttnThreads) % Tl::kPieces;
                     const int d = p * Tl::kElems < a.D ? p * Tl::kElems : a.D - Tl::kElems;
-                    const int64_t at = place_of[n & 1][m / Tl::kPieces];
-                    if (!whole) {
+                    if (!all) {
                         pk[i] = u32x4(0);
                         pv[i] = u32x4(0);
                     }
-                    if (whole || at >= 0) {
-                        pk[i] = load_once<C == 16>((const u32x4 *)(kp + at + d));
-                        pv[i] = load_once<C == 16>((const u32x4 *)(vp + at + d));
+                    if (all || at[i] >= 0) {
+                        pk[i] = load_once<C == 16>((const u32x4 *)(kp + at[i] + d));
+                        pv[i] = load_once<C == 16>((const u32x4 *)(vp + at[i] + d));
                     }
                 }
             };
-            if (all_readable(a, u, j0, j0 + kTileKeys - 1))
+            if (whole(n))
                 load(true);
             else
                 load(false);
         };
+        if (a.tree != nullptr && !(whole(n0) && (n0 + 1 >= n1 || whole(n0 + 1))))
+            __syncthreads();                   // what the drafts see is there
         if (t < kTileKeys) {
             find_row(n0);
             keep_row(n0);
@@ -570,7 +596,7 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_at
         }
         __syncthreads();
         if (done)
-            finish_again<T>(a, u, seq, hk, block * RB, RB, redo, place, wave, lane);
+            finish_again<T>(a, u, seq, hk, block * RB, RB, redo, drafts, wave, lane);
         at += n1 - n0;
         ++piece_no;
     }
@@ -585,7 +611,8 @@ constexpr int kJoinRows = 16;      // query rows of a joining workgroup
 template <class T, int DP, int DU>
 __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int numbers)
 {
-    __shared__ int redo[kJoinRows], place[64];
+    __shared__ int redo[kJoinRows];
+    __shared__ Drafts drafts;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int RB = a.block_rows, group = a.Hq / a.Hkv;
     const int hk = blockIdx.x / numbers, number = blockIdx.x % numbers;
@@ -618,8 +645,6 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int number
 
     if (t < kJoinRows)
         redo[t] = 0;
-    if (a.tree != nullptr && t < 64 && t < u.drafts)
-        place[t] = draft_place(u.ctx, draft_mask(a, u.q_begin, u.drafts, t));
     __syncthreads();
     constexpr int kOutPieces = DU / 4;
     for (int m = t; m < kJoinRows * kOutPieces; m += kAttnThreads) {
@@ -648,7 +673,12 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int number
         finish<T>(a, u.q_begin + r / group, hk * group + r % group, p, best, sum, o, redo + lr);
     }
     __syncthreads();
-    finish_again<T>(a, u, seq, hk, block * RB + row0, kJoinRows, redo, place, wave, lane);
+    if (!__any(lane < kJoinRows && redo[lane] != 0))    // the same in all wavefronts
+        return;
+    if (wave == 0 && a.tree != nullptr)
+        find_drafts(a, u, lane, drafts);
+    __syncthreads();
+    finish_again<T>(a, u, seq, hk, block * RB + row0, kJoinRows, redo, drafts, wave, lane);
 }
 
 template <class T, int DP, int DU>

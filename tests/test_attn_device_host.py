@@ -25,3 +25,8 @@ def run_program(tmp_path, name):
 @pytest.mark.skipif(not os.path.exists(HIPCC), reason="needs hipcc")
 def test_a_chain_reads_its_own_operands_only(tmp_path):
     assert "chain: ok" in run_program(tmp_path, "attn_chain")
+
+
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="needs hipcc")
+def test_rows_of_drafts_that_may_be_read(tmp_path):
+    assert "drafts: ok" in run_program(tmp_path, "attn_draft")

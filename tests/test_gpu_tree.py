@@ -226,6 +226,27 @@ def test_an_infinite_value_beside_masked_keys(dtype, D, drafts):
             assert_close(lse[h], f["lse"], 2 * f["lse_tol"], "lse")
 
 
+@BOTH
+def test_pages_that_no_mask_names_are_not_read(dtype):
+    """Pages that no draft sees hold nonsense in the table, whatever the reason."""
+    # both drafts stand at ctx + 1: key ctx - window + 1, the last of page 24, is behind them
+    dead = [(0, p) for p in range(1, 25)]
+    check([500], [2], 4, 2, 64, dtype, 16, 102, 4, seed=35, dead=dead, masks=[[3, 3]])
+    check([500], [2], 4, 2, 64, dtype, 16, 102, 0, seed=35, dead=dead + [(0, 0)], masks=[[3, 3]])
+    # drafts past the 64th are seen by none
+    bits = [(0x9E3779B97F4A7C15 * (i + 1)) & (1 << 64) - 1 for i in range(150)]
+    check([60], [150], 2, 1, 64, dtype, 16, None, 0, seed=36, dead=[(0, p) for p in range(8, 14)], masks=[bits])
+    # drafts that no mask names
+    check([64, 30], [40, 3], 2, 1, 128, dtype, 16, None, 0, seed=37, dead=[(0, 5), (0, 6)],
+          masks=[[b & 0xffff for b in bits[:40]], [1, 3, 7]])
+    # named drafts that the window hides: the last one stands 39 behind them
+    check([64], [40], 2, 1, 64, dtype, 16, 2, 0, seed=38, dead=[(0, p) for p in (0, 1, 2, 4, 5)],
+          masks=[[0] * 39 + [(1 << 40) - 1]])
+    # nothing is seen
+    check([100, 20], [3, 1], 2, 1, 64, dtype, 16, 1, 0, seed=39, dead=[(0, p) for p in range(7)],
+          masks=[[0, 0, 0], [1]])
+
+
 def test_strided_pools_and_queries():
     """Pools that are one layer of a larger tensor, queries cut from a fused
     tensor."""
