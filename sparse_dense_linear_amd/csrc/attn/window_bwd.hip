@@ -54,9 +54,11 @@ __device__ GradRows<T> grad_rows(const WindowArgs &a, int q_begin, int k_begin, 
     return r;
 }
 
-// lse in base 2.  A query that sees nothing has -infinity, which against a
-// masked score would be no number; any finite value gives it weights of 0.
-__device__ inline float base2(float lse) { return lse == SDL_NEG_INF ? 0.0f : lse * kLog2e; }
+// lse in base 2, of a query at position pos.  One that sees nothing (pos < 0)
+// has -infinity, which against a masked score would be no number; any finite
+// value gives it weights of 0.  One whose scores are all -infinity has the
+// same sum, and its weights are no numbers.
+__device__ inline float base2(float lse, int pos) { return pos < 0 ? 0.0f : lse * kLog2e; }
 
 // ------------------------------------------------------------------- dq
 
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
         if (qi <= i1 && half == 0 && ks == 0)
             a.delta[(int64_t)head * a.Tq + q_begin + qi] = delta;
     }
-    const float lse2 = base2(r.lse[row]);
+    const float lse2 = base2(r.lse[row], row + shift);
 
     f32x16 dQ[DB];
 #pragma unroll
@@ -408,7 +410,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
         g_in.load(gt, r.dout, first, lq - 1, wave);
         if (t < 2 * QT) {
             const int i = first + (t & (QT - 1)) < lq ? first + (t & (QT - 1)) : lq - 1;
-            carried = t < QT ? base2(r.lse[i]) : r.delta[i];
+            carried = t < QT ? base2(r.lse[i], i + shift) : r.delta[i];
         }
         if (++next_step == steps.to) {
             next_step = steps.from;

@@ -350,6 +350,40 @@ def test_a_lost_training_step(dtype, D):
     assert bool(torch.isfinite(dv).all()) and bool(torch.isfinite(dk[:, 1]).all())
 
 
+SIZES = pytest.mark.parametrize("D", [40, 64, 96, 128])
+#: query heads on one key head: dk and dv of a key tile in one piece, and in parts
+PARTS = pytest.mark.parametrize("Hq", [2, 16], ids=["whole", "parts"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@SIZES
+@PARTS
+def test_scores_that_are_all_minus_infinity(dtype, D, Hq):
+    """Queries 0 .. 30 see only keys whose scores are -infinity: their weights
+    are no numbers, and so is all that takes part in them.  For the others
+    those keys have weight 0, which leaves attention of queries 31 .. 63 over
+    keys 95 .. 127."""
+    c = 7
+    q, k, v, do, qs, ks = operands([64], [128], Hq, 1, D, dtype, seed=40)
+    q[:, :, c] = q[:, :, c].abs() + 0.5
+    want = window_ref(q[31:], k[95:], v[95:], [0, 33], [0, 33], sdl.NO_WINDOW, 0, None, do[31:])
+    k[:95, :, c] = -math.inf
+    t = [x.cuda() for x in (q, k, v, do)]
+    o, lse = sdl.window_attention(*t[:3], i32(qs), i32(ks))
+    dq, dk, dv = (x.cpu() for x in sdl.window_attention_backward(t[3], *t[:3], o, lse, i32(qs), i32(ks)))
+    o, lse = o.cpu(), lse.cpu()
+    assert bool(torch.isneginf(lse[:, :31]).all())
+    for name, x in (("o", o[:31]), ("dq", dq[:31]), ("dk", dk[:95]), ("dv", dv[:95])):
+        assert bool(torch.isnan(x).all()), name
+    assert bool(torch.isnan(dq[31:, :, c]).all())            # 0 times the infinite element
+    assert_close(o[31:], want["o"], want["o_tol"], "o")
+    assert_close(lse[:, 31:], want["lse"], want["lse_tol"], "lse")
+    rest = [d for d in range(D) if d != c]
+    assert_close(dq[31:][:, :, rest], want["dq"][:, :, rest], want["dq_tol"][:, :, rest], "dq")
+    assert_close(dk[95:], want["dk"], want["dk_tol"], "dk")
+    assert_close(dv[95:], want["dv"], want["dv_tol"], "dv")
+
+
 def test_large_scores():
     """Scores far apart: weights of exactly 0 and 1, no overflow."""
     n = 100
