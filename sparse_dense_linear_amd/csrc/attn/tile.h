@@ -528,42 +528,53 @@ struct Seen {
     }
 };
 
-// Scores of one 32 x 32 result whose pair is not seen become -infinity.  Lane:
-// one query at position p; rows: keys from j0 on.  (renewed() keeps the
-// comparisons on the caller's side of its branch: most tiles lie within the
-// window and skip them.)
-__device__ inline void mask_keys(f32x16 &x, const Seen &seen, int p, int j0, int half)
+// Scores of one 32 x 32 result whose pair is not seen become -infinity, and
+// its elements of `zeroed` 0: what the weight of 0 multiplies later must not be
+// an infinity.  Lane: one query at position p; rows: keys from j0 on.
+// (renewed() keeps the comparisons on the caller's side of its branch: most
+// tiles lie within the window and skip them.)
+template <class... Zeroed>
+__device__ inline void mask_keys(const Seen &seen, int p, int j0, int half, f32x16 &x, Zeroed &...zeroed)
 {
     const int t = renewed(p - j0 - 4 * half);
     if (j0 >= seen.sinks) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-            if ((uint32_t)(t - (8 * (r >> 2) + (r & 3))) >= (uint32_t)seen.window)
+            if ((uint32_t)(t - (8 * (r >> 2) + (r & 3))) >= (uint32_t)seen.window) {
                 x[r] = SDL_NEG_INF;
+                ((zeroed[r] = 0.0f), ...);
+            }
     } else {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-            if (!seen(p, p - t + 8 * (r >> 2) + (r & 3)))
+            if (!seen(p, p - t + 8 * (r >> 2) + (r & 3))) {
                 x[r] = SDL_NEG_INF;
+                ((zeroed[r] = 0.0f), ...);
+            }
     }
 }
 
 // The same with one key a lane, rows: queries from position p0 on, of which
 // `count` exist.
-__device__ inline void mask_queries(f32x16 &x, const Seen &seen, int key, int p0, int count, int half)
+__device__ inline void mask_queries(const Seen &seen, int key, int p0, int count, int half, f32x16 &x,
+                                    f32x16 &zeroed)
 {
     const int t = renewed(p0 - key + 4 * half);
     const uint32_t limit = key < seen.sinks ? 0x7fffffff : seen.window;
 #pragma unroll
     for (int r = 0; r < 16; ++r)
-        if ((uint32_t)(t + 8 * (r >> 2) + (r & 3)) >= limit)
+        if ((uint32_t)(t + 8 * (r >> 2) + (r & 3)) >= limit) {
             x[r] = SDL_NEG_INF;
+            zeroed[r] = 0.0f;
+        }
     if (count < 32) {
         const int left = renewed(count - 4 * half);
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-            if (8 * (r >> 2) + (r & 3) >= left)
+            if (8 * (r >> 2) + (r & 3) >= left) {
                 x[r] = SDL_NEG_INF;
+                zeroed[r] = 0.0f;
+            }
     }
 }
 

@@ -160,7 +160,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
                         x = mma(f, qf[i >> 1], x);
                 });
             if (!seen.all(wp0, wp1, j0, j0 + 31))
-                mask_keys(x, seen, pos, j0, half);
+                mask_keys(seen, pos, j0, half, x, dp);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c2, -lse2)) * (dp[i] - delta);
@@ -466,7 +466,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
                     x = mma(f, kf[i >> 1], x);
             });
         if (last < first + 31 || !seen.all(first + shift, last + shift, wj0, wj0 + 31))
-            mask_queries(x, seen, key, first + shift, last + 1 - first, half);
+            mask_queries(seen, key, first + shift, last + 1 - first, half, x, dp);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const f32x4 l4 = *(const f32x4 *)(stat + 32 * qw + 8 * g + 4 * half);

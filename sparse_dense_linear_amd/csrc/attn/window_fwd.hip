@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? (RG == 4 ? 3 : 2) : 
         if (!seen.all(wp0, wp1, j0, j1)) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-                mask_keys(x[b], seen, pos, j0 + 32 * b, half);
+                mask_keys(seen, pos, j0 + 32 * b, half, x[b]);
         }
         float most = max_of(x[0]);
 #pragma unroll

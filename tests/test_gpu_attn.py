@@ -384,6 +384,28 @@ def test_scores_that_are_all_minus_infinity(dtype, D, Hq):
     assert_close(dv[95:], want["dv"], want["dv_tol"], "dv")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@SIZES
+@PARTS
+@pytest.mark.parametrize("value", [math.nan, math.inf, 3e38])
+def test_a_key_that_no_query_sees_has_no_gradient(dtype, D, Hq, value):
+    """Key 352 is just behind the window of the first query, in the tiles of
+    keys that are seen: whatever it holds, its gradients are zero and the others
+    do not change.  (3e38: finite, but its products are not.)"""
+    at, a = 352, dict(window=48, sinks=2)
+    q, k, v, do, qs, ks = operands([100], [500], Hq, 1, D, dtype, seed=41)
+    want = window_ref(q, k, v, qs, ks, 48, 2, None, do)
+    k[at], v[at] = value, value
+    t = [x.cuda() for x in (q, k, v, do)]
+    o, lse = sdl.window_attention(*t[:3], i32(qs), i32(ks), **a)
+    got = sdl.window_attention_backward(t[3], *t[:3], o, lse, i32(qs), i32(ks), **a)
+    assert_close(o, want["o"], want["o_tol"], "o")
+    assert_close(lse, want["lse"], want["lse_tol"], "lse")
+    for name, x in zip(("dq", "dk", "dv"), got):
+        assert_close(x, want[name], want[name + "_tol"], name)
+    assert not bool(got[1][at].any()) and not bool(got[2][at].any())
+
+
 def test_large_scores():
     """Scores far apart: weights of exactly 0 and 1, no overflow."""
     n = 100
