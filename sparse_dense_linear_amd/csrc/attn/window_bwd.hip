@@ -312,22 +312,24 @@ __device__ inline float *sums_at(float *sums, int unit, int parts, int part, int
 
 // Computes rows of keys again that came out non-finite, where that is called
 // for: bits 0 .. 31 (and the same again from 32) of `redo` are keys wj0 .. wj1;
-// steps: the queries that the tile met.
+// steps: the queries that the tile met; has_far: for first keys, far runs too.
 template <class T, int DU>
 __device__ inline void again_dkv(const WindowArgs &a, const Seen &seen, uint64_t redo, const StepRange &steps,
-                                 int wj0, int wj1, int q_begin, int k_begin, int lq, int lk, int hk, int lane)
+                                 bool has_far, int wj0, int wj1, int q_begin, int k_begin, int lq, int lk, int hk, int lane)
 {
     if (redo == 0)
         return;
     // queries of the steps that a key of this wavefront does not see: before
-    // the keys, and behind the window (a step's missing rows repeat the last)
+    // the keys, and behind the window (a step's missing rows repeat the last,
+    // the last step of the far runs included)
     const int shift = lk - lq;
     const int before = wj1 - shift < lq ? wj1 - shift : lq;
     int behind = wj0 + seen.window - shift < lq - 1 ? wj0 + seen.window - shift : lq - 1;
     behind = behind > 0 ? behind : 0;
     const int end = steps.to * kStepRows < lq ? steps.to * kStepRows : lq;
     if (a.D == DU && !odd_queries<T>(a, q_begin, k_begin, hk, steps.from * kStepRows, before, lane) &&
-        !odd_queries<T>(a, q_begin, k_begin, hk, behind, end, lane))
+        !odd_queries<T>(a, q_begin, k_begin, hk, behind, end, lane) &&
+        !(has_far && odd_queries<T>(a, q_begin, k_begin, hk, lq - 1, lq, lane)))
         return;
     for (uint32_t left = (uint32_t)(redo | (redo >> 32)); left != 0; left &= left - 1)
         exact_dkv_row<T>(a, q_begin, k_begin, lq, lk, hk, wj0 + __ffs(left) - 1, lane);
@@ -559,7 +561,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? 2 : 1) void window_d
                     store4(v + at, z[0], z[1], z[2], z[3]);
                 }
     }
-    again_dkv<T, DU>(a, seen, __ballot(!clean), steps, wj0, wj1, q_begin, k_begin, lq, lk, hk, lane);
+    again_dkv<T, DU>(a, seen, __ballot(!clean), steps, false, wj0, wj1, q_begin, k_begin, lq, lk, hk, lane);
 }
 
 constexpr int kPartThreads = 512;
@@ -617,8 +619,8 @@ __global__ __launch_bounds__(kPartThreads) void window_dkv_parts(WindowArgs a, i
         atomicOr(&odd[lane & 31], 1);
     __syncthreads();
     if (wave == 0)
-        again_dkv<T, DU>(a, Seen{a.window, a.sinks}, __ballot(odd[lane & 31] != 0), steps, wj0, wj1, q_begin, k_begin,
-                         lq, lk, hk, lane);
+        again_dkv<T, DU>(a, Seen{a.window, a.sinks}, __ballot(odd[lane & 31] != 0), steps, has_far, wj0, wj1, q_begin,
+                         k_begin, lq, lk, hk, lane);
 }
 
 // One wavefront for each first key of each sequence and key head.
@@ -660,9 +662,11 @@ __global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slot
         if (lane + 64 * e < a.D)
             clean = clean && finite(sum[0][e]) && finite(sum[1][e]);
     }
-    // queries before the key are all that it does not see
+    // queries before the key are all that it does not see, and what repeats the
+    // last one behind the sequence
     const int before = j1 - (lk - lq) < lq ? j1 - (lk - lq) : lq;
-    if (!__all(clean) && (a.D != DU || odd_queries<T>(a, q_begin, k_begin, hk, 0, before, lane))) {
+    if (!__all(clean) && (a.D != DU || odd_queries<T>(a, q_begin, k_begin, hk, 0, before, lane) ||
+                          odd_queries<T>(a, q_begin, k_begin, hk, lq - 1, lq, lane))) {
         exact_dkv_row<T>(a, q_begin, k_begin, lq, lk, hk, j, lane);
         return;
     }

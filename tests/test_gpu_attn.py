@@ -406,6 +406,26 @@ def test_a_key_that_no_query_sees_has_no_gradient(dtype, D, Hq, value):
     assert not bool(got[1][at].any()) and not bool(got[2][at].any())
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@SIZES
+@PARTS
+def test_an_infinite_gradient_in_the_last_query(dtype, D, Hq):
+    """The last query of a sequence whose length fills no tile has one
+    infinite element of the incoming gradient: it reaches that element of dv of
+    the keys that the query sees, the first keys among them, as an infinity, and
+    no other element."""
+    n, w, s, d = 300, 40, 3, 5
+    q, k, v, do, qs, ks = operands([n, 20], [n, 20], Hq, 1, D, dtype, seed=42)
+    do[n - 1, 0, d] = 0
+    want = window_ref(q, k, v, qs, ks, w, s, None, do)
+    do[n - 1, 0, d] = math.inf
+    want["dv"][[j for j in range(n) if n - 1 - j < w or j < s], 0, d] = math.inf
+    t = [x.cuda() for x in (q, k, v, do)]
+    o, lse = sdl.window_attention(*t[:3], i32(qs), window=w, sinks=s)
+    dv = sdl.window_attention_backward(t[3], *t[:3], o, lse, i32(qs), window=w, sinks=s)[2]
+    assert_close(dv, want["dv"], want["dv_tol"], "dv")
+
+
 def test_large_scores():
     """Scores far apart: weights of exactly 0 and 1, no overflow."""
     n = 100
