@@ -7,10 +7,12 @@
 // that comes out of a tiled kernel non-finite is therefore computed once
 // more here, from the pairs that are seen alone, if a row that a masked pair
 // of its tiles brought in is not finite (any_odd): a few dozen rows at the
-// edges of the window, so infinities and NaN that are seen cost no more than
-// that look.  Finite data never come here; the tiles pay one test per
-// output.  A row all of whose elements have become NaN is not followed to
-// its end.
+// edges of the window.  An output whose sum left the range of fp32 before it was
+// divided (weights reach 2^8 there, TooLarge) is computed again too.  So
+// infinities and NaN that are seen cost no more than those two looks, and the
+// tiles pay one test per output.  Finite data come here only so, and for a
+// draft that sees no key.  A row all of whose elements have become NaN is not
+// followed to its end.
 #pragma once
 
 #include "tile.h"
@@ -59,6 +61,31 @@ __device__ inline bool any_odd(Row row, int from, int to, int D, int lane)
     return any_odd<T>(row, [](int) { return true; }, from, to, D, lane);
 }
 
+// Whether an output is infinite or no number though no value that it sums up is:
+// first the columns in which some value is not finite (of rows that may be
+// more than a query sees), then, for each output, what it holds in the others.
+template <class T>
+struct TooLarge {
+    bool odd0 = false, odd1 = false;           // of the lane's columns, lane and lane + 64
+    template <class Row, class Counts>
+    __device__ void look(Row val, Counts counts, int from, int to, int D, int lane)
+    {
+#pragma unroll 4
+        for (int j = from; j < to; ++j) {
+            if (!counts(j))
+                continue;
+            const T *v = val(j);
+            odd0 = odd0 || (lane < D && !finite((float)v[lane]));
+            odd1 = odd1 || (lane + 64 < D && !finite((float)v[lane + 64]));
+        }
+    }
+    __device__ bool operator()(const T *o, int D, int lane) const
+    {
+        return __any((lane < D && !odd0 && !finite((float)o[lane])) ||
+                     (lane + 64 < D && !odd1 && !finite((float)o[lane + 64])));
+    }
+};
+
 // Whether every lane's share of a row has become NaN.
 __device__ inline bool all_nan(float a0, float a1, int D, int lane)
 {
@@ -100,14 +127,16 @@ __device__ inline void put_row(T *row, float a0, float a1, int D, int lane)
 // o and lse of one query over keys 0 .. a - 1 and b .. c - 1 (a <= b) that
 // seen(j) lets through; key(j) and val(j) are their rows.  c2 = scale *
 // log2(e).  No key at all: 0 and -infinity.  have_lse: *lse is right already.
+// Three passes: the maximum, the sum, and the values by weights that are divided
+// already, whose sum leaves the range of fp32 only where the result does.
 template <class T, class Key, class Val, class SeenAt>
 __device__ inline void exact_row(const T *q, Key key, Val val, SeenAt seen, int a, int b, int c,
                                  int D, float c2, T *o, float *lse, bool have_lse, int lane)
 {
     const float nan = __builtin_nanf("");
-    float top = SDL_NEG_INF, total = 0.0f, a0 = 0.0f, a1 = 0.0f;
+    float top = SDL_NEG_INF, total = 0.0f, inv = 0.0f, a0 = 0.0f, a1 = 0.0f;
     bool any = false;
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int pass = 0; pass < 3; ++pass) {
         for (int j0 = 0; j0 < c; j0 += 64) {
             if (j0 >= a && j0 + 64 <= b)
                 continue;
@@ -126,10 +155,13 @@ __device__ inline void exact_row(const T *q, Key key, Val val, SeenAt seen, int 
                 continue;
             }
             const float p = in ? __builtin_amdgcn_exp2f(x - (top == SDL_NEG_INF ? 0.0f : top)) : 0.0f;
-            total += p;
+            if (pass == 1) {
+                total += p;
+                continue;
+            }
             for (uint64_t left = __ballot(in); left != 0; left &= left - 1) {
                 const int n = __ffsll((unsigned long long)left) - 1;
-                add_row(val(j0 + n), __shfl(p, n), D, lane, a0, a1);
+                add_row(val(j0 + n), __shfl(p, n) * inv, D, lane, a0, a1);
             }
             if (have_lse && all_nan(a0, a1, D, lane)) {
                 put_row(o, nan, nan, D, lane);
@@ -144,11 +176,12 @@ __device__ inline void exact_row(const T *q, Key key, Val val, SeenAt seen, int 
                     *lse = top;
                 return;
             }
+        } else if (pass == 1) {
+            total = wave_sum(total);
+            inv = 1.0f / total;
         }
     }
-    total = wave_sum(total);
-    const float inv = 1.0f / total;
-    put_row(o, any ? a0 * inv : 0.0f, any ? a1 * inv : 0.0f, D, lane);
+    put_row(o, a0, a1, D, lane);               // no key at all: the sums are empty
     if (lane == 0)
         *lse = any ? kLn2 * (top + __builtin_amdgcn_logf(total)) : SDL_NEG_INF;
 }

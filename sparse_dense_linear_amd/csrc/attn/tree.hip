@@ -259,8 +259,9 @@ struct Span {
 
 // A finished row lr of a block: four elements of its output from the sum of
 // weights and the unnormalised values.  redo[lr]: 1, the output is to be
-// computed again if a row that is masked is not finite; 2, the sum too (no
-// key was seen, or a score is infinite or no number).
+// computed again if a row that is masked is not finite, or its sum became too
+// large; 2, the sum of weights too (no key was seen, or a score is infinite
+// or no number).
 template <class T>
 __device__ inline void finish(const TreeArgs &a, int64_t token, int head, int p, float best, float sum,
                               const f32x4 &o, int *redo)
@@ -291,21 +292,30 @@ __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, i
                                     const int *redo, const Drafts &drafts, int wave, int lane)
 {
     const int group = a.Hq / a.Hkv;
-    bool some = false;
+    bool some = false, outputs = false;
     for (int lr = lane; lr < count; lr += 64)
-        some = some || redo[lr] != 0;
+        some = some || redo[lr] != 0, outputs = outputs || redo[lr] == 1;
     if (!__any(some))
         return;
     const int32_t *table = a.table + (int64_t)seq * a.table_stride;
     const PoolRows<T> key{a, table, (const T *)a.k_pages + hk * a.head_stride};
     const PoolRows<T> val{a, table, (const T *)a.v_pages + hk * a.head_stride};
-    const bool odd = odd_unseen<T>(u, seen_rows(a, u, drafts), key, val, a.D, lane);
+    const SeenRows rows = seen_rows(a, u, drafts);
+    const bool odd = odd_unseen<T>(u, rows, key, val, a.D, lane);
+    TooLarge<T> too_large;
+    if (!odd && __any(outputs)) {
+        too_large.look(val, rows, 0, a.sinks < u.low ? a.sinks : u.low, a.D, lane);
+        too_large.look(val, rows, u.low, u.end, a.D, lane);
+    }
     for (int lr = wave; lr < count; lr += 4) {
-        const int why = redo[lr];
-        if (why < (odd ? 1 : 2))               // uniform over the wavefront
+        const int why = redo[lr];              // uniform over the wavefront
+        if (why == 0)
             continue;
         const int r = first + lr, t = r / group, head = hk * group + r % group;
         const int64_t token = u.q_begin + t;
+        T *o = (T *)a.o + (token * a.Hq + head) * a.D;
+        if (why == 1 && !odd && !too_large(o, a.D, lane))
+            continue;
         DraftSeen seen;
         seen.ctx = u.ctx;
         seen.drafts = u.drafts;
@@ -316,7 +326,7 @@ __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, i
         seen.place = a.tree != nullptr ? drafts.place : nullptr;
         exact_row<T>((const T *)a.q + token * a.q_row + head * a.q_head, key, val, seen,
                      a.sinks < u.low ? a.sinks : u.low, u.low, u.end, a.D, a.scale * kLog2e,
-                     (T *)a.o + (token * a.Hq + head) * a.D, a.lse + head * a.Tq + token, why == 1, lane);
+                     o, a.lse + head * a.Tq + token, why == 1, lane);
     }
 }
 

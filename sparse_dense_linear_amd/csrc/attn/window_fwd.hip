@@ -92,19 +92,29 @@ __device__ inline void again(const WindowArgs &a, const Seen &seen, uint64_t red
     const T *V = (const T *)a.v.base + (int64_t)k_begin * a.v.row_stride + hk * a.v.head_stride;
     auto key_row = [&](int j) { return K + (int64_t)j * a.k.row_stride; };
     auto val_row = [&](int j) { return V + (int64_t)j * a.v.row_stride; };
-    // (a sum that is not finite says too little: an infinite score, a score
-    // that is no number, or an infinite key times the zeros past D)
-    if (!odd_masked_keys<T>(seen, key_row, val_row, wp0, p1, walk.first_tiles, walk.band, KT, lk, a.D, lane))
-        redo &= __ballot(!finite(lse));
+    const bool odd = odd_masked_keys<T>(seen, key_row, val_row, wp0, p1, walk.first_tiles, walk.band, KT, lk, a.D, lane);
+    TooLarge<T> too_large;
+    if (!odd && (redo & __ballot(finite(lse))) != 0) {
+        const int lo = wp0 - seen.window + 1 > 0 ? wp0 - seen.window + 1 : 0;
+        auto every = [](int) { return true; };
+        too_large.look(val_row, every, 0, seen.sinks < lo ? seen.sinks : lo, a.D, lane);
+        too_large.look(val_row, every, lo, p1 + 1, a.D, lane);
+        __threadfence_block();                 // the outputs, which other lanes stored
+    }
     for (uint32_t left = (uint32_t)(redo | (redo >> 32)); left != 0; left &= left - 1) {
         const int n = __ffs(left) - 1, i = wi0 + n, p = i + shift;
+        T *o = (T *)a.o.base + (int64_t)(q_begin + i) * a.o.row_stride + head * a.o.head_stride;
+        // (a sum of weights that is not finite says too little: an infinite
+        // score, a score that is no number, or an infinite key times the zeros
+        // past D)
+        const bool have_lse = finite(__shfl(lse, n));
+        if (!odd && have_lse && !too_large(o, a.D, lane))
+            continue;
         const int lo = p - seen.window + 1 > 0 ? p - seen.window + 1 : 0;
         exact_row<T>(
             (const T *)a.q.base + (int64_t)(q_begin + i) * a.q.row_stride + head * a.q.head_stride, key_row,
             val_row, [&](int j) { return seen(p, j); }, seen.sinks < lo ? seen.sinks : lo, lo, p + 1, a.D,
-            a.scale * kLog2e,
-            (T *)a.o.base + (int64_t)(q_begin + i) * a.o.row_stride + head * a.o.head_stride,
-            a.lse + (int64_t)head * a.Tq + q_begin + i, finite(__shfl(lse, n)), lane);
+            a.scale * kLog2e, o, a.lse + (int64_t)head * a.Tq + q_begin + i, have_lse, lane);
     }
 }
 

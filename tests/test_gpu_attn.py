@@ -426,6 +426,20 @@ def test_an_infinite_gradient_in_the_last_query(dtype, D, Hq):
     assert_close(dv, want["dv"], want["dv_tol"], "dv")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@SIZES
+@pytest.mark.parametrize("ql,kl", [([300, 40], [300, 40]), ([40, 3], [5000, 700])], ids=["whole", "split"])
+def test_values_near_the_end_of_the_range(dtype, D, ql, kl):
+    """Values of up to 2^126: their weighted mean is finite, their sum with
+    weights that are not yet divided is not."""
+    q, k, v, do, qs, ks = operands(ql, kl, 2, 1, D, dtype, seed=43)
+    v[:, :, 3] = (v[:, :, 3].abs() + 1).clamp(max=3) * 2.0 ** 124
+    want = window_ref(q, k, v, qs, ks, 2000, 2)
+    o, lse = sdl.window_attention(q.cuda(), k.cuda(), v.cuda(), i32(qs), i32(ks), window=2000, sinks=2)
+    assert_close(o, want["o"], want["o_tol"], "o")
+    assert_close(lse, want["lse"], want["lse_tol"], "lse")
+
+
 def test_large_scores():
     """Scores far apart: weights of exactly 0 and 1, no overflow."""
     n = 100

@@ -247,6 +247,26 @@ def test_pages_that_no_mask_names_are_not_read(dtype):
           masks=[[0, 0, 0], [1]])
 
 
+@BOTH
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx,drafts", [(700, 1), (700, 40), (20000, 2)])
+def test_values_near_the_end_of_the_range(dtype, D, ctx, drafts):
+    """Values of up to 2^126: their weighted mean is finite, their sum with
+    weights that are not yet divided is not."""
+    cache = Cache([ctx + drafts], 16, 1, D, dtype, 33)
+    for row in [cache.rows_v[0]] + list(cache.v):
+        row[..., 3] = (row[..., 3].abs() + 1).clamp(max=3) * 2.0 ** 124
+    q = torch.randn(drafts, 4, D, generator=torch.Generator().manual_seed(34)).to(dtype)
+    k, v, table = cache.on_gpu()
+    o, lse = sdl.tree_attention(q.cuda(), k, v, table, i32([ctx]), i32([0, drafts]), window=15000, sinks=2)
+    seen = chain_seen(ctx, drafts, 15000, 2)
+    for h in range(4):
+        f = head_forward(q[:, h].double(), cache.rows_k[0][:, 0].double(), cache.rows_v[0][:, 0].double(), seen,
+                         D ** -0.5, dtype)
+        assert_close(o[:, h], f["o"], 2 * f["o_tol"], "o")
+        assert_close(lse[h], f["lse"], 2 * f["lse_tol"], "lse")
+
+
 def test_strided_pools_and_queries():
     """Pools that are one layer of a larger tensor, queries cut from a fused
     tensor."""
