@@ -35,6 +35,10 @@
  * path: row pointers non-decreasing and within the row counts, page numbers
  * (of what a draft may see) within the pool, tables long enough.
  *
+ * A launch holds fewer than 2^24 workgroups.  Calls that would need more (2^24
+ * sequences times heads, roughly) are refused (SPMM_ERROR_UNSUPPORTED) before
+ * anything is enqueued.
+ *
  * Memory: calls allocate nothing.  Some take scratch memory from the
  * caller (device, 16-byte aligned, the size told by a host-only call); its
  * contents need no preparation and mean nothing afterwards.  Calls that may

@@ -112,7 +112,8 @@ spmm_status_t check_window(int32_t dtype, const attn_window_t *w)
         return bad("negative size");
     if (w->S >= kMaxRows || w->Tq >= kMaxRows || w->Tk >= kMaxRows)
         return bad("S, Tq and Tk must be below 2^30");
-    // workgroups of the largest launch, with room
+    // so that workgroups and their numbers fit 31 bits; what a launch holds is
+    // checked by the calls
     if (2 * (w->Tq / 32 + w->Tk / 32 + 2 * w->S) * w->Hq > kMaxGrid ||
         w->S * w->Hkv * (w->sinks > 0 ? w->sinks : 1) > kMaxGrid)
         return unsupported("too many workgroups: fewer sequences, rows or heads");
@@ -212,11 +213,18 @@ PagesArgs pages_args(const attn_pool_t *p)
     return a;
 }
 
-// 2 * layers * count * per > kMaxGrid, without overflow (all below 2^30)
-bool too_many(int64_t layers, int64_t count, int64_t per)
+// Whether 2 * layers * count * parts workgroups are more than a launch holds,
+// without overflow (all below 2^60)
+bool too_many(int64_t layers, int64_t count, int64_t parts)
 {
-    return (unsigned __int128)2 * (uint64_t)layers * (uint64_t)count * (uint64_t)per >
-           (unsigned __int128)kMaxGrid;
+    return (unsigned __int128)2 * kAttnThreads * (uint64_t)layers * (uint64_t)count >
+           (unsigned __int128)kMaxThreads / (uint64_t)parts;
+}
+
+spmm_status_t check_threads(int64_t threads)
+{
+    return threads <= kMaxThreads ? SPMM_SUCCESS
+                                  : unsupported("too many workgroups: fewer sequences, rows or heads");
 }
 
 }  // namespace
@@ -257,6 +265,8 @@ spmm_status_t window_attn_fwd(int32_t dtype, const attn_window_t *shape, const a
         return bad("scratch is smaller than window_attn_fwd_scratch says");
     if (need > 0 && (scratch == nullptr || !aligned(scratch, 16)))
         return bad("scratch is null or not 16-byte aligned");
+    if ((st = check_threads(window_fwd_threads(dtype, a))) != SPMM_SUCCESS)
+        return st;
     return launched(launch_window_fwd(dtype, a, (hipStream_t)stream), "window attention");
 }
 
@@ -330,6 +340,8 @@ spmm_status_t window_attn_bwd(int32_t dtype, const attn_window_t *shape, const a
     a.dv = out_rows(dv);
     a.delta = (float *)scratch;
     a.partial = (float *)((char *)scratch + s.delta);
+    if ((st = check_threads(window_bwd_threads(dtype, a))) != SPMM_SUCCESS)
+        return st;
     return launched(launch_window_bwd(dtype, a, (hipStream_t)stream), "window attention backward");
 }
 
@@ -399,6 +411,8 @@ spmm_status_t tree_attn_paged(int32_t dtype, const attn_tree_t *shape, const att
     a.partial = (float *)scratch;
     a.workers = sh.workers;
     a.block_rows = sh.block_rows;
+    if ((st = check_threads(tree_threads(a))) != SPMM_SUCCESS)
+        return st;
     return launched(launch_tree(dtype, a, (hipStream_t)stream), "tree attention");
 }
 
@@ -416,7 +430,7 @@ spmm_status_t pages_copy(const attn_pool_t *pool, const int32_t *src, const int3
         return st;
     if (src == nullptr || dst == nullptr || !aligned(src, 4) || !aligned(dst, 4))
         return bad("src or dst is null or not 4-byte aligned");
-    if (count >= kMaxRows || too_many(pool->layers, count, pool->page * pool->row_bytes / 16384 + 1))
+    if (count >= kMaxRows || too_many(pool->layers, count, pages_copy_parts(pool->page * pool->row_bytes)))
         return unsupported("too many pages for one call");
     PagesArgs a = pages_args(pool);
     a.src = src;
@@ -446,6 +460,8 @@ spmm_status_t pages_compact(const attn_pool_t *pool, const int32_t *table, int64
         return bad("S, kept and table_stride must be below 2^30");
     if (pool->layers > 4 * kMaxGridY || pool->row_bytes > kMaxRows / 16)
         return unsupported("at most 262140 layers, and 64 MiB to a row");
+    if (S * kAttnThreads > kMaxThreads)
+        return unsupported("too many sequences for one call");
     PagesArgs a = pages_args(pool);
     a.table = table;
     a.table_stride = table_stride;

@@ -10,6 +10,10 @@ namespace sdl {
 constexpr int kAttnThreads = 256;   // 4 wavefronts
 constexpr int kMaxHeadDim = 128;
 
+// A launch holds fewer than 2^32 threads in a dimension.  The *_threads
+// functions below tell the most that a call needs along x.
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;
+
 // Packed rows of heads: element (row, head, d) at base + row * row_stride +
 // head * head_stride + d.
 struct Rows {
@@ -54,6 +58,8 @@ inline bool few_tiles(const WindowArgs &a) { return (a.Tq / 128 + a.S) * a.Hq < 
 hipError_t launch_window_fwd(int dtype, const WindowArgs &a, hipStream_t stream);
 hipError_t launch_window_bwd(int dtype, const WindowArgs &a, hipStream_t stream);
 int64_t window_fwd_scratch_bytes(int dtype, const WindowArgs &a);
+int64_t window_fwd_threads(int dtype, const WindowArgs &a);
+int64_t window_bwd_threads(int dtype, const WindowArgs &a);
 // Bytes of delta and of the partial sums (0: none) of a backward call.
 int64_t window_bwd_delta_bytes(int64_t Tq, int64_t Hq);
 int64_t window_bwd_partial_bytes(int64_t S, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
@@ -85,6 +91,7 @@ struct TreeShape {
     int64_t bytes;
 };
 TreeShape tree_shape(int dtype, int64_t S, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D);
+int64_t tree_threads(const TreeArgs &a);
 hipError_t launch_tree(int dtype, const TreeArgs &a, hipStream_t stream);
 
 struct PagesArgs {
@@ -97,6 +104,8 @@ struct PagesArgs {
     const int32_t *keep;       // [count, kept]
     int64_t count, kept;
 };
+// Workgroups that copy a page in one layer of one pool.
+int64_t pages_copy_parts(int64_t page_bytes);
 hipError_t launch_pages_copy(const PagesArgs &a, hipStream_t stream);
 hipError_t launch_pages_compact(const PagesArgs &a, hipStream_t stream);
 

@@ -109,9 +109,11 @@ __global__ __launch_bounds__(kAttnThreads) void compact_kernel(PagesArgs a)
 
 }  // namespace
 
+int64_t pages_copy_parts(int64_t page_bytes) { return (page_bytes + kCopyBytes - 1) / kCopyBytes; }
+
 hipError_t launch_pages_copy(const PagesArgs &a, hipStream_t stream)
 {
-    const int64_t parts = (a.page * a.row_bytes + kCopyBytes - 1) / kCopyBytes;
+    const int64_t parts = pages_copy_parts(a.page * a.row_bytes);
     copy_kernel<<<dim3((uint32_t)(2 * a.layers * a.count * parts)), kAttnThreads, 0, stream>>>(a, (int)parts);
     return hipGetLastError();
 }

@@ -691,6 +691,9 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int number
     finish_again<T>(a, u, seq, hk, block * RB + row0, kJoinRows, redo, drafts, wave, lane);
 }
 
+// Blocks of queries that the join numbers, of one key head.
+int64_t join_numbers(const TreeArgs &a) { return a.Tq * (a.Hq / a.Hkv) / a.block_rows + a.S; }
+
 template <class T, int DP, int DU>
 hipError_t launch(const TreeArgs &a, hipStream_t stream)
 {
@@ -705,7 +708,7 @@ hipError_t launch(const TreeArgs &a, hipStream_t stream)
     hipError_t err = hipGetLastError();
     if (err != hipSuccess)
         return err;
-    const int64_t numbers = a.Tq * (a.Hq / a.Hkv) / a.block_rows + a.S;
+    const int64_t numbers = join_numbers(a);
     tree_join<T, DP, DU><<<dim3((uint32_t)(numbers * a.Hkv), a.block_rows / kJoinRows), kAttnThreads, 0, stream>>>(
         a, (int)numbers);
     return hipGetLastError();
@@ -727,6 +730,12 @@ TreeShape tree_shape(int dtype, int64_t S, int64_t Tq, int64_t Hq, int64_t Hkv, 
         sh.workers = 256 * (DP == 64 ? per_cu<float, 64>(sh.block_rows) : per_cu<float, 128>(sh.block_rows));
     sh.bytes = 4 * (2 * ((S + 1 + 31) / 32 * 32) + 2 * (int64_t)sh.workers * sh.block_rows * (2 + DP));
     return sh;
+}
+
+int64_t tree_threads(const TreeArgs &a)
+{
+    const int64_t join = join_numbers(a) * a.Hkv, most = join > a.workers ? join : a.workers;
+    return most * kAttnThreads;
 }
 
 hipError_t launch_tree(int dtype, const TreeArgs &a, hipStream_t stream)

@@ -623,9 +623,11 @@ __global__ __launch_bounds__(kPartThreads) void window_dkv_parts(WindowArgs a, i
                          k_begin, lq, lk, hk, lane);
 }
 
+constexpr int kJoinThreads = 64;
+
 // One wavefront for each first key of each sequence and key head.
 template <class T, int DP, int DU>
-__global__ __launch_bounds__(64) void window_dkv_join(WindowArgs a, int far_slots, int far_rows)
+__global__ __launch_bounds__(kJoinThreads) void window_dkv_join(WindowArgs a, int far_slots, int far_rows)
 {
     const int lane = threadIdx.x;
     const int j = blockIdx.x % a.sinks, hk = blockIdx.x / a.sinks % a.Hkv;
@@ -725,6 +727,23 @@ int64_t parts_floats(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, int64_t part
     return parts == 1 ? 0 : (Tk / kKeyRows + S) * Hkv * parts * kKeyRows * 2 * DU;
 }
 
+// The launches of dk and dv.
+struct DkvShape {
+    int64_t key_slots, far, far_tiles, parts;
+    int far_rows;
+};
+
+DkvShape dkv_shape(bool f32, const WindowArgs &a)
+{
+    DkvShape s;
+    s.key_slots = a.Tk / kKeyRows + a.S;
+    s.far = far_runs(f32, a.S, a.Tq, a.Tk, a.Hkv, a.window, a.sinks);
+    s.far_rows = (int)far_run_rows(f32, a.S, a.Tk, a.Hkv);
+    s.far_tiles = s.far > 0 ? (a.sinks + kKeyRows - 1) / kKeyRows : 0;
+    s.parts = dkv_parts(f32, a.S, a.Tq, a.Tk, a.Hq, a.Hkv, a.window);
+    return s;
+}
+
 template <class T, int DP, int DU, int RG>
 hipError_t launch_dq(const WindowArgs &a, hipStream_t stream)
 {
@@ -737,10 +756,7 @@ template <class T, int DP, int DU>
 hipError_t launch(const WindowArgs &a, hipStream_t stream)
 {
     constexpr bool f32 = sizeof(T) == 4;
-    const int64_t key_slots = a.Tk / kKeyRows + a.S;
-    const int64_t far = far_runs(f32, a.S, a.Tq, a.Tk, a.Hkv, a.window, a.sinks);
-    const int far_rows = (int)far_run_rows(f32, a.S, a.Tk, a.Hkv);
-    const int64_t far_tiles = far > 0 ? (a.sinks + kKeyRows - 1) / kKeyRows : 0;
+    const DkvShape s = dkv_shape(f32, a);
     hipError_t err;
     if (a.Tq > 0) {
         err = few_tiles(a) ? launch_dq<T, DP, DU, 2>(a, stream) : launch_dq<T, DP, DU, 4>(a, stream);
@@ -748,19 +764,20 @@ hipError_t launch(const WindowArgs &a, hipStream_t stream)
             return err;
     }
     if (a.Tk > 0) {
-        const int64_t parts = dkv_parts(f32, a.S, a.Tq, a.Tk, a.Hq, a.Hkv, a.window);
-        float *sums = a.partial + far_floats(a.S, a.Hkv, a.D, a.sinks, far);
-        window_dkv<T, DP, DU><<<dim3((uint32_t)((key_slots + far * far_tiles) * a.Hkv), (uint32_t)parts), kAttnThreads,
-                                0, stream>>>(a, (int)key_slots, (int)far, (int)far_tiles, far_rows, sums);
+        float *sums = a.partial + far_floats(a.S, a.Hkv, a.D, a.sinks, s.far);
+        window_dkv<T, DP, DU><<<dim3((uint32_t)((s.key_slots + s.far * s.far_tiles) * a.Hkv), (uint32_t)s.parts),
+                                kAttnThreads, 0, stream>>>(a, (int)s.key_slots, (int)s.far, (int)s.far_tiles,
+                                                           s.far_rows, sums);
         if ((err = hipGetLastError()) != hipSuccess)
             return err;
-        if (parts > 1) {
-            window_dkv_parts<T, DP, DU><<<dim3((uint32_t)(key_slots * a.Hkv), 2), kPartThreads, 0, stream>>>(
-                a, (int)key_slots, far_rows, (int)parts, sums);
+        if (s.parts > 1) {
+            window_dkv_parts<T, DP, DU><<<dim3((uint32_t)(s.key_slots * a.Hkv), 2), kPartThreads, 0, stream>>>(
+                a, (int)s.key_slots, s.far_rows, (int)s.parts, sums);
             return hipGetLastError();
         }
-        if (far > 0) {
-            window_dkv_join<T, DP, DU><<<dim3((uint32_t)(a.S * a.Hkv * a.sinks)), 64, 0, stream>>>(a, (int)far, far_rows);
+        if (s.far > 0) {
+            window_dkv_join<T, DP, DU><<<dim3((uint32_t)(a.S * a.Hkv * a.sinks)), kJoinThreads, 0, stream>>>(
+                a, (int)s.far, s.far_rows);
             if ((err = hipGetLastError()) != hipSuccess)
                 return err;
         }
@@ -778,6 +795,21 @@ int64_t window_bwd_partial_bytes(int64_t S, int64_t Tq, int64_t Tk, int64_t Hq, 
     // enough for both types: bf16 has more runs, fp32 more parts
     return 4 * (far_floats(S, Hkv, D, sinks, far_runs(false, S, Tq, Tk, Hkv, window, sinks)) +
                 parts_floats(S, Tk, Hkv, D, dkv_parts(true, S, Tq, Tk, Hq, Hkv, window)));
+}
+
+int64_t window_bwd_threads(int dtype, const WindowArgs &a)
+{
+    const DkvShape s = dkv_shape(dtype == SPMM_DTYPE_F32, a);
+    auto most = [](int64_t x, int64_t y) { return x > y ? x : y; };
+    int64_t n = 0;
+    if (a.Tq > 0)
+        n = (a.Tq / (few_tiles(a) ? 64 : 128) + a.S) * a.Hq * kAttnThreads;
+    if (a.Tk > 0) {
+        n = most(n, (s.key_slots + s.far * s.far_tiles) * a.Hkv * kAttnThreads);
+        n = most(n, s.parts > 1 ? s.key_slots * a.Hkv * kPartThreads : 0);
+        n = most(n, s.parts == 1 && s.far > 0 ? (int64_t)a.S * a.Hkv * a.sinks * kJoinThreads : 0);
+    }
+    return n;
 }
 
 hipError_t launch_window_bwd(int dtype, const WindowArgs &a, hipStream_t stream)

@@ -441,6 +441,11 @@ int64_t window_fwd_scratch_bytes(int dtype, const WindowArgs &a)
     return (a.Tq / split.rows + a.S) * a.Hq * split.parts * split.rows * (2 + DU) * 4;
 }
 
+int64_t window_fwd_threads(int dtype, const WindowArgs &a)
+{
+    return (a.Tq / window_split(dtype, a).rows + a.S) * a.Hq * kAttnThreads;
+}
+
 hipError_t launch_window_fwd(int dtype, const WindowArgs &a, hipStream_t stream)
 {
     if (dtype == SPMM_DTYPE_BF16)

@@ -221,6 +221,39 @@ def test_pages_refuse_the_rest():
     assert LIB.pages_copy(None, FAKE, FAKE, 1, None) == INVALID
 
 
+#: calls at the edge of what a launch holds (2^32 - 1 threads along x): below it,
+#: they get as far as a HIP call
+EDGE = 1 << 24
+WIDE = {n: rows(32) for n in ("dout", "q", "o", "dq")} | {n: rows(8) for n in ("k", "v", "dk", "dv")}
+AT_THE_LIMIT = [
+    # 128 queries of a head to a workgroup, and one more for each sequence
+    (lambda n: fwd(window(S=n, Hq=1, Hkv=1)), EDGE - 1),
+    (lambda n: fwd(window(S=524000, Tq=128 * n, Hq=32), q=rows(32), o=rows(32)), EDGE // 32 - 524000 - 1),
+    # the backward pass: queries, keys in tiles of 64, the far runs of first keys and their joining
+    (lambda n: bwd(window(S=n, Tk=0, Hq=1, Hkv=1), size=1 << 50), EDGE - 1),
+    (lambda n: bwd(window(S=8, Tk=64 * n, Hq=32, Hkv=8, sinks=0), size=1 << 50, **WIDE), EDGE // 8 - 9),
+    (lambda n: bwd(window(S=n, Hq=1, Hkv=1, window=10), size=1 << 50), EDGE - 1),
+    (lambda n: bwd(window(S=n, Tq=512 * 9, Tk=64 * 1000, Hq=1, Hkv=1), size=1 << 50), (EDGE - 1 - 1009) // 2),
+    (lambda n: bwd(window(S=n, Hq=1, Hkv=1, sinks=128), size=1 << 50), EDGE * 4 // 128 - 1),
+    # blocks of 16 queries
+    (lambda n: tree(tshape(S=n, Hq=1, Hkv=1)), EDGE - 1),
+    # 16 KB of a page, in a layer of a pool
+    (lambda n: copy(pool(layers=64), count=n), EDGE // 128 - 1),
+    (lambda n: copy(pool(layers=64, row_bytes=1024), count=n), EDGE // 128 - 1),
+    (lambda n: copy(pool(layers=64, row_bytes=1040), count=n), EDGE // 256 - 1),
+    (lambda n: compact(S=n), EDGE - 1),
+]
+
+
+@pytest.mark.parametrize("case", range(len(AT_THE_LIMIT)))
+def test_calls_that_no_launch_holds_are_refused(case):
+    call, most = AT_THE_LIMIT[case]
+    assert call(most + 1) == UNSUPPORTED
+    assert sdl.lib().spmm_last_error() != b""
+    if not torch.cuda.is_available():
+        assert call(most) == HIP
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path")
 def test_valid_calls_without_gpu_report_hip_errors():
     assert fwd() == HIP and bwd() == HIP and tree() == HIP and copy() == HIP and compact() == HIP
