@@ -33,7 +33,11 @@
  *
  * Preconditions, as for the CSR arrays of spmm.h not checked by the fast
  * path: row pointers non-decreasing and within the row counts, page numbers
- * (of what a draft may see) within the pool, tables long enough.
+ * (of what a draft may see) within the pool, tables long enough, contexts with
+ * their drafts below 2^30.  Outputs, gradients and scratch memory overlap
+ * neither each other nor any input: rows are written while others are still
+ * read, and a row that comes out non-finite is computed again from its inputs.
+ * (Inputs may overlap each other.)
  *
  * A launch holds fewer than 2^24 workgroups.  Calls that would need more (2^24
  * sequences times heads, roughly) are refused (SPMM_ERROR_UNSUPPORTED) before
@@ -106,8 +110,7 @@ spmm_status_t window_attn_fwd_scratch(int32_t dtype,
  *     dv_j = sum_i p_ij dout_i
  * dk and dv sum over all query heads that share a key head.  They are
  * overwritten, for every row of every sequence (keys that no query sees:
- * zero).  o and lse are those of the forward call.  dq must not overlap any
- * input.
+ * zero).  o and lse are those of the forward call.
  */
 spmm_status_t window_attn_bwd(int32_t dtype, const attn_window_t *shape,
                               const attn_rows_t *dout, const attn_rows_t *q,

@@ -155,6 +155,16 @@ def _rows(out, t, name, device, dtype, shape):
     out += (t.data_ptr(), rs if n > 1 else h * d, hs if h > 1 else d)
 
 
+def _apart(r, outs, names):
+    """Refuses an output that begins where another operand of the call does:
+    results would be written over what is still to be read."""
+    at = r[::3]
+    for i in outs:
+        if at[i] and at.count(at[i]) > 1:
+            j = next(j for j in range(len(at)) if j != i and at[j] == at[i])
+            raise ValueError(f"{names[i]} must not overlap {names[j]}")
+
+
 def _scale(scale, d) -> float:
     return 1.0 / math.sqrt(d or 1) if scale is None else float(scale)
 
@@ -180,8 +190,9 @@ def _window_shape(q, k, v, q_rowptr, window, sinks, scale, device):
 
 
 # ----------------------------------------------------------------- window
+# (fresh: the outputs were just allocated)
 
-def _fwd(q, k, v, q_rowptr, k_rowptr, o, lse, window, sinks, scale, device, handle):
+def _fwd(q, k, v, q_rowptr, k_rowptr, o, lse, window, sinks, scale, device, handle, fresh=False):
     dt = _dtype(q, "q")
     w, S = _window_shape(q, k, v, q_rowptr, window, sinks, scale, device)
     i32 = torch.int32
@@ -194,6 +205,8 @@ def _fwd(q, k, v, q_rowptr, k_rowptr, o, lse, window, sinks, scale, device, hand
     _rows(r, k, "k", device, e, k.shape)
     _rows(r, v, "v", device, e, k.shape)
     _rows(r, o, "o", device, e, q.shape)
+    if not fresh:
+        _apart(r, (3,), ("q", "k", "v", "o"))
     r = array("q", r)
     at, shape = r.buffer_info()[0], ctypes.addressof(w)
     need = ctypes.c_int64()
@@ -207,7 +220,8 @@ def _fwd(q, k, v, q_rowptr, k_rowptr, o, lse, window, sinks, scale, device, hand
         _check(st, "window_attn_fwd")
 
 
-def _bwd(dout, q, k, v, o, lse, q_rowptr, k_rowptr, dq, dk, dv, window, sinks, scale, device, handle):
+def _bwd(dout, q, k, v, o, lse, q_rowptr, k_rowptr, dq, dk, dv, window, sinks, scale, device, handle,
+         fresh=False):
     dt = _dtype(q, "q")
     w, S = _window_shape(q, k, v, q_rowptr, window, sinks, scale, device)
     i32 = torch.int32
@@ -224,6 +238,8 @@ def _bwd(dout, q, k, v, o, lse, q_rowptr, k_rowptr, dq, dk, dv, window, sinks, s
     _rows(r, dq, "dq", device, e, qs)
     _rows(r, dk, "dk", device, e, ks)
     _rows(r, dv, "dv", device, e, ks)
+    if not fresh:
+        _apart(r, (5, 6, 7), ("dout", "q", "k", "v", "o", "dq", "dk", "dv"))
     r = array("q", r)
     at, shape = r.buffer_info()[0], ctypes.addressof(w)
     need = ctypes.c_int64()
@@ -242,7 +258,8 @@ def window_attn_fwd(q, k, v, q_rowptr, k_rowptr, o, lse, window=None, sinks: int
                     scale: float | None = None, stream=None) -> None:
     """o and lse of window attention (window_attn_fwd); enqueued on `stream`
     (default: torch's current stream of q's device).  q and o [Tq, Hq, D], k
-    and v [Tk, Hkv, D] with any row and head strides, lse [Hq, Tq] float32.
+    and v [Tk, Hkv, D] with any row and head strides, lse [Hq, Tq] float32; o
+    and lse overlap nothing that the call reads.
     window None: no window; scale None: 1 / sqrt(D).  The scratch memory, if
     the call needs any, is taken from torch for this call alone."""
     device = _first(q, "q", 3, "three dimensions: rows, heads, D")
@@ -252,8 +269,9 @@ def window_attn_fwd(q, k, v, q_rowptr, k_rowptr, o, lse, window=None, sinks: int
 
 def window_attn_bwd(dout, q, k, v, o, lse, q_rowptr, k_rowptr, dq, dk, dv, window=None,
                     sinks: int = 0, scale: float | None = None, stream=None) -> None:
-    """Gradients of window_attn_fwd into dq, dk and dv (window_attn_bwd).
-    The scratch memory is taken from torch for this call alone."""
+    """Gradients of window_attn_fwd into dq, dk and dv (window_attn_bwd), which
+    overlap neither each other nor anything that the call reads.  The scratch
+    memory is taken from torch for this call alone."""
     device = _first(q, "q", 3, "three dimensions: rows, heads, D")
     with _On(device, stream) as handle:
         _bwd(dout, q, k, v, o, lse, q_rowptr, k_rowptr, dq, dk, dv, window, sinks, scale, device, handle)
@@ -274,7 +292,7 @@ def window_attention(q, k, v, q_rowptr, k_rowptr=None, window=None, sinks: int =
         o = torch.empty(q.shape, dtype=q.dtype, device=device)
         lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=device)
         _fwd(q, k, v, q_rowptr, q_rowptr if k_rowptr is None else k_rowptr, o, lse, window, sinks, scale,
-             device, handle)
+             device, handle, fresh=True)
     return o, lse
 
 
@@ -288,7 +306,7 @@ def window_attention_backward(dout, q, k, v, o, lse, q_rowptr, k_rowptr=None, wi
     with _On(device, stream) as handle:
         dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=device) for t in (q, k, v))
         _bwd(dout, q, k, v, o, lse, q_rowptr, q_rowptr if k_rowptr is None else k_rowptr, dq, dk, dv, window,
-             sinks, scale, device, handle)
+             sinks, scale, device, handle, fresh=True)
     return dq, dk, dv
 
 
@@ -338,6 +356,8 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
               _scale(scale, D), 0)
     r = []
     _rows(r, q, "q", device, q.dtype, q.shape)
+    if r[0] and r[0] == o.data_ptr():
+        raise ValueError("o must not overlap q")
     r = array("q", r)
     need, shape = ctypes.c_int64(), ctypes.addressof(w)
     st = _ready.tree_attn_scratch(dt, shape, ctypes.addressof(need))
@@ -354,8 +374,9 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
 def tree_attn_paged(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window=None,
                     sinks: int = 0, scale: float | None = None, stream=None) -> None:
     """Attention of drafted tokens over a paged cache into o [Tq, Hq, D] and
-    lse [Hq, Tq] (tree_attn_paged); see tree_attention.  The scratch memory is
-    taken from torch for this call alone."""
+    lse [Hq, Tq] (tree_attn_paged); see tree_attention.  o and lse overlap
+    nothing that the call reads.  The scratch memory is taken from torch for
+    this call alone."""
     device = _first(q, "q", 3, "three dimensions: rows, heads, D")
     with _On(device, stream) as handle:
         _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks, scale, device, handle)

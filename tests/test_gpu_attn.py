@@ -619,3 +619,22 @@ def test_binding_refusals():
         sdl.window_attention_backward(q, q, k, k, o.bfloat16(), lse, rp)
     with pytest.raises(ValueError):
         sdl.window_attention_backward(q[:, :2], q, k, k, o, lse, rp)
+
+
+def test_outputs_over_inputs_are_refused():
+    """Results written over what is still to be read."""
+    q, k, v, do = (torch.randn(40, h, 64, device="cuda") for h in (4, 2, 2, 4))
+    rp = i32([0, 40])
+    o, lse = sdl.window_attention(q, k, v, rp)
+    for t in (q, torch.cat([q, k], 1)[:, :4]):
+        with pytest.raises(ValueError, match="o must not overlap q"):
+            sdl.window_attn_fwd(t, k, v, rp, rp, t, lse)
+    grads = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v))
+    for name, over in (("dq", q), ("dq", do), ("dq", o), ("dk", k), ("dk", v), ("dv", v), ("dk", grads["dv"])):
+        with pytest.raises(ValueError, match="must not overlap"):
+            sdl.window_attn_bwd(do, q, k, v, o, lse, rp, rp, **(grads | {name: over}))
+    same = sdl.window_attention(q, k, k, rp)[0]          # inputs may be one tensor
+    assert torch.equal(same, sdl.window_attention(q, k, k.clone(), rp)[0])
+    pool, table, ctx = k[:32].view(2, 16, 2, 64), i32([[0, 1]]), i32([20])
+    with pytest.raises(ValueError, match="o must not overlap q"):
+        sdl.tree_attn_paged(q[:1], pool, pool, table, ctx, i32([0, 1]), None, q[:1], lse[:, :1].contiguous())
