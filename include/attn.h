@@ -169,7 +169,8 @@ spmm_status_t tree_attn_scratch(int32_t dtype, const attn_tree_t *shape,
 /*
  * Moves within the two pools of a cache, all layers in one launch.  A pool
  * is [layers, pages, page, row_bytes], contiguous; row_bytes (all heads of a
- * position) is a multiple of 16, the pools are 16-byte aligned.
+ * position) is a multiple of 16, the pools are 16-byte aligned and do not
+ * overlap (a precondition; pages_copy may be given one pool as both).
  *
  * pages_copy: page dst[i] becomes a copy of page src[i] in every layer of
  * both pools, i < count (a fork's partly filled page).  Pairs with a number

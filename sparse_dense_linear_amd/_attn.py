@@ -405,9 +405,9 @@ def tree_attention(q, k_pages, v_pages, table, ctx, q_rowptr, tree=None, window=
 
 # ------------------------------------------------------------------ pages
 
-def _pool(k_pool, v_pool):
+def _pool(k_pool, v_pool, one=False):
     """attn_pool_t of pools [layers, pages, page, ...], contiguous, of one
-    shape and type, and their device."""
+    shape and type, that do not overlap (one: or are one), and their device."""
     _lib()
     _is_tensor(k_pool, "k_pool")
     device = k_pool.device
@@ -422,15 +422,18 @@ def _pool(k_pool, v_pool):
     if not k_pool.is_contiguous() or not v_pool.is_contiguous():
         raise ValueError("the pools must be contiguous")
     row = math.prod(shape[3:]) * k_pool.element_size()
+    apart = abs(k_pool.data_ptr() - v_pool.data_ptr())
+    if apart < math.prod(shape[:3]) * row and not (one and apart == 0):
+        raise ValueError("the pools must not overlap")
     return _Pool(k_pool.data_ptr() or None, v_pool.data_ptr() or None, shape[0], shape[1], shape[2], row), device
 
 
 def copy_pages(k_pool, v_pool, src, dst, stream=None) -> None:
     """Page dst[i] becomes a copy of page src[i] in every layer of both pools
-    [layers, pages, page, ...] (pages_copy).  Pairs with a number outside the
-    pool are passed over; dst numbers must differ from each other and from
-    the src of other pairs."""
-    pool, device = _pool(k_pool, v_pool)
+    [layers, pages, page, ...] (pages_copy), which may be one.  Pairs with a
+    number outside the pool are passed over; dst numbers must differ from each
+    other and from the src of other pairs."""
+    pool, device = _pool(k_pool, v_pool, one=True)
     _is_tensor(src, "src")
     n = src.numel()
     sp = _index(src, "src", device, torch.int32, (n,))

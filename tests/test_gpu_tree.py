@@ -438,6 +438,27 @@ def test_compact_pages(dtype, page):
     assert torch.equal(kc.cpu(), k) and torch.equal(vc.cpu(), v)
 
 
+def test_one_pool_as_both():
+    """A pool given twice: copying does the same twice, compaction would move
+    rows that have moved already."""
+    x = torch.randn(2, 6, 16, 2, 32, device="cuda")
+    want = x.clone()
+    want[:, 4] = want[:, 1]
+    sdl.copy_pages(x, x, i32([1]), i32([4]))
+    assert torch.equal(x, want)
+    for k, v in ((x, x), (x[:1], x[:1]), (x.view(-1)[:1024 * 3].view(1, 3, 16, 2, 32), x.view(-1)[1024:1024 * 4].view(
+            1, 3, 16, 2, 32))):
+        with pytest.raises(ValueError, match="overlap"):
+            sdl.compact_pages(k, v, i32([[0, 1]]), i32([3]), i32([[1, 3]]))
+    with pytest.raises(ValueError, match="overlap"):
+        sdl.copy_pages(k, v, i32([1]), i32([2]))
+    sdl.compact_pages(x[:1], x[1:], i32([[0, 1]]), i32([3]), i32([[1, 3]]))
+    empty = x[:, :0]
+    sdl.compact_pages(empty, empty, i32([[0, 1]]), i32([3]), i32([[1, 3]]))
+    want[:, 0, 3:5] = want[:, 0, 4:7:2]
+    assert torch.equal(x, want)
+
+
 def test_pages_in_a_graph_and_on_a_stream():
     k = torch.randn(2, 8, 16, 2, 64, device="cuda")
     v = torch.randn(2, 8, 16, 2, 64, device="cuda")
