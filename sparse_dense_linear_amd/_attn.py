@@ -170,7 +170,12 @@ def _scale(scale, d) -> float:
 
 
 def _window_size(window) -> int:
-    return NO_WINDOW if window is None else index(window)
+    # (a number past 64 bits would be cut off on its way into the structure)
+    return NO_WINDOW if window is None else max(min(index(window), NO_WINDOW), -1)
+
+
+def _sinks(sinks) -> int:
+    return max(min(index(sinks), 1 << 62), -1)
 
 
 def _window_shape(q, k, v, q_rowptr, window, sinks, scale, device):
@@ -186,7 +191,7 @@ def _window_shape(q, k, v, q_rowptr, window, sinks, scale, device):
         raise ValueError("q_rowptr must hold S+1 entries")
     Tq, Hq, D = q.shape
     Tk, Hkv, _ = k.shape
-    return _Window(S, Tq, Tk, Hq, Hkv, D, _window_size(window), index(sinks), _scale(scale, D), 0), S
+    return _Window(S, Tq, Tk, Hq, Hkv, D, _window_size(window), _sinks(sinks), _scale(scale, D), 0), S
 
 
 # ----------------------------------------------------------------- window
@@ -352,7 +357,7 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
     hs = hs if Hkv > 1 else D
     rs = rs if page > 1 else Hkv * D
     ps = ps if pages > 1 else page * Hkv * D
-    w = _Tree(S, Tq, Hq, Hkv, D, page, ps, rs, hs, table.shape[1], _window_size(window), index(sinks),
+    w = _Tree(S, Tq, Hq, Hkv, D, page, ps, rs, hs, table.shape[1], _window_size(window), _sinks(sinks),
               _scale(scale, D), 0)
     r = []
     _rows(r, q, "q", device, q.dtype, q.shape)

@@ -638,3 +638,21 @@ def test_outputs_over_inputs_are_refused():
     pool, table, ctx = k[:32].view(2, 16, 2, 64), i32([[0, 1]]), i32([20])
     with pytest.raises(ValueError, match="o must not overlap q"):
         sdl.tree_attn_paged(q[:1], pool, pool, table, ctx, i32([0, 1]), None, q[:1], lse[:, :1].contiguous())
+
+
+def test_numbers_past_64_bits():
+    """A window of any size is taken for what it is, and so is a count of first
+    keys: refused."""
+    q, k = torch.randn(40, 2, 64, device="cuda"), torch.randn(40, 2, 64, device="cuda")
+    rp = i32([0, 40])
+    want = sdl.window_attention(q, k, k, rp)[0]
+    pool, table, ctx = k[:32].view(2, 16, 2, 64), i32([[0, 1]]), i32([20])
+    answer = sdl.tree_attention(q[:1], pool, pool, table, ctx, i32([0, 1]))[0]
+    for window in ((1 << 62) + 1, (1 << 63) + 5, (1 << 64) + 1, 1 << 100):
+        assert torch.equal(sdl.window_attention(q, k, k, rp, window=window)[0], want)
+        assert torch.equal(sdl.tree_attention(q[:1], pool, pool, table, ctx, i32([0, 1]), window=window)[0], answer)
+    for bad in (dict(window=-(1 << 64) + 1), dict(sinks=1 << 64), dict(sinks=(1 << 64) + 3), dict(sinks=-(1 << 64))):
+        with pytest.raises(sdl.SpmmError):
+            sdl.window_attention(q, k, k, rp, **bad)
+        with pytest.raises(sdl.SpmmError):
+            sdl.tree_attention(q[:1], pool, pool, table, ctx, i32([0, 1]), **bad)
