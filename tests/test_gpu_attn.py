@@ -1,6 +1,7 @@
 """Window attention, forward and backward, against its definition in 64 bits
 (tests/attn_ref.py states the bounds)."""
 import math
+import random
 
 import pytest
 import torch
@@ -185,6 +186,39 @@ def test_long_walks_are_split_and_joined(dtype, window, sinks):
     assert_close(o.cpu()[keep], want["o"][keep], want["o_tol"][keep], "o")
     assert_close(lse.cpu()[:, keep], want["lse"][:, keep], want["lse_tol"][:, keep], "lse")
     assert bool(torch.isnan(o[60:70]).all()) and bool(torch.isnan(lse[:, 60:70]).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D,window,sinks", [(64, 100, 70), (72, 33, 4), (128, None, 0), (128, 100, 70)])
+def test_batches_that_fill_the_gpu(dtype, D, window, sinks):
+    """Enough workgroups that walks stay whole, dq takes 128 queries at a time,
+    and far runs are of 512: (Tq / 128 + S) Hq is at least 1024 and (Tk / 64 + S)
+    Hkv at least 512."""
+    r = random.Random(D)
+    ql = [1300, 0, 570] + [r.choice([1, 2, 31, 33, 64, 65, 100, 130]) for _ in range(60)]
+    kl = [n + r.choice([0, 0, 1, 50]) for n in ql]
+    Hq, Hkv = 16, 8
+    assert (sum(ql) // 128 + len(ql)) * Hq >= 1024 and (sum(kl) // 64 + len(kl)) * Hkv >= 512
+    check(ql, kl, Hq, Hkv, D, dtype, window, sinks, seed=50)
+    # a query that is no number, among those of the far runs: the first keys
+    # it sees, and those of its window, and nothing else
+    q, k, v, do, qs, ks = operands(ql, kl, Hq, Hkv, D, dtype, seed=51)
+    at, w = 1250, sdl.NO_WINDOW if window is None else window
+    do[at] = 0
+    want = window_ref(q, k, v, qs, ks, w, sinks, None, do)
+    q[at], do[at] = math.nan, math.nan
+    t = [x.cuda() for x in (q, k, v, do)]
+    a = dict(window=window, sinks=sinks)
+    o, lse = sdl.window_attention(*t[:3], i32(qs), i32(ks), **a)
+    got = [x.cpu() for x in sdl.window_attention_backward(t[3], *t[:3], o, lse, i32(qs), i32(ks), **a)]
+    p = at + kl[0] - ql[0]
+    sees = torch.tensor([j <= p and (p - j < w or j < sinks) for j in range(ks[-1])])
+    others = torch.arange(qs[-1]) != at
+    assert_close(o.cpu()[others], want["o"][others], want["o_tol"][others], "o")
+    assert_close(got[0][others], want["dq"][others], want["dq_tol"][others], "dq")
+    for n, x in zip(("dk", "dv"), got[1:]):
+        assert bool(torch.isnan(x[sees]).all()), n
+        assert_close(x[~sees], want[n][~sees], want[n + "_tol"][~sees], n)
 
 
 def test_scale():
