@@ -13,7 +13,8 @@
  * and summed in fp32; softmax statistics and all sums are fp32; the softmax
  * weights and the gradients of the scores are rounded to bf16 once, as
  * operands of the second products, and results once, when they are stored.
- * fp32 calls round nothing below fp32.
+ * The backward call takes o as it was stored: in bf16 the products delta =
+ * <dout, o> carry its rounding.  fp32 calls round nothing below fp32.
  *
  * Masks are exact: a pair that is not seen contributes nothing, whatever its
  * key, value, query or incoming gradient holds (infinities and NaN too).  A

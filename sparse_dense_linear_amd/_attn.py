@@ -291,7 +291,10 @@ def window_attention(q, k, v, q_rowptr, k_rowptr=None, window=None, sinks: int =
     positions: query i of Lq has position i + Lk - Lq and sees key j when
     j <= position and (position - j < window or j < sinks).  Allocates o
     [Tq, Hq, D] in q's type and lse [Hq, Tq] float32, on `stream` if given;
-    rows of no sequence are left as they were allocated."""
+    rows of no sequence are left as they were allocated.
+
+    As all operators of this library it records no autograd graph, also for
+    operands that require gradients: window_attention_backward gives them."""
     device = _first(q, "q", 3, "three dimensions: rows, heads, D")
     with _On(device, stream) as handle:
         o = torch.empty(q.shape, dtype=q.dtype, device=device)
@@ -399,7 +402,7 @@ def tree_attention(q, k_pages, v_pages, table, ctx, q_rowptr, tree=None, window=
     chain; one token is a chain of one).  A draft stands at position ctx +
     (drafts it sees) - 1, and the window and the sinks are those of
     window_attention.  Allocates o [Tq, Hq, D] and lse [Hq, Tq] float32, on
-    `stream` if given."""
+    `stream` if given; records no autograd graph."""
     device = _first(q, "q", 3, "three dimensions: rows, heads, D")
     with _On(device, stream) as handle:
         o = torch.empty(q.shape, dtype=q.dtype, device=device)

@@ -56,7 +56,9 @@ __device__ inline f32x16 mma(f32x8 a, f32x8 b, f32x16 c)
 
 // Registers 8 * half .. + 7 of a result as a B operand (order above).  bf16:
 // weights and score gradients are rounded to nearest even here, once, as
-// the matrix instructions take them; their sums stay in fp32.
+// the matrix instructions take them; their sums stay in fp32.  (What is rounded
+// away of the score gradients, as a second product: a training step 870 us
+// instead of 620.)
 template <class T>
 __device__ inline Frag<T> result_frag(const f32x16 &c, int half)
 {
@@ -199,11 +201,13 @@ __device__ inline int renewed(int x)
 // A tile of ROWS rows of DP elements, of which the kernels work on the first
 // DU (D of 65 .. 96 lies in rows of 128 and costs three quarters of them: of
 // a training step in fp32 with D = 80 that saved 48 of 249 us).
-// The 16-byte pieces of a row are exchanged among themselves by its row number: neighbouring rows differ by
-// a pair of pieces and every eighth one by the order within the pair, so
-// that 8 lanes that read one piece of 8 consecutive rows, 16 lanes that read
-// 32 bytes of 4 rows, and 32 lanes that read across a row and across the one
-// 4 further touch different banks.  Rows 16 apart are exchanged alike.
+// The 16-byte pieces of a row are exchanged among themselves by its row number:
+// neighbouring rows differ by a pair of pieces and every eighth one by the order
+// within the pair, so that 8 lanes that read one piece of 8 consecutive rows,
+// and 32 lanes that read across a row and across the one 4 further, touch
+// different banks: loops of nothing but these reads count no conflicts.  bf16's
+// transposing reads (16 lanes, 32 bytes of 4 rows) count half of their cycles as
+// conflicts.  Rows 16 apart are exchanged alike.
 template <class T, int DP, int ROWS>
 struct Tile {
     static constexpr int kRowBytes = DP * (int)sizeof(T);

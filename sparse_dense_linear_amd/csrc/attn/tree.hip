@@ -17,9 +17,9 @@
 // same result every time.
 //
 // One answered token of each sequence is bound by the read of the cache: 64
-// sequences, 1.39 GB in 231 us = 6.0 TB/s (a plain read reaches 7.1), 6 us
+// sequences, 1.39 GB in 225 us = 6.2 TB/s (a plain read reaches 7.1), 6 us
 // for the join.  Drafts of up to 64 tokens with 8 heads on one are bound by
-// latency, two workgroups to a CU: 23 GFLOP in 76 us and 12 for the join.
+// latency, two workgroups to a CU: 23 GFLOP in 73 us and 12 for the join.
 #include "ops.h"
 #include "draft.h"
 #include "exact.h"
@@ -330,9 +330,9 @@ __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, i
     }
 }
 
-// Sequences whose queries fill no more than one block read their keys once:
-// keeping them in the caches would only push out what is read again.  (64
-// answers: 231 us against 255; trees of drafts, several blocks each, 83
+// Where sequences fill one block of 16 queries in the mean, most keys are read
+// once, and keeping them in the caches would only push out what is read again.
+// (64 answers: 231 us against 255; trees of drafts, several blocks each, 83
 // against 76 the other way round.)
 template <bool ONCE>
 __device__ inline u32x4 load_once(const u32x4 *p)

@@ -18,12 +18,18 @@
 // launch adds in a fixed order.  Where key tiles are few, their windows are
 // taken in parts too (dkv_parts).
 //
-// 8192 tokens, 32 heads of 128 on 8, window 1024, bf16 (forward 145 us): dq
-// 200 us, dk and dv 313, the join 5.  dq keeps the matrix cores busy 41 % of
+// delta is formed from o as the forward pass stored it.  In bf16 it carries o's
+// rounding, which is what remains in dq and dk where <do_i, v_j> - delta_i
+// cancels (windows of few keys: off by 0.0037 of their norm for 2 keys, 0.0025
+// from 16 on, where rounding alone is 0.0017).  An exact one would need the
+// products with k and v once more before this pass.
+//
+// 8192 tokens, 32 heads of 128 on 8, window 1024, bf16 (forward 136 us): dq
+// 188 us, dk and dv 292, the join 5.  dq keeps the matrix cores busy 41 % of
 // the cycles, as the forward does; dk and dv, with 128 accumulator registers
-// a lane for two gradients, have two workgroups on a CU and 37 %.  fp32 is nearer to its
-// bound (60 % in dk and dv): its matrix instructions are 16 times slower, so
-// everything else hides behind them.
+// a lane for two gradients, have two workgroups on a CU and 36 %.  fp32 is nearer
+// to its bound (54 % in dk and dv): its matrix instructions are 16 times slower,
+// so everything else hides behind them.
 #include "ops.h"
 
 #include "exact.h"

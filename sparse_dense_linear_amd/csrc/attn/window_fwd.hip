@@ -24,7 +24,8 @@ namespace {
 
 // Keys of a tile.  In bf16, 128 queries to a workgroup, tiles of 32 leave
 // room for a third workgroup on a CU (16384 tokens, 32 heads of 128 on 8,
-// window 1024: 300 us, against 326 with tiles of 64 and two workgroups).
+// window 1024: 300 us, against 326 with tiles of 64 and two workgroups, timed in
+// turn).
 __host__ __device__ constexpr int tile_keys(bool bf16, int rows) { return bf16 && rows == 128 ? 32 : 64; }
 
 // The shape of a call.  128 queries to a workgroup, unless that makes too few
@@ -121,12 +122,13 @@ __device__ inline void again(const WindowArgs &a, const Seen &seen, uint64_t red
 // The walk of a workgroup may be split over several (SplitShape): each takes
 // split.tiles key tiles of it, and what they leave is joined by window_join.
 //
-// What bounds it is the issue of instructions: matrix instructions take about
-// as long as the softmax between them, and overlap only between wavefronts
-// of a SIMD, of which three workgroups on a CU give three (tile_keys).
-// 16384 tokens, 32 heads of 128 on 8, window 1024, bf16: 309 us, 770 TFLOP/s of
-// pairs that are seen; matrix instructions keep 41 % of the cycles busy, a
-// third of the LDS cycles are bank conflicts of the transposed reads.
+// No unit bounds it alone.  16384 tokens, 32 heads of 128 on 8, window 1024,
+// bf16: 303 - 316 us, 770 TFLOP/s of pairs that are seen; matrix instructions
+// keep 41 % of the cycles busy, VALU instructions 50 %, and LDS reads take 63 %
+// of what they take in a loop of nothing else (a third of that is bank
+// conflicts of the transposing reads).  Within a wavefront products, softmax and
+// products follow each other, and overlap only between wavefronts of a SIMD, of
+// which three workgroups on a CU give three (tile_keys).
 template <class T, int DP, int DU, int RG>
 __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 ? (RG == 4 ? 3 : 2) : 1) void window_fwd(WindowArgs a, int slots, SplitShape split)
 {
