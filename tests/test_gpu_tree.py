@@ -438,6 +438,32 @@ def test_compact_pages(dtype, page):
     assert torch.equal(kc.cpu(), k) and torch.equal(vc.cpu(), v)
 
 
+def test_the_longest_lists():
+    """Lists padded to what one launch holds, and one entry more."""
+    layers, most = 64, (1 << 24) // 128 - 1
+    k = torch.randn(layers, 3, 1, 1, 4, device="cuda")
+    v = torch.randn_like(k)
+    want_k, want_v = k.clone(), v.clone()
+    want_k[:, 2], want_v[:, 2] = k[:, 0], v[:, 0]
+    src = torch.full((most + 1,), -1, dtype=torch.int32, device="cuda")
+    dst = src.clone()
+    src[most - 1], dst[most - 1] = 0, 2
+    sdl.copy_pages(k, v, src[:most], dst[:most])
+    assert torch.equal(k, want_k) and torch.equal(v, want_v)
+    with pytest.raises(sdl.SpmmError):
+        sdl.copy_pages(k, v, src, dst)
+    most = (1 << 24) - 1
+    table = torch.full((most + 1, 2), -1, dtype=torch.int32, device="cuda")
+    ctx = torch.zeros(most + 1, dtype=torch.int32, device="cuda")
+    keep = torch.full((most + 1, 1), -1, dtype=torch.int32, device="cuda")
+    table[most - 1, 0], table[most - 1, 1], keep[most - 1] = 1, 2, 1
+    want_k[:1, 1], want_v[:1, 1] = want_k[:1, 2], want_v[:1, 2]
+    sdl.compact_pages(k[:1], v[:1], table[:most], ctx[:most], keep[:most])
+    assert torch.equal(k, want_k) and torch.equal(v, want_v)
+    with pytest.raises(sdl.SpmmError):
+        sdl.compact_pages(k[:1], v[:1], table, ctx, keep)
+
+
 def test_one_pool_as_both():
     """A pool given twice: copying does the same twice, compaction would move
     rows that have moved already."""
