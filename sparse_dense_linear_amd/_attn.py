@@ -170,12 +170,21 @@ def _scale(scale, d) -> float:
 
 
 def _window_size(window) -> int:
-    # (a number past 64 bits would be cut off on its way into the structure)
-    return NO_WINDOW if window is None else max(min(index(window), NO_WINDOW), -1)
+    if window is None:
+        return NO_WINDOW
+    window = index(window)
+    return window if -1 <= window <= NO_WINDOW else _cut(window, NO_WINDOW)
 
 
 def _sinks(sinks) -> int:
-    return max(min(index(sinks), 1 << 62), -1)
+    sinks = index(sinks)
+    return sinks if -1 <= sinks <= NO_WINDOW else _cut(sinks, NO_WINDOW)
+
+
+def _cut(x, most) -> int:
+    """A number past 64 bits would lose its upper ones on its way into a
+    structure; those below 0 and above `most` are all alike."""
+    return most if x > most else -1
 
 
 def _window_shape(q, k, v, q_rowptr, window, sinks, scale, device):
@@ -364,7 +373,8 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
               _scale(scale, D), 0)
     r = []
     _rows(r, q, "q", device, q.dtype, q.shape)
-    if r[0] and r[0] == o.data_ptr():
+    op = o.data_ptr()
+    if op and op == r[0]:
         raise ValueError("o must not overlap q")
     r = array("q", r)
     need, shape = ctypes.c_int64(), ctypes.addressof(w)
@@ -373,7 +383,7 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
         _check(st, "tree_attn_scratch")
     scratch = torch.empty(need.value, dtype=torch.uint8, device=device)
     st = _ready.tree_attn_paged(dt, shape, r.buffer_info()[0], k_pages.data_ptr() or None,
-                                v_pages.data_ptr() or None, bp, cp, qp, tp, o.data_ptr() or None, lp,
+                                v_pages.data_ptr() or None, bp, cp, qp, tp, op or None, lp,
                                 scratch.data_ptr() or None, need.value, handle)
     if st:
         _check(st, "tree_attn_paged")
@@ -429,11 +439,12 @@ def _pool(k_pool, v_pool, one=False):
         raise ValueError("the pools must have one shape and element type")
     if not k_pool.is_contiguous() or not v_pool.is_contiguous():
         raise ValueError("the pools must be contiguous")
+    layers, pages, page = shape[:3]
     row = math.prod(shape[3:]) * k_pool.element_size()
-    apart = abs(k_pool.data_ptr() - v_pool.data_ptr())
-    if apart < math.prod(shape[:3]) * row and not (one and apart == 0):
+    kp, vp = k_pool.data_ptr(), v_pool.data_ptr()
+    if abs(kp - vp) < layers * pages * page * row and not (one and kp == vp):
         raise ValueError("the pools must not overlap")
-    return _Pool(k_pool.data_ptr() or None, v_pool.data_ptr() or None, shape[0], shape[1], shape[2], row), device
+    return _Pool(kp or None, vp or None, layers, pages, page, row), device
 
 
 def copy_pages(k_pool, v_pool, src, dst, stream=None) -> None:
