@@ -48,3 +48,4 @@ from ._attn import (  # noqa: F401
     window_attn_bwd,
     window_attn_fwd,
 )
+from ._cache import append_pages  # noqa: F401

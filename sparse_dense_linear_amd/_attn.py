@@ -35,6 +35,19 @@ class _Pool(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("layers", "pages", "page", "row_bytes")]
 
 
+class _Scales(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int64) for n in ("block", "page_stride", "block_stride", "head_stride")]
+
+
+class _CodePool(ctypes.Structure):
+    _fields_ = [("pool", _Pool), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("block", ctypes.c_int64), ("heads", ctypes.c_int64)]
+
+
+#: What a pool holds (include/cache.h).
+CACHE_AS_IS, CACHE_E4M3, CACHE_INT8 = 0, 1, 2
+
 #: Bytes of one operand's description (attn_rows_t): descriptions of a call
 #: are laid out one after another in an array of 64-bit numbers.
 _ROWS = ctypes.sizeof(_Rows)
@@ -57,7 +70,13 @@ def _lib():
         L.tree_attn_scratch.argtypes = [I32, P, P]
         L.pages_copy.argtypes = [P, P, P, I64, P]
         L.pages_compact.argtypes = [P, P, I64, P, P, I64, I64, P]
-        for name in ("window_attn_fwd", "window_attn_fwd_scratch", "window_attn_bwd", "window_attn_bwd_scratch",
+        L.cache_append.argtypes = [I32, I32] + [P] * 15
+        L.cache_tree_attn.argtypes = [I32, I32] + [P] * 12 + [I64, P]
+        L.cache_tree_attn_scratch.argtypes = [I32, I32, P, P]
+        L.cache_copy.argtypes = [P, P, P, I64, P]
+        L.cache_compact.argtypes = [I32, P, P, I64, P, P, I64, I64, P]
+        for name in ("cache_append", "cache_tree_attn", "cache_tree_attn_scratch", "cache_copy", "cache_compact",
+                     "window_attn_fwd", "window_attn_fwd_scratch", "window_attn_bwd", "window_attn_bwd_scratch",
                      "tree_attn_paged", "tree_attn_scratch", "pages_copy", "pages_compact"):
             getattr(L, name).restype = I32
         _ready = L
@@ -116,6 +135,16 @@ def _dtype(t, name) -> int:
     if t.dtype is torch.bfloat16:
         return DTYPE_BF16
     raise TypeError(f"{name} must be float32 or bfloat16")
+
+
+def _codes(t, name) -> int:
+    """What a pool of 8 bits holds."""
+    _is_tensor(t, name)
+    if t.dtype is torch.float8_e4m3fn:
+        return CACHE_E4M3
+    if t.dtype is torch.int8:
+        return CACHE_INT8
+    raise TypeError(f"{name} must be float8_e4m3fn or int8")
 
 
 def _with(t, name, device):
@@ -327,9 +356,47 @@ def window_attention_backward(dout, q, k, v, o, lse, q_rowptr, k_rowptr=None, wi
     return dq, dk, dv
 
 
+# ---------------------------------------------------------------- pools
+
+def _paging(k_pages, v_pages, D):
+    """Pages, page, heads and strides of two pools [pages, page, heads, D]."""
+    pages, page, Hkv, Dk = k_pages.shape
+    if v_pages.shape != k_pages.shape or Dk != D:
+        raise ValueError("the pools must have one shape, with the D of q")
+    if page < 1:
+        raise ValueError("a page must hold at least one position")
+    ps, rs, hs, ds = k_pages.stride()
+    if pages and Hkv and D and (v_pages.stride() != (ps, rs, hs, ds) or (D > 1 and ds != 1)):
+        raise ValueError("the pools must have the same strides and be contiguous along D")
+    # the stride of a dimension that holds one element says nothing
+    hs = hs if Hkv > 1 else D
+    rs = rs if page > 1 else Hkv * D
+    ps = ps if pages > 1 else page * Hkv * D
+    return pages, page, Hkv, ps, rs, hs
+
+
+def _scales(k_scale, v_scale, device, pages, page, heads):
+    """cache_scales_t of scales [pages, page / block, heads], with any strides."""
+    _with(k_scale, "k_scale", device)
+    _with(v_scale, "v_scale", device)
+    if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+        raise TypeError("the scales must be float32")
+    shape = k_scale.shape
+    if len(shape) != 3 or v_scale.shape != shape or shape[0] != pages or shape[2] != heads:
+        raise ValueError("the scales must have one shape: pages, blocks of a page, heads")
+    blocks = shape[1]
+    if blocks < 1 or page % blocks:
+        raise ValueError("the blocks of a page must divide its positions")
+    ps, bs, hs = k_scale.stride()
+    if v_scale.stride() != (ps, bs, hs) and pages and heads:
+        raise ValueError("the scales must have the same strides")
+    return _Scales(k_scale.data_ptr() or None, v_scale.data_ptr() or None, page // blocks, ps, bs, hs)
+
+
 # ------------------------------------------------------------------- tree
 
-def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks, scale, device, handle):
+def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks, scale, k_scale, v_scale,
+          device, handle):
     dt = _dtype(q, "q")
     _with(k_pages, "k_pages", device)
     _with(v_pages, "v_pages", device)
@@ -342,7 +409,6 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
         raise ValueError("table must have two dimensions: sequences, pages")
     S = ctx.numel()
     Tq, Hq, D = q.shape
-    pages, page, Hkv, Dk = k_pages.shape
     i32 = torch.int32
     cp = _index(ctx, "ctx", device, i32, (S,))
     qp = _index(q_rowptr, "q_rowptr", device, i32, (S + 1,))
@@ -354,21 +420,16 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
             raise TypeError("tree must hold 64-bit masks (int64 or uint64)")
         tp = _index(tree, "tree", device, tree.dtype, (Tq,))
     lp = _index(lse, "lse", device, torch.float32, (Hq, Tq))
-    if k_pages.dtype is not q.dtype or v_pages.dtype is not q.dtype or o.dtype is not q.dtype:
-        raise TypeError("the pools and o must have the element type of q")
-    if v_pages.shape != k_pages.shape or Dk != D:
-        raise ValueError("the pools must have one shape, with the D of q")
+    held = k_scale is not None or v_scale is not None
+    if held:
+        kind = _codes(k_pages, "k_pages")
+        if v_pages.dtype is not k_pages.dtype or o.dtype is not q.dtype:
+            raise TypeError("the pools must have one element type, and o that of q")
+    elif k_pages.dtype is not q.dtype or v_pages.dtype is not q.dtype or o.dtype is not q.dtype:
+        raise TypeError("the pools (without scales) and o must have the element type of q")
+    pages, page, Hkv, ps, rs, hs = _paging(k_pages, v_pages, D)
     if o.shape != q.shape or not o.is_contiguous():
         raise ValueError("o must be contiguous, with the shape of q")
-    if page < 1:
-        raise ValueError("a page must hold at least one position")
-    ps, rs, hs, ds = k_pages.stride()
-    if pages and Hkv and D and (v_pages.stride() != (ps, rs, hs, ds) or (D > 1 and ds != 1)):
-        raise ValueError("the pools must have the same strides and be contiguous along D")
-    # the stride of a dimension that holds one element says nothing
-    hs = hs if Hkv > 1 else D
-    rs = rs if page > 1 else Hkv * D
-    ps = ps if pages > 1 else page * Hkv * D
     w = _Tree(S, Tq, Hq, Hkv, D, page, ps, rs, hs, table.shape[1], _window_size(window), _sinks(sinks),
               _scale(scale, D), 0)
     r = []
@@ -378,6 +439,18 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
         raise ValueError("o must not overlap q")
     r = array("q", r)
     need, shape = ctypes.c_int64(), ctypes.addressof(w)
+    if held:
+        scales = _scales(k_scale, v_scale, device, pages, page, Hkv)
+        st = _ready.cache_tree_attn_scratch(dt, kind, shape, ctypes.addressof(need))
+        if st:
+            _check(st, "cache_tree_attn_scratch")
+        scratch = torch.empty(need.value, dtype=torch.uint8, device=device)
+        st = _ready.cache_tree_attn(dt, kind, shape, r.buffer_info()[0], k_pages.data_ptr() or None,
+                                    v_pages.data_ptr() or None, ctypes.addressof(scales), bp, cp, qp, tp,
+                                    op or None, lp, scratch.data_ptr() or None, need.value, handle)
+        if st:
+            _check(st, "cache_tree_attn")
+        return
     st = _ready.tree_attn_scratch(dt, shape, ctypes.addressof(need))
     if st:
         _check(st, "tree_attn_scratch")
@@ -390,18 +463,19 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
 
 
 def tree_attn_paged(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window=None,
-                    sinks: int = 0, scale: float | None = None, stream=None) -> None:
+                    sinks: int = 0, scale: float | None = None, stream=None, k_scale=None, v_scale=None) -> None:
     """Attention of drafted tokens over a paged cache into o [Tq, Hq, D] and
-    lse [Hq, Tq] (tree_attn_paged); see tree_attention.  o and lse overlap
+    lse [Hq, Tq] (tree_attn_paged, with scales cache_tree_attn); see tree_attention.  o and lse overlap
     nothing that the call reads.  The scratch memory is taken from torch for
     this call alone."""
     device = _first(q, "q", 3, "three dimensions: rows, heads, D")
     with _On(device, stream) as handle:
-        _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks, scale, device, handle)
+        _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks, scale, k_scale, v_scale,
+              device, handle)
 
 
 def tree_attention(q, k_pages, v_pages, table, ctx, q_rowptr, tree=None, window=None, sinks: int = 0,
-                   scale: float | None = None, stream=None):
+                   scale: float | None = None, stream=None, k_scale=None, v_scale=None):
     """(o, lse) of drafted tokens over a paged cache.
 
     Sequence s has ctx[s] cached positions, and its drafts are rows
@@ -411,13 +485,21 @@ def tree_attention(q, k_pages, v_pages, table, ctx, q_rowptr, tree=None, window=
     tree[row] says that the draft sees draft a of its sequence (tree None: a
     chain; one token is a chain of one).  A draft stands at position ctx +
     (drafts it sees) - 1, and the window and the sinks are those of
-    window_attention.  Allocates o [Tq, Hq, D] and lse [Hq, Tq] float32, on
-    `stream` if given; records no autograd graph."""
+    window_attention.
+
+    The pools hold rows of q's type, or, with k_scale and v_scale, codes of 8
+    bits (float8_e4m3fn or int8): value = code * scale, the scales [pages,
+    page / block, Hkv] float32 for each block of positions and head, with any
+    strides.  D is then a multiple of 16.
+
+    Allocates o [Tq, Hq, D] and lse [Hq, Tq] float32, on `stream` if given;
+    records no autograd graph."""
     device = _first(q, "q", 3, "three dimensions: rows, heads, D")
     with _On(device, stream) as handle:
         o = torch.empty(q.shape, dtype=q.dtype, device=device)
         lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=device)
-        _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks, scale, device, handle)
+        _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks, scale, k_scale,
+              v_scale, device, handle)
     return o, lse
 
 
@@ -447,28 +529,66 @@ def _pool(k_pool, v_pool, one=False):
     return _Pool(kp or None, vp or None, layers, pages, page, row), device
 
 
-def copy_pages(k_pool, v_pool, src, dst, stream=None) -> None:
+def _code_pool(pool, k_pool, k_scale, v_scale, device):
+    """cache_pool_t of pools of codes [layers, pages, page, heads, D] and their
+    scales [layers, pages, page / block, heads], contiguous."""
+    if k_pool.dim() != 5:
+        raise ValueError("a pool with scales must have five dimensions: layers, pages, page, heads, D")
+    _codes(k_pool, "k_pool")
+    _with(k_scale, "k_scale", device)
+    _with(v_scale, "v_scale", device)
+    layers, pages, page, heads, _ = k_pool.shape
+    shape = k_scale.shape
+    if len(shape) != 4 or v_scale.shape != shape or shape[:2] != (layers, pages) or shape[3] != heads:
+        raise ValueError("the scales must have one shape: layers, pages, blocks of a page, heads")
+    if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+        raise TypeError("the scales must be float32")
+    if not k_scale.is_contiguous() or not v_scale.is_contiguous():
+        raise ValueError("the scales must be contiguous")
+    blocks = shape[2]
+    if blocks < 1 or page % blocks:
+        raise ValueError("the blocks of a page must divide its positions")
+    ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    same = pool.k == pool.v
+    if (ks == vs) != same or (not same and abs(ks - vs) < 4 * layers * pages * blocks * heads):
+        raise ValueError("the scales must not overlap, or be one where the pools are")
+    return _CodePool(pool, ks or None, vs or None, max(1, page // blocks), heads)
+
+
+def copy_pages(k_pool, v_pool, src, dst, stream=None, k_scale=None, v_scale=None) -> None:
     """Page dst[i] becomes a copy of page src[i] in every layer of both pools
     [layers, pages, page, ...] (pages_copy), which may be one.  Pairs with a
     number outside the pool are passed over; dst numbers must differ from each
-    other and from the src of other pairs."""
+    other and from the src of other pairs.  Pools of 8 bits [layers, pages, page,
+    heads, D] take their scales [layers, pages, page / block, heads] with them
+    (cache_copy)."""
     pool, device = _pool(k_pool, v_pool, one=True)
+    held = k_scale is not None or v_scale is not None
+    if held:
+        pool = _code_pool(pool, k_pool, k_scale, v_scale, device)
     _is_tensor(src, "src")
     n = src.numel()
     sp = _index(src, "src", device, torch.int32, (n,))
     dp = _index(dst, "dst", device, torch.int32, (n,))
     with _On(device, stream) as handle:
-        st = _ready.pages_copy(ctypes.addressof(pool), sp, dp, n, handle)
+        copy = _ready.cache_copy if held else _ready.pages_copy
+        st = copy(ctypes.addressof(pool), sp, dp, n, handle)
     if st:
-        _check(st, "pages_copy")
+        _check(st, "cache_copy" if held else "pages_copy")
 
 
-def compact_pages(k_pool, v_pool, table, ctx, keep, stream=None) -> None:
+def compact_pages(k_pool, v_pool, table, ctx, keep, stream=None, k_scale=None, v_scale=None) -> None:
     """The kept drafts of each sequence move to the front of its drafts, in
     every layer of both pools (pages_compact): position ctx[s] + keep[s, t]
     to ctx[s] + t, up to the first negative entry of keep [S, kept]; the
-    entries before it are strictly ascending."""
+    entries before it are strictly ascending.  In pools of 8 bits [layers, pages,
+    page, heads, D] with scales [layers, pages, page / block, heads], a block
+    that kept rows move into takes the largest scale of those that its rows come
+    from, and codes are rounded to it (cache_compact)."""
     pool, device = _pool(k_pool, v_pool)
+    held = k_scale is not None or v_scale is not None
+    if held:
+        pool, kind = _code_pool(pool, k_pool, k_scale, v_scale, device), _codes(k_pool, "k_pool")
     _is_tensor(table, "table")
     _is_tensor(ctx, "ctx")
     _is_tensor(keep, "keep")
@@ -480,6 +600,9 @@ def compact_pages(k_pool, v_pool, table, ctx, keep, stream=None) -> None:
     bp = _index(table, "table", device, torch.int32, (S, wide))
     kp = _index(keep, "keep", device, torch.int32, (S, kept))
     with _On(device, stream) as handle:
-        st = _ready.pages_compact(ctypes.addressof(pool), bp, wide, cp, kp, S, kept, handle)
+        if held:
+            st = _ready.cache_compact(kind, ctypes.addressof(pool), bp, wide, cp, kp, S, kept, handle)
+        else:
+            st = _ready.pages_compact(ctypes.addressof(pool), bp, wide, cp, kp, S, kept, handle)
     if st:
-        _check(st, "pages_compact")
+        _check(st, "cache_compact" if held else "pages_compact")

@@ -24,7 +24,7 @@ SOURCES = ["api.hip", "plan.hip", "worker.hip", "sddmm.hip", "eb.hip",
            "worker_f32_buf.hip", "worker_f32_flat.hip", "worker_bf16_buf.hip",
            "worker_bf16_flat.hip", "worker_fused_buf.hip", "worker_fused_flat.hip",
            "attn/api.hip", "attn/window_fwd.hip", "attn/window_bwd.hip", "attn/tree.hip",
-           "attn/pages.hip"]
+           "attn/pages.hip", "attn/tree_e4m3.hip", "attn/tree_int8.hip", "attn/cache.hip", "attn/append.hip"]
 CEILING_SOURCE = "ceiling.hip"
 CEILING_PATH = os.path.join(HERE, "libsdl_ceiling.so")
 ARCH = "gfx950"

@@ -37,16 +37,16 @@ __device__ inline float wave_sum(float x)
 
 // Whether one of rows from .. to - 1 (row(j): where it starts) that counts(j)
 // lets through has an element that is not finite.
-template <class T, class Row, class Counts>
+template <class Row, class Counts>
 __device__ inline bool any_odd(Row row, Counts counts, int from, int to, int D, int lane)
 {
     bool odd = false;
     for (int j = from + lane; j < to; j += 64) {
         if (!counts(j))
             continue;
-        const T *p = row(j);
+        const auto p = row(j);
         for (int d = 0; d < D; d += 8) {
-            const Frag<T> x = load8(p + d);
+            const auto x = load8(p + d);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 odd = odd || !finite((float)x[e]);
@@ -55,10 +55,10 @@ __device__ inline bool any_odd(Row row, Counts counts, int from, int to, int D, 
     return __any(odd);
 }
 
-template <class T, class Row>
+template <class Row>
 __device__ inline bool any_odd(Row row, int from, int to, int D, int lane)
 {
-    return any_odd<T>(row, [](int) { return true; }, from, to, D, lane);
+    return any_odd(row, [](int) { return true; }, from, to, D, lane);
 }
 
 // Whether an output is infinite or no number though no value that it sums up is:
@@ -74,7 +74,7 @@ struct TooLarge {
         for (int j = from; j < to; ++j) {
             if (!counts(j))
                 continue;
-            const T *v = val(j);
+            const auto v = val(j);
             odd0 = odd0 || (lane < D && !finite((float)v[lane]));
             odd1 = odd1 || (lane + 64 < D && !finite((float)v[lane + 64]));
         }
@@ -92,12 +92,13 @@ __device__ inline bool all_nan(float a0, float a1, int D, int lane)
     return __all((lane >= D || a0 != a0) && (lane + 64 >= D || a1 != a1));
 }
 
-template <class T>
-__device__ inline float dot_row(const T *a, const T *b, int D)
+template <class A, class B>
+__device__ inline float dot_row(A a, B b, int D)
 {
     float s = 0.0f;
     for (int d = 0; d < D; d += 8) {
-        const Frag<T> x = load8(a + d), y = load8(b + d);
+        const auto x = load8(a + d);
+        const auto y = load8(b + d);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             s = fmaf((float)x[e], (float)y[e], s);
@@ -106,8 +107,8 @@ __device__ inline float dot_row(const T *a, const T *b, int D)
 }
 
 // Adds w * row[d] to (a0: d = lane, a1: d = lane + 64).
-template <class T>
-__device__ inline void add_row(const T *row, float w, int D, int lane, float &a0, float &a1)
+template <class Row>
+__device__ inline void add_row(Row row, float w, int D, int lane, float &a0, float &a1)
 {
     if (lane < D)
         a0 = fmaf(w, (float)row[lane], a0);
@@ -258,7 +259,7 @@ __device__ inline bool odd_masked_keys(const Seen &seen, Key key, Val val, int p
 {
     auto odd = [&](int from, int to) {
         to = to < lk ? to : lk;
-        return any_odd<T>(key, from, to, D, lane) || any_odd<T>(val, from, to, D, lane);
+        return any_odd(key, from, to, D, lane) || any_odd(val, from, to, D, lane);
     };
     const int from = band * KT > seen.sinks ? band * KT : seen.sinks;
     // past the queries, behind the window, behind the first keys (and the

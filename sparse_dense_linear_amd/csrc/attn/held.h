@@ -1,0 +1,151 @@
+// held.h -- rows of a cache that are held as codes of 8 bits: value = code *
+// scale, one fp32 scale for each block of positions and head.
+//
+// Codes are exact in bf16 and fp32 (e4m3 has 4 significant bits, an integer 8),
+// so the matrix instructions take them as they are, and the scales, which
+// differ from key to key, are applied in fp32 to the scores and to the softmax
+// weights: nothing is rounded that rows of bf16 would not round.
+#pragma once
+
+#include "tile.h"
+
+namespace sdl {
+
+struct E4M3 { uint8_t code; };      // sign, 4 bits of exponent, 3 of fraction; no infinity; 0x7f, 0xff: NaN
+struct Int8 { int8_t code; };
+
+template <class H> inline constexpr bool kCodes = false;
+template <> inline constexpr bool kCodes<E4M3> = true;
+template <> inline constexpr bool kCodes<Int8> = true;
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Values of the four codes in w.
+template <class H>
+__device__ inline f32x4 wide(uint32_t w)
+{
+    if constexpr (std::is_same_v<H, E4M3>) {
+        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+        return f32x4{a[0], a[1], b[0], b[1]};
+    } else {
+        return f32x4{(float)(int8_t)w, (float)(int8_t)(w >> 8), (float)(int8_t)(w >> 16), (float)(int8_t)(w >> 24)};
+    }
+}
+
+template <class H>
+__device__ inline bf16x4 wide_bf16(uint32_t w)
+{
+    if constexpr (std::is_same_v<H, E4M3>) {
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
+        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3);
+    } else {
+        const f32x4 x = wide<H>(w);
+        return bf16x4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+    }
+}
+
+// Largest value of a code, and the codes of four values that are divided by
+// their scale already (no larger than that, or no number), to nearest even.
+template <class H> inline constexpr float kMost = std::is_same_v<H, E4M3> ? 448.0f : 127.0f;
+
+template <class H>
+__device__ inline uint32_t narrow(f32x4 x)
+{
+    if constexpr (std::is_same_v<H, E4M3>) {
+        const int low = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+        return __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], low, true);
+    } else {
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w |= ((uint32_t)(int)__builtin_rintf(x[e]) & 0xff) << (8 * e);     // NaN: 0
+        return w;
+    }
+}
+
+// The smallest power of two s >= 2^-126 with top <= kMost s, for a finite top >= 0.
+template <class H>
+__device__ inline float scale_of_top(float top)
+{
+    // kMost is 1.75 * 2^8 or 1.984375 * 2^6
+    constexpr uint32_t most = std::is_same_v<H, E4M3> ? 0x43e00000 : 0x42fe0000;
+    const uint32_t bits = __float_as_uint(top);
+    const int e = (int)(bits >> 23) - (int)(most >> 23) + ((bits & 0x7fffff) > (most & 0x7fffff) ? 1 : 0);
+    return __uint_as_float((uint32_t)(e > -126 ? e + 127 : 1) << 23);
+}
+
+// Division by a scale, rounded once: a product where the scale is a power of
+// two, which it is unless another program wrote it.
+struct Divide {
+    float by, inverse;
+    bool power;
+    __device__ explicit Divide(float scale) : by(scale)
+    {
+        const uint32_t bits = __float_as_uint(scale), e = bits >> 23;
+        power = (bits & 0x7fffff) == 0 && e >= 1 && e <= 253;
+        inverse = __uint_as_float((254 - e) << 23);
+    }
+    __device__ f32x4 operator()(f32x4 x) const
+    {
+        if (power)
+            return f32x4{x[0] * inverse, x[1] * inverse, x[2] * inverse, x[3] * inverse};
+        return f32x4{x[0] / by, x[1] / by, x[2] / by, x[3] / by};
+    }
+};
+
+// The larger scale; NaN if either is.
+__device__ inline float larger_scale(float a, float b) { return a != a || a >= b ? a : b; }
+
+// A row of codes as a row of values, for exact.h.
+template <class H>
+struct CodeRow {
+    const H *at;
+    float scale;
+    __device__ CodeRow operator+(int d) const { return {at + d, scale}; }
+    __device__ float operator[](int d) const { return wide<H>(*(const uint8_t *)(at + d))[0] * scale; }
+};
+
+template <class H>
+__device__ inline f32x8 load8(CodeRow<H> r)
+{
+    const uint32_t *w = (const uint32_t *)r.at;
+    const f32x4 a = wide<H>(w[0]) * r.scale, b = wide<H>(w[1]) * r.scale;
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// A 16-byte piece of a pool's row into an LDS tile of T.
+template <class T, class H, class Tl>
+__device__ inline void put_piece(char *tile, int row, int piece, u32x4 x)
+{
+    if constexpr (!kCodes<H>) {
+        *(u32x4 *)(tile + Tl::at(row, piece)) = x;
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const auto a = wide_bf16<H>(x[2 * i]), b = wide_bf16<H>(x[2 * i + 1]);
+            *(bf16x8 *)(tile + Tl::at(row, 2 * piece + i)) = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *(f32x4 *)(tile + Tl::at(row, 4 * piece + i)) = wide<H>(x[i]);
+    }
+}
+
+// Scores or weights of a result's rows times the scales of their keys, four
+// consecutive ones to a group of registers and eight apart; `scale`: of the
+// lane's first.
+template <int COUNT, class Acc>
+__device__ inline void times_scales(Acc &x, const float *scale)
+{
+#pragma unroll
+    for (int g = 0; g < COUNT / 4; ++g) {
+        const f32x4 s = *(const f32x4 *)(scale + 8 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[4 * g + e] *= s[e];
+    }
+}
+
+}  // namespace sdl

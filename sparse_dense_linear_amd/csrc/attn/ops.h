@@ -83,6 +83,10 @@ struct TreeArgs {
     float scale;
     float *partial;
     int32_t workers, block_rows;   // launch shape (tree_shape)
+    // pools of codes only: scales of blocks of positions, and their strides
+    const float *k_scale, *v_scale;
+    int64_t scale_page, scale_block, scale_head;
+    int32_t block;
 };
 
 // Workgroups of the split, queries of a workgroup, and the workspace.
@@ -90,9 +94,11 @@ struct TreeShape {
     int32_t workers, block_rows;
     int64_t bytes;
 };
-TreeShape tree_shape(int dtype, int64_t S, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D);
+TreeShape tree_shape(int dtype, int held, int64_t S, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D);
 int64_t tree_threads(const TreeArgs &a);
 hipError_t launch_tree(int dtype, const TreeArgs &a, hipStream_t stream);
+hipError_t launch_tree_e4m3(int dtype, const TreeArgs &a, hipStream_t stream);
+hipError_t launch_tree_int8(int dtype, const TreeArgs &a, hipStream_t stream);
 
 struct PagesArgs {
     char *k, *v;               // [layers, pages, page, row_bytes]
@@ -103,10 +109,34 @@ struct PagesArgs {
     const int32_t *ctx;        // [count]
     const int32_t *keep;       // [count, kept]
     int64_t count, kept;
+    // pools of codes only (cache.h): scales [layers, pages, page / block, heads]
+    float *k_scale, *v_scale;
+    int64_t block, heads;
 };
 // Workgroups that copy a page in one layer of one pool.
 int64_t pages_copy_parts(int64_t page_bytes);
 hipError_t launch_pages_copy(const PagesArgs &a, hipStream_t stream);
 hipError_t launch_pages_compact(const PagesArgs &a, hipStream_t stream);
+hipError_t launch_cache_compact(int held, const PagesArgs &a, hipStream_t stream);
+
+struct AppendArgs {
+    Rows q, k, v;
+    OutRows q_out;
+    const float *cosines, *sines;   // [angles, rotated / 2]
+    const int32_t *table;           // [S, table_stride]
+    int64_t table_stride;
+    const int32_t *ctx;             // [S]
+    const int32_t *rowptr;          // [S + 1]
+    const uint64_t *tree;           // [T] or null (a chain)
+    void *k_pages, *v_pages;
+    int64_t pages, page_stride, row_stride, head_stride;
+    float *k_scale, *v_scale;       // pools of codes only
+    int64_t scale_page, scale_block, scale_head;
+    int32_t block;
+    int32_t S, T, Hq, Hkv, D, page;
+    int32_t rotated, angles, interleaved;
+};
+int64_t append_threads(int held, const AppendArgs &a);
+hipError_t launch_append(int dtype, int held, const AppendArgs &a, hipStream_t stream);
 
 }  // namespace sdl

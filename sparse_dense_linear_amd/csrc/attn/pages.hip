@@ -3,6 +3,8 @@
 // moved byte is read and written once, 16 bytes a lane.
 #include "ops.h"
 
+#include "cache.h"
+#include "held.h"
 #include "tile.h"
 
 namespace sdl {
@@ -42,6 +44,12 @@ __global__ __launch_bounds__(kAttnThreads) void copy_kernel(PagesArgs a, int par
         const int64_t at = 16 * (int64_t)(threadIdx.x + i * kAttnThreads);
         if (at < left)
             __builtin_nontemporal_store(piece[i], (u32x4 *)(to + at));
+    }
+    if (a.k_scale != nullptr && begin == 0) {              // of pools of codes
+        float *scale = item / a.count / a.layers == 0 ? a.k_scale : a.v_scale;
+        const int64_t n = a.page / a.block * a.heads;
+        for (int64_t i = threadIdx.x; i < n; i += kAttnThreads)
+            scale[(layer * a.pages + dst) * n + i] = scale[(layer * a.pages + src) * n + i];
     }
 }
 
@@ -107,6 +115,147 @@ __global__ __launch_bounds__(kAttnThreads) void compact_kernel(PagesArgs a)
     }
 }
 
+constexpr int kCodeItems = 4;                                   // layers and pools of a workgroup
+constexpr int kCodeBatch = 64;                                  // rows found at once
+
+// Pools of codes.  Workgroup: one sequence, kCodeItems of its (layer, pool)
+// pairs; block after block of the positions that kept rows move to, in ascending
+// order, which is also the order of where they come from.  A thread takes a
+// 16-byte column, which belongs to one head, through the block's rows: first the
+// scales of where they come from, then the rows.  Rows are read no later than
+// anything is written over them, since a row never comes from before its place;
+// a block's scale is written when its rows have been read.
+template <class H>
+__global__ __launch_bounds__(kAttnThreads) void compact_codes(PagesArgs a)
+{
+    __shared__ int64_t from[kCodeBatch], to[kCodeBatch];      // rows of a layer; -1: nothing
+    __shared__ int first_end;
+    const int t = threadIdx.x;
+    const int64_t seq = blockIdx.x, first = (int64_t)blockIdx.y * kCodeItems;
+    const int items = (int)(2 * a.layers - first < kCodeItems ? 2 * a.layers - first : kCodeItems);
+    const uint32_t cols = (uint32_t)(a.row_bytes / 16), D = (uint32_t)(a.row_bytes / a.heads);
+    const int64_t layer_rows = a.pages * a.page, layer_scales = layer_rows / a.block * a.heads;
+    const int32_t *table = a.table + seq * a.table_stride, *keep = a.keep + seq * a.kept;
+    const int64_t ctx = a.ctx[seq];
+    // a position's row, -1 if it has none
+    auto row_at = [&](int64_t pos) -> int64_t {
+        if (pos < 0 || pos / a.page >= a.table_stride)
+            return -1;
+        const int64_t number = table[pos / a.page];
+        return number < 0 || number >= a.pages ? -1 : number * a.page + pos % a.page;
+    };
+    // kept rows: up to the first negative entry
+    if (t == 0)
+        first_end = (int)a.kept;
+    __syncthreads();
+    for (int64_t i = t; i < a.kept; i += kAttnThreads)
+        if (keep[i] < 0) {
+            atomicMin(&first_end, (int)i);
+            break;
+        }
+    __syncthreads();
+    const int64_t end = ctx + first_end;
+    for (int64_t begin = ctx / a.block * a.block; begin < end; begin += a.block) {
+        const int64_t lo = begin > ctx ? begin : ctx, hi = begin + a.block < end ? begin + a.block : end;
+        const int64_t block_row = row_at(begin);
+        if (block_row < 0)
+            continue;                          // the same for the whole workgroup
+        auto find = [&](int64_t p0) {          // rows p0 .. p0 + kCodeBatch - 1 of the block
+            __syncthreads();
+            if (t < kCodeBatch) {
+                const int64_t p = p0 + t;
+                const int64_t f = p < hi ? row_at(ctx + keep[p - ctx]) : -1;
+                from[t] = f;
+                to[t] = f < 0 ? -1 : block_row + (p - begin);
+            }
+            __syncthreads();
+        };
+        if (hi - lo <= kCodeBatch)
+            find(lo);
+        bool any = false;
+        // kMine columns to a thread, whole heads to a turn: no turn reads a scale
+        // that an earlier one has written
+        constexpr int kMine = 4;
+        const uint32_t wide_turn = kMine * kAttnThreads / (D / 16) * (D / 16);
+        for (uint32_t m0 = 0; m0 < cols * items; m0 += wide_turn) {
+            const uint32_t m1 = m0 + wide_turn < cols * items ? m0 + wide_turn : cols * items;
+            float scale[kMine], before[kMine];
+            char *pool[kMine];
+            float *scales[kMine];
+#pragma unroll
+            for (int c = 0; c < kMine; ++c) {
+                const uint32_t m = m0 + c * kAttnThreads + t, item = m / cols, col = m - item * cols;
+                const int64_t n = first + item;
+                const bool is_k = n < a.layers;
+                const int64_t layer = is_k ? n : n - a.layers;
+                pool[c] = nullptr;
+                if (m >= m1)
+                    continue;
+                pool[c] = (is_k ? a.k : a.v) + layer * layer_rows * a.row_bytes + 16 * (int64_t)col;
+                scales[c] = (is_k ? a.k_scale : a.v_scale) + layer * layer_scales + 16 * col / D;
+                before[c] = scales[c][block_row / a.block * a.heads];
+                scale[c] = lo > begin ? before[c] : 0.0f;
+            }
+            for (int64_t p0 = lo; p0 < hi; p0 += kCodeBatch) {
+                if (hi - lo > kCodeBatch)
+                    find(p0);
+                for (int i = 0; i < kCodeBatch && p0 + i < hi; ++i) {
+                    if (from[i] < 0)
+                        continue;
+                    any = true;
+#pragma unroll
+                    for (int c = 0; c < kMine; ++c)
+                        if (pool[c] != nullptr)
+                            scale[c] = larger_scale(scale[c], scales[c][from[i] / a.block * a.heads]);
+                }
+            }
+            if (!any)
+                break;                         // the same for the whole workgroup
+            auto convert = [&](int c, int64_t source, int64_t dest, float old) {
+                const u32x4 x = *(const u32x4 *)(pool[c] + source * a.row_bytes);
+                const Divide divide(scale[c]);
+                u32x4 y = x;
+                if (old != scale[c])
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f32x4 u = wide<H>(x[e]);
+                        y[e] = narrow<H>(divide(f32x4{u[0] * old, u[1] * old, u[2] * old, u[3] * old}));
+                    }
+                *(u32x4 *)(pool[c] + dest * a.row_bytes) = y;
+            };
+#pragma unroll
+            for (int c = 0; c < kMine; ++c)
+                if (pool[c] != nullptr && scale[c] != before[c])
+                    for (int64_t p = begin; p < lo; ++p)
+                        convert(c, block_row + (p - begin), block_row + (p - begin), before[c]);
+            for (int64_t p0 = lo; p0 < hi; p0 += kCodeBatch) {
+                if (hi - lo > kCodeBatch)
+                    find(p0);
+                for (int i = 0; i < kCodeBatch && p0 + i < hi; ++i) {
+                    if (from[i] < 0)
+                        continue;
+#pragma unroll
+                    for (int c = 0; c < kMine; ++c) {
+                        if (pool[c] == nullptr)
+                            continue;
+                        const float old = scales[c][from[i] / a.block * a.heads];
+                        if (from[i] != to[i] || old != scale[c])
+                            convert(c, from[i], to[i], old);
+                    }
+                }
+            }
+            __syncthreads();                   // all have read the scales
+#pragma unroll
+            for (int c = 0; c < kMine; ++c) {
+                const uint32_t m = m0 + c * kAttnThreads + t, col = m % cols;
+                if (pool[c] != nullptr && 16 * col % D == 0)
+                    scales[c][block_row / a.block * a.heads] = scale[c];
+            }
+        }
+        __syncthreads();                       // and written them
+    }
+}
+
 }  // namespace
 
 int64_t pages_copy_parts(int64_t page_bytes) { return (page_bytes + kCopyBytes - 1) / kCopyBytes; }
@@ -122,6 +271,16 @@ hipError_t launch_pages_compact(const PagesArgs &a, hipStream_t stream)
 {
     const dim3 grid((uint32_t)a.count, (uint32_t)((2 * a.layers + kItems - 1) / kItems));
     compact_kernel<<<grid, kAttnThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_cache_compact(int held, const PagesArgs &a, hipStream_t stream)
+{
+    const dim3 grid((uint32_t)a.count, (uint32_t)((2 * a.layers + kCodeItems - 1) / kCodeItems));
+    if (held == CACHE_E4M3)
+        compact_codes<E4M3><<<grid, kAttnThreads, 0, stream>>>(a);
+    else
+        compact_codes<Int8><<<grid, kAttnThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -282,8 +282,8 @@ __device__ bool odd_queries(const WindowArgs &a, int q_begin, int k_begin, int h
         for (int i = from + lane; i < to; i += 64)
             odd = odd || r.lse[i] != r.lse[i] || !finite(r.delta[i]);
         odd = __any(odd) ||
-              any_odd<T>([&](int i) { return r.q + (int64_t)i * r.q_stride; }, from, to, a.D, lane) ||
-              any_odd<T>([&](int i) { return r.dout + (int64_t)i * r.dout_stride; }, from, to, a.D, lane);
+              any_odd([&](int i) { return r.q + (int64_t)i * r.q_stride; }, from, to, a.D, lane) ||
+              any_odd([&](int i) { return r.dout + (int64_t)i * r.dout_stride; }, from, to, a.D, lane);
     }
     return odd;
 }
