@@ -214,6 +214,19 @@ spmm_status_t cache_tree_attn(int32_t dtype, int32_t held, const attn_tree_t *sh
     a.scale_page = scales->page_stride;
     a.scale_block = scales->block_stride;
     a.scale_head = scales->head_stride;
+    a.by_page = divisor((uint32_t)shape->page);
+    a.by_block = divisor((uint32_t)scales->block);
+    // 16 keys in one page, whose bytes are 32 bits apart at most, and four with one scale
+    a.together = shape->page % 16 == 0 && scales->block % 4 == 0 && shape->row_stride < ((int64_t)1 << 27);
+    if (a.block_rows == 16) {
+        // blocks of fewer rows where there are no more, each of several steps of keys
+        if (a.together)
+            a.block_rows = a.mean_rows <= 4 ? 4 : (a.mean_rows <= 8 ? 8 : 16);
+        a.tile_keys = 32 * (16 / a.block_rows) * (4 / a.wave_heads);
+        a.slot_rows = a.block_rows * a.wave_heads;
+        if ((st = check_threads(tree_threads(a))) != SPMM_SUCCESS)
+            return st;
+    }
     return launched(held == CACHE_E4M3 ? launch_tree_e4m3(dtype, a, (hipStream_t)stream)
                                        : launch_tree_int8(dtype, a, (hipStream_t)stream),
                     "tree attention over 8 bits");

@@ -40,8 +40,11 @@ __device__ inline bf16x4 wide_bf16(uint32_t w)
         const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3);
     } else {
+        // 8 bits lie in the upper half of a fp32
         const f32x4 x = wide<H>(w);
-        return bf16x4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+        const uint32_t a = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302);
+        const uint32_t b = __builtin_amdgcn_perm(__float_as_uint(x[3]), __float_as_uint(x[2]), 0x07060302);
+        return __builtin_bit_cast(bf16x4, (uint64_t)b << 32 | a);
     }
 }
 

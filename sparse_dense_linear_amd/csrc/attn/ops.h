@@ -65,6 +65,23 @@ int64_t window_bwd_delta_bytes(int64_t Tq, int64_t Hq);
 int64_t window_bwd_partial_bytes(int64_t S, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
                                  int64_t window, int64_t sinks);
 
+// x / d for 0 <= x < 2^31 is (x * factor) >> (31 + shift).
+struct Divisor {
+    uint32_t factor;
+    int32_t shift;
+};
+inline Divisor divisor(uint32_t d)
+{
+    int s = 0;
+    while (((uint64_t)1 << s) < d)
+        ++s;
+    return {(uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d), s};
+}
+
+// Workgroups of tree_codes.h to a CU, by the bytes of an element of q and the head's
+// size, that registers have room for.
+constexpr int stream_per_cu(int bytes, int DP) { return bytes == 2 && DP == 64 ? 3 : 2; }
+
 struct TreeArgs {
     const void *q;
     int64_t q_row, q_head;    // strides
@@ -82,16 +99,20 @@ struct TreeArgs {
     int32_t window, sinks;
     float scale;
     float *partial;
-    int32_t workers, block_rows;   // launch shape (tree_shape)
-    // pools of codes only: scales of blocks of positions, and their strides
+    int32_t workers, block_rows, slot_rows;   // launch shape (tree_shape)
+    // pools of codes only: key heads of a workgroup and keys of a tile, whether 16
+    // keys lie together (tree_codes.h),: scales of blocks of positions, and their strides
+    int32_t wave_heads, tile_keys, together, mean_rows;
     const float *k_scale, *v_scale;
     int64_t scale_page, scale_block, scale_head;
     int32_t block;
+    Divisor by_page, by_block;
 };
 
 // Workgroups of the split, queries of a workgroup, and the workspace.
 struct TreeShape {
-    int32_t workers, block_rows;
+    int32_t workers, block_rows, wave_heads;
+    int64_t rows;                  // queries that share a key head, of the mean sequence
     int64_t bytes;
 };
 TreeShape tree_shape(int dtype, int held, int64_t S, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D);

@@ -39,6 +39,19 @@ namespace {
 // each has half a tile.
 __host__ __device__ constexpr int tile_keys(int block_rows) { return block_rows == 16 ? 64 : 128; }
 
+// Key heads that are worked on together by one workgroup: more than one where
+// codes are streamed (tree_codes.h).
+template <class H>
+__device__ inline int wave_heads(const TreeArgs &a)
+{
+    if constexpr (kCodes<H>)
+        return a.wave_heads;
+    else
+        return 1;
+}
+template <class H>
+__device__ inline int key_groups(const TreeArgs &a) { return kCodes<H> ? a.Hkv / wave_heads<H>(a) : a.Hkv; }
+
 // What sequence s asks for.
 struct Unit {
     int q_begin, drafts, ctx, end;   // end: ctx + drafts
@@ -48,6 +61,7 @@ struct Unit {
     int tile_keys;
 };
 
+template <class H>
 __device__ inline Unit unit_of(const TreeArgs &a, int s)
 {
     Unit u;
@@ -56,7 +70,10 @@ __device__ inline Unit unit_of(const TreeArgs &a, int s)
     u.ctx = a.ctx[s];
     u.end = u.ctx + u.drafts;
     u.low = u.ctx - a.window + 1 > 0 ? u.ctx - a.window + 1 : 0;
-    u.tile_keys = tile_keys(a.block_rows);
+    if constexpr (kCodes<H>)
+        u.tile_keys = a.tile_keys;
+    else
+        u.tile_keys = tile_keys(a.block_rows);
     u.band = u.low / u.tile_keys;
     u.first_tiles = (a.sinks + u.tile_keys - 1) / u.tile_keys;
     u.first_tiles = u.first_tiles < u.band ? u.first_tiles : u.band;
@@ -188,7 +205,7 @@ struct Slots {
     {
         base = (int64_t *)a.partial;
         stat = a.partial + 2 * (((int64_t)a.S + 1 + 31) / 32 * 32);
-        out = stat + (int64_t)2 * a.workers * a.block_rows * 2;
+        out = stat + (int64_t)2 * a.workers * a.slot_rows * 2;
     }
 };
 
@@ -199,6 +216,7 @@ struct Span {
     int64_t base;          // first tile of the sequence
 
     // By all threads of the workgroup; false: it has none.
+    template <class H>
     __device__ bool begin(const TreeArgs &a, const Slots &slots)
     {
         __shared__ int64_t scan[4];
@@ -208,16 +226,18 @@ struct Span {
         // the total of all tiles, then the sequence
         Spans spans;
         spans.tiles = 0;
+        int64_t n = 0;
         for (int s0 = 0; s0 < a.S; s0 += kAttnThreads) {
-            int64_t n = 0;
+            n = 0;
             if (s0 + t < a.S) {
-                const Unit u = unit_of(a, s0 + t);
-                n = (int64_t)a.Hkv * u.blocks * u.tiles;
+                const Unit u = unit_of<H>(a, s0 + t);
+                n = (int64_t)key_groups<H>(a) * u.blocks * u.tiles;
             }
+            int64_t all = n;
             for (int d = 32; d > 0; d >>= 1)
-                n += __shfl_xor(n, d);
+                all += __shfl_xor(all, d);
             if (lane == 0)
-                scan[wave] = n;
+                scan[wave] = all;
             __syncthreads();
             spans.tiles += scan[0] + scan[1] + scan[2] + scan[3];
             __syncthreads();
@@ -230,10 +250,12 @@ struct Span {
         stop = spans.start(w + 1);
         int64_t sum = 0;
         for (int s0 = 0; s0 < a.S; s0 += kAttnThreads) {
-            int64_t n = 0;
-            if (s0 + t < a.S) {
-                const Unit u = unit_of(a, s0 + t);
-                n = (int64_t)a.Hkv * u.blocks * u.tiles;
+            if (a.S > kAttnThreads) {          // else as it was
+                n = 0;
+                if (s0 + t < a.S) {
+                    const Unit u = unit_of<H>(a, s0 + t);
+                    n = (int64_t)key_groups<H>(a) * u.blocks * u.tiles;
+                }
             }
             int64_t upto = n;                  // inclusive sum over the wavefront
             for (int d = 1; d < 64; d <<= 1) {
@@ -295,11 +317,11 @@ __device__ inline void finish(const TreeArgs &a, int64_t token, int head, int p,
 }
 
 // What finish() left to do in rows first .. first + count - 1 of a sequence's
-// query rows, by the four wavefronts of a workgroup; place: the drafts'
+// query rows, by the first `waves` wavefronts of a workgroup; place: the drafts'
 // positions.
 template <class T, class H>
 __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, int hk, int first, int count,
-                                    const int *redo, const Drafts &drafts, int wave, int lane)
+                                    const int *redo, const Drafts &drafts, int wave, int lane, int waves = 4)
 {
     const int group = a.Hq / a.Hkv;
     bool some = false, outputs = false;
@@ -317,7 +339,7 @@ __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, i
         too_large.look(val, rows, 0, a.sinks < u.low ? a.sinks : u.low, a.D, lane);
         too_large.look(val, rows, u.low, u.end, a.D, lane);
     }
-    for (int lr = wave; lr < count; lr += 4) {
+    for (int lr = wave; lr < count; lr += waves) {
         const int why = redo[lr];              // uniform over the wavefront
         if (why == 0)
             continue;
@@ -358,6 +380,65 @@ constexpr int per_cu(int block_rows)
     return tile <= 16384 ? 4 : (tile <= 32768 && block_rows == 16 ? 3 : (tile <= 65536 ? 2 : 1));
 }
 
+// Which part of which unit a workgroup has worked on: key tiles n0 .. n1 - 1, the
+// first or a later piece of its span.
+struct Piece {
+    int w, seq, hk, block, n0, n1;
+    bool later;
+};
+
+// Joins the wavefronts of each query group, whose outputs lie in lds (Tile<float,
+// DP, C> for each wavefront) with their maxima and sums, and writes: the unit's
+// results if the piece is all of it, else a slot.
+template <class T, class H, int DP, int DU, int C, int RG>
+__device__ inline void join_waves(const TreeArgs &a, const Unit &u, const Piece &c, const Slots &slots, const char *lds,
+                                  const float (&tops)[4][C], const float (&totals)[4][C], int *redo,
+                                  const Drafts &drafts, int wave, int lane)
+{
+    constexpr int KS = 4 / RG, RB = C * RG;
+    typedef Tile<float, DP, C> Out;
+    const int group = a.Hq / a.Hkv, rows = u.drafts * group;
+    const bool done = c.n0 == 0 && c.n1 == u.tiles;
+    const int64_t slot = 2 * (int64_t)c.w + (c.later ? 1 : 0);
+    constexpr int kOutPieces = DU / 4;
+    for (int m = threadIdx.x; m < RB * kOutPieces; m += kAttnThreads) {
+        const int lr = m / kOutPieces, p = m % kOutPieces;
+        const int rr = c.block * RB + lr;
+        if (rr >= rows)
+            break;
+        float best = SDL_NEG_INF;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+            best = fmaxf(best, tops[k * RG + lr / C][lr % C]);
+        const float ref = best == SDL_NEG_INF ? 0.0f : best;
+        float sum = 0.0f;
+        f32x4 o = f32x4(0.0f);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int wv = k * RG + lr / C;
+            const float f = __builtin_amdgcn_exp2f(tops[wv][lr % C] - ref);
+            sum = fmaf(f, totals[wv][lr % C], sum);
+            const f32x4 x = *(const f32x4 *)(lds + wv * Out::kBytes + Out::at(lr % C, p));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = fmaf(f, x[e], o[e]);
+        }
+        if (!done) {
+            float *to = slots.out + (slot * RB + lr) * DP + 4 * p;
+            *(f32x4 *)to = o;
+            if (p == 0) {
+                slots.stat[(slot * RB + lr) * 2] = best;
+                slots.stat[(slot * RB + lr) * 2 + 1] = sum;
+            }
+            continue;
+        }
+        finish<T>(a, u.q_begin + rr / group, c.hk * group + rr % group, p, best, sum, o, redo + lr);
+    }
+    __syncthreads();
+    if (done)
+        finish_again<T, H>(a, u, c.seq, c.hk, c.block * RB, RB, redo, drafts, wave, lane);
+}
+
 // RG groups of C queries; the 4 / RG wavefronts of a group share the keys of
 // a tile.
 template <class T, class H, int DP, int DU, int C, int RG>
@@ -391,7 +472,7 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_at
     const Slots slots(a);
 
     Span span;
-    if (!span.begin(a, slots))
+    if (!span.begin<H>(a, slots))
         return;
     const int w = span.w;
     int64_t at = span.at, base = span.base;
@@ -401,13 +482,13 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_at
     // ---- the units of the span, one piece after another
     int64_t piece_no = 0;
     while (at < stop) {
-        Unit u = unit_of(a, seq);
-        int64_t mine = (int64_t)a.Hkv * u.blocks * u.tiles;
+        Unit u = unit_of<H>(a, seq);
+        int64_t mine = (int64_t)key_groups<H>(a) * u.blocks * u.tiles;
         while (at >= base + mine) {            // the next sequence that has tiles
             base += mine;
             ++seq;
-            u = unit_of(a, seq);
-            mine = (int64_t)a.Hkv * u.blocks * u.tiles;
+            u = unit_of<H>(a, seq);
+            mine = (int64_t)key_groups<H>(a) * u.blocks * u.tiles;
         }
         const int unit = (int)Spans::divide(at - base, u.tiles);
         const int hk = unit / u.blocks, block = unit % u.blocks;
@@ -606,49 +687,52 @@ __global__ __launch_bounds__(kAttnThreads, (per_cu<T, DP>(C * RG))) void tree_at
                                  Out::at(lane % C, (C * d + Co::key_of(4 * g)) / 4 + part)),
                        O[d][4 * g], O[d][4 * g + 1], O[d][4 * g + 2], O[d][4 * g + 3]);
         __syncthreads();
-        const bool done = n0 == 0 && n1 == u.tiles;
-        const int64_t slot = 2 * (int64_t)w + (piece_no == 0 ? 0 : 1);
-        constexpr int kOutPieces = DU / 4;
-        for (int m = t; m < RB * kOutPieces; m += kAttnThreads) {
-            const int lr = m / kOutPieces, p = m % kOutPieces;
-            const int rr = block * RB + lr;
-            if (rr >= rows)
-                break;
-            float best = SDL_NEG_INF;
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-                best = fmaxf(best, tops[k * RG + lr / C][lr % C]);
-            const float ref = best == SDL_NEG_INF ? 0.0f : best;
-            float sum = 0.0f;
-            f32x4 o = f32x4(0.0f);
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const int wv = k * RG + lr / C;
-                const float f = __builtin_amdgcn_exp2f(tops[wv][lr % C] - ref);
-                sum = fmaf(f, totals[wv][lr % C], sum);
-                const f32x4 x = *(const f32x4 *)(lds + wv * Out::kBytes + Out::at(lr % C, p));
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[e] = fmaf(f, x[e], o[e]);
-            }
-            if (!done) {
-                float *to = slots.out + (slot * RB + lr) * DP + 4 * p;
-                *(f32x4 *)to = o;
-                if (p == 0) {
-                    slots.stat[(slot * RB + lr) * 2] = best;
-                    slots.stat[(slot * RB + lr) * 2 + 1] = sum;
-                }
-                continue;
-            }
-            finish<T>(a, u.q_begin + rr / group, hk * group + rr % group, p, best, sum, o, redo + lr);
-        }
-        __syncthreads();
-        if (done)
-            finish_again<T, H>(a, u, seq, hk, block * RB, RB, redo, drafts, wave, lane);
+        join_waves<T, H, DP, DU, C, RG>(a, u, {w, seq, hk, block, n0, n1, piece_no != 0}, slots, lds, tops, totals, redo,
+                                        drafts, wave, lane);
         at += n1 - n0;
         ++piece_no;
     }
 }
+
+// A unit that spans have cut, for its joining workgroup.
+struct Cut {
+    Unit u;
+    int seq, hk, block, w0, w1;      // spans w0 .. w1
+    int64_t slot0;                   // of the first; a unit that goes on is a span's first piece
+
+    // By each wavefront; false: nothing to join from row0 of the block on.
+    template <class H>
+    __device__ bool find(const TreeArgs &a, const Slots &slots, int numbers, int row0, int lane)
+    {
+        const int RB = a.block_rows, group = a.Hq / a.Hkv;
+        const int number = blockIdx.x % numbers;
+        hk = blockIdx.x / numbers;
+        const int64_t tiles = slots.base[a.S];
+        int left = a.S;              // the last sequence whose first number is <= number
+        seq = 0;
+        while (left > 1) {
+            const int step = (left + 63) / 64, s = seq + lane * step;
+            const bool at = lane * step < left && (int64_t)a.q_rowptr[s] * group / RB + s <= number;
+            const int n = __popcll(__ballot(at)) - 1;
+            if (n < 0)
+                return false;
+            seq += n * step;
+            left = left - n * step < step ? left - n * step : step;
+        }
+        u = unit_of<H>(a, seq);
+        block = number - (int)((int64_t)u.q_begin * group / RB + seq);
+        if (block < 0 || block >= u.blocks || block * RB + row0 >= u.drafts * group)
+            return false;
+        Spans spans;
+        spans.tiles = tiles;
+        spans.workers = tiles < a.workers ? (int)tiles : a.workers;
+        const int64_t from = slots.base[seq] + (int64_t)(hk / wave_heads<H>(a) * u.blocks + block) * u.tiles;
+        w0 = spans.of(from);
+        w1 = spans.of(from + u.tiles - 1);
+        slot0 = 2 * (int64_t)w0 + (spans.start(w0) >= from ? 0 : 1);
+        return w0 != w1;
+    }
+};
 
 constexpr int kJoinRows = 16;      // query rows of a joining workgroup
 
@@ -663,33 +747,13 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int number
     __shared__ Drafts drafts;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int RB = a.block_rows, group = a.Hq / a.Hkv;
-    const int hk = blockIdx.x / numbers, number = blockIdx.x % numbers;
-    const Slots slots(a);
-    const int64_t tiles = slots.base[a.S];
-    int seq = 0, left = a.S;                   // the last sequence whose first number is <= number
-    while (left > 1) {
-        const int step = (left + 63) / 64, s = seq + lane * step;
-        const bool at = lane * step < left && (int64_t)a.q_rowptr[s] * group / RB + s <= number;
-        const int n = __popcll(__ballot(at)) - 1;
-        if (n < 0)
-            return;
-        seq += n * step;
-        left = left - n * step < step ? left - n * step : step;
-    }
-    const Unit u = unit_of(a, seq);
-    const int block = number - (int)((int64_t)u.q_begin * group / RB + seq);
-    const int rows = u.drafts * group;
     const int row0 = blockIdx.y * kJoinRows;
-    if (block < 0 || block >= u.blocks || block * RB + row0 >= rows)
+    const Slots slots(a);
+    Cut cut;
+    if (!cut.find<H>(a, slots, numbers, row0, lane))
         return;
-    Spans spans;
-    spans.tiles = tiles;
-    spans.workers = tiles < a.workers ? (int)tiles : a.workers;
-    const int64_t from = slots.base[seq] + (int64_t)(hk * u.blocks + block) * u.tiles;
-    const int w0 = spans.of(from), w1 = spans.of(from + u.tiles - 1);
-    if (w0 == w1)
-        return;
-    const int64_t slot0 = 2 * (int64_t)w0 + (spans.start(w0) >= from ? 0 : 1);
+    const Unit &u = cut.u;
+    const int hk = cut.hk, block = cut.block, rows = u.drafts * group, heads = wave_heads<H>(a);
 
     if (t < kJoinRows)
         redo[t] = 0;
@@ -698,12 +762,12 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int number
     for (int m = t; m < kJoinRows * kOutPieces; m += kAttnThreads) {
         const int lr = m / kOutPieces, p = m % kOutPieces;
         const int r = block * RB + row0 + lr;
-        if (r >= rows)
+        if (r >= rows || row0 + lr >= RB)
             break;
         float best = SDL_NEG_INF, sum = 0.0f;
         f32x4 o = f32x4(0.0f);
         auto add = [&](int64_t slot) {
-            const int64_t row = slot * RB + row0 + lr;
+            const int64_t row = (slot * heads + hk % heads) * RB + row0 + lr;
             const float top = slots.stat[2 * row], total = slots.stat[2 * row + 1];
             const f32x4 x = *(const f32x4 *)(slots.out + row * DP + 4 * p);
             const float now = fmaxf(best, top), ref = now == SDL_NEG_INF ? 0.0f : now;
@@ -714,9 +778,9 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int number
             for (int e = 0; e < 4; ++e)
                 o[e] = fmaf(theirs, x[e], mine * o[e]);
         };
-        add(slot0);
+        add(cut.slot0);
 #pragma unroll 4
-        for (int w = w0 + 1; w <= w1; ++w)     // a unit that goes on is a span's first
+        for (int w = cut.w0 + 1; w <= cut.w1; ++w)     // a unit that goes on is a span's first
             add(2 * (int64_t)w);
         finish<T>(a, u.q_begin + r / group, hk * group + r % group, p, best, sum, o, redo + lr);
     }
@@ -726,38 +790,44 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int number
     if (wave == 0 && a.tree != nullptr)
         find_drafts(a, u, lane, drafts);
     __syncthreads();
-    finish_again<T, H>(a, u, seq, hk, block * RB + row0, kJoinRows, redo, drafts, wave, lane);
+    finish_again<T, H>(a, u, cut.seq, hk, block * RB + row0, kJoinRows, redo, drafts, wave, lane);
 }
 
 // Blocks of queries that the join numbers, of one key head.
 int64_t join_numbers(const TreeArgs &a) { return a.Tq * (a.Hq / a.Hkv) / a.block_rows + a.S; }
 
 template <class T, class H, int DP, int DU>
-hipError_t launch(const TreeArgs &a, hipStream_t stream)
+hipError_t launch_join(const TreeArgs &a, hipStream_t stream)
 {
-    if (a.block_rows == 16)
-        tree_attn<T, H, DP, DU, 16, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
-    else if (a.block_rows == 32)
-        tree_attn<T, H, DP, DU, 32, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
-    else if (a.block_rows == 64)
-        tree_attn<T, H, DP, DU, 32, 2><<<a.workers, kAttnThreads, 0, stream>>>(a);
-    else
-        tree_attn<T, H, DP, DU, 32, 4><<<a.workers, kAttnThreads, 0, stream>>>(a);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess)
         return err;
     const int64_t numbers = join_numbers(a);
-    tree_join<T, H, DP, DU><<<dim3((uint32_t)(numbers * a.Hkv), a.block_rows / kJoinRows), kAttnThreads, 0, stream>>>(
+    tree_join<T, H, DP, DU><<<dim3((uint32_t)(numbers * a.Hkv), (a.block_rows + kJoinRows - 1) / kJoinRows), kAttnThreads, 0, stream>>>(
         a, (int)numbers);
     return hipGetLastError();
 }
 
-// By the head's size, for q of type T.
-template <class T, class H>
+template <class T, int DP, int DU>
+hipError_t launch(const TreeArgs &a, hipStream_t stream)
+{
+    if (a.block_rows == 16)
+        tree_attn<T, T, DP, DU, 16, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    else if (a.block_rows == 32)
+        tree_attn<T, T, DP, DU, 32, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    else if (a.block_rows == 64)
+        tree_attn<T, T, DP, DU, 32, 2><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    else
+        tree_attn<T, T, DP, DU, 32, 4><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    return launch_join<T, T, DP, DU>(a, stream);
+}
+
+// By the head's size.
+template <class T>
 hipError_t launch_sized(const TreeArgs &a, hipStream_t stream)
 {
-    return a.D <= 64 ? launch<T, H, 64, 64>(a, stream)
-                     : (a.D <= 96 ? launch<T, H, 128, 96>(a, stream) : launch<T, H, 128, 128>(a, stream));
+    return a.D <= 64 ? launch<T, 64, 64>(a, stream)
+                     : (a.D <= 96 ? launch<T, 128, 96>(a, stream) : launch<T, 128, 128>(a, stream));
 }
 
 }  // namespace
