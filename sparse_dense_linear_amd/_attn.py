@@ -5,7 +5,9 @@ from __future__ import annotations
 import ctypes
 import math
 from array import array
+from functools import lru_cache
 from operator import index
+from struct import Struct
 
 from ._binding import DTYPE_BF16, DTYPE_F32, _check, _torch, lib
 
@@ -45,6 +47,10 @@ class _CodePool(ctypes.Structure):
                 ("block", ctypes.c_int64), ("heads", ctypes.c_int64)]
 
 
+#: The structures as packed bytes, which cost a call less than ctypes structures.
+_PACK_TREE, _PACK_SCALES, _PACK_ROWS = Struct("12qfi"), Struct("6q"), Struct("3q")
+_PACK_POOL, _PACK_CODE_POOL = Struct("6q"), Struct("10q")
+
 #: What a pool holds (include/cache.h).
 CACHE_AS_IS, CACHE_E4M3, CACHE_INT8 = 0, 1, 2
 
@@ -54,12 +60,14 @@ _ROWS = ctypes.sizeof(_Rows)
 
 _ready = None
 torch = None
+_Tensor = _device_index = None
 
 
 def _lib():
-    global _ready, torch
+    global _ready, torch, _Tensor, _device_index
     if _ready is None:
         torch = _torch()
+        _Tensor, _device_index = torch.Tensor, torch._C._cuda_getDevice
         L = lib()
         P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
         L.window_attn_fwd.argtypes = [I32] + [P] * 9 + [I64, P]
@@ -92,12 +100,13 @@ class _On:
 
     def __init__(self, device, stream):
         cuda = torch.cuda
-        self.guards = []
-        if cuda.current_device() != device.index:
-            self.guards.append(cuda.device(device))
+        self.guards = ()
+        if _device_index() != device.index:
+            self.guards = [cuda.device(device)]
         if stream is None:
             self.handle = torch._C._cuda_getCurrentRawStream(device.index)
         else:
+            self.guards = list(self.guards)
             if stream.device != device:
                 raise ValueError("stream is on another device than the operands")
             self.guards.append(cuda.stream(stream))
@@ -148,13 +157,17 @@ def _codes(t, name) -> int:
 
 
 def _with(t, name, device):
-    _is_tensor(t, name)
-    if t.device != device:
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != device.index:
         raise ValueError(f"{name} must live on the same GPU as the other operands")
 
 
 def _index(t, name, device, dtype, shape):
     """The address of a contiguous array."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device.index and t.shape == shape and \
+            t.is_contiguous():
+        return t.data_ptr() or None
     _with(t, name, device)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
@@ -168,10 +181,10 @@ def _index(t, name, device, dtype, shape):
 def _rows(out, t, name, device, dtype, shape):
     """Adds the description of t [rows, heads, D], with any row and head
     strides and D contiguous, to the list `out`."""
-    _with(t, name, device)
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must have the element type of q")
-    if t.shape != shape:
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device.index and t.shape == shape):
+        _with(t, name, device)
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must have the element type of q")
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     n, h, d = shape
     rs, hs, ds = t.stride()
@@ -195,7 +208,11 @@ def _apart(r, outs, names):
 
 
 def _scale(scale, d) -> float:
-    return 1.0 / math.sqrt(d or 1) if scale is None else float(scale)
+    if scale is None:
+        return 1.0 / math.sqrt(d or 1)
+    scale = float(scale)
+    # past the range of fp32: as infinite
+    return scale if not abs(scale) > 3.4028234663852886e38 else math.copysign(math.inf, scale)
 
 
 def _window_size(window) -> int:
@@ -360,8 +377,9 @@ def window_attention_backward(dout, q, k, v, o, lse, q_rowptr, k_rowptr=None, wi
 
 def _paging(k_pages, v_pages, D):
     """Pages, page, heads and strides of two pools [pages, page, heads, D]."""
-    pages, page, Hkv, Dk = k_pages.shape
-    if v_pages.shape != k_pages.shape or Dk != D:
+    shape = k_pages.shape
+    pages, page, Hkv, Dk = shape
+    if v_pages.shape != shape or Dk != D:
         raise ValueError("the pools must have one shape, with the D of q")
     if page < 1:
         raise ValueError("a page must hold at least one position")
@@ -376,12 +394,12 @@ def _paging(k_pages, v_pages, D):
 
 
 def _scales(k_scale, v_scale, device, pages, page, heads):
-    """cache_scales_t of scales [pages, page / block, heads], with any strides."""
+    """cache_scales_t, packed, of scales [pages, page / block, heads], with any strides."""
     _with(k_scale, "k_scale", device)
     _with(v_scale, "v_scale", device)
     if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
         raise TypeError("the scales must be float32")
-    shape = k_scale.shape
+    shape = tuple(k_scale.shape)
     if len(shape) != 3 or v_scale.shape != shape or shape[0] != pages or shape[2] != heads:
         raise ValueError("the scales must have one shape: pages, blocks of a page, heads")
     blocks = shape[1]
@@ -390,7 +408,20 @@ def _scales(k_scale, v_scale, device, pages, page, heads):
     ps, bs, hs = k_scale.stride()
     if v_scale.stride() != (ps, bs, hs) and pages and heads:
         raise ValueError("the scales must have the same strides")
-    return _Scales(k_scale.data_ptr() or None, v_scale.data_ptr() or None, page // blocks, ps, bs, hs)
+    return _PACK_SCALES.pack(k_scale.data_ptr(), v_scale.data_ptr(), page // blocks, ps, bs, hs)
+
+
+@lru_cache(maxsize=1024)
+def _tree_scratch(dt, kind, w) -> int:
+    """Scratch bytes for a packed attn_tree_t: by sizes alone, asked for once."""
+    need = ctypes.c_int64()
+    if kind == CACHE_AS_IS:
+        st, name = _ready.tree_attn_scratch(dt, w, ctypes.addressof(need)), "tree_attn_scratch"
+    else:
+        st, name = _ready.cache_tree_attn_scratch(dt, kind, w, ctypes.addressof(need)), "cache_tree_attn_scratch"
+    if st:
+        _check(st, name)
+    return need.value
 
 
 # ------------------------------------------------------------------- tree
@@ -420,7 +451,7 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
             raise TypeError("tree must hold 64-bit masks (int64 or uint64)")
         tp = _index(tree, "tree", device, tree.dtype, (Tq,))
     lp = _index(lse, "lse", device, torch.float32, (Hq, Tq))
-    held = k_scale is not None or v_scale is not None
+    held, kind = k_scale is not None or v_scale is not None, CACHE_AS_IS
     if held:
         kind = _codes(k_pages, "k_pages")
         if v_pages.dtype is not k_pages.dtype or o.dtype is not q.dtype:
@@ -430,34 +461,24 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
     pages, page, Hkv, ps, rs, hs = _paging(k_pages, v_pages, D)
     if o.shape != q.shape or not o.is_contiguous():
         raise ValueError("o must be contiguous, with the shape of q")
-    w = _Tree(S, Tq, Hq, Hkv, D, page, ps, rs, hs, table.shape[1], _window_size(window), _sinks(sinks),
-              _scale(scale, D), 0)
+    w = _PACK_TREE.pack(S, Tq, Hq, Hkv, D, page, ps, rs, hs, table.shape[1], _window_size(window), _sinks(sinks),
+                        _scale(scale, D), 0)
     r = []
     _rows(r, q, "q", device, q.dtype, q.shape)
     op = o.data_ptr()
     if op and op == r[0]:
         raise ValueError("o must not overlap q")
-    r = array("q", r)
-    need, shape = ctypes.c_int64(), ctypes.addressof(w)
+    need = _tree_scratch(dt, kind, w)
+    scratch = torch.empty(need, dtype=torch.uint8, device=device)
+    kp, vp, sp = k_pages.data_ptr() or None, v_pages.data_ptr() or None, scratch.data_ptr() or None
+    r = _PACK_ROWS.pack(*r)
     if held:
         scales = _scales(k_scale, v_scale, device, pages, page, Hkv)
-        st = _ready.cache_tree_attn_scratch(dt, kind, shape, ctypes.addressof(need))
-        if st:
-            _check(st, "cache_tree_attn_scratch")
-        scratch = torch.empty(need.value, dtype=torch.uint8, device=device)
-        st = _ready.cache_tree_attn(dt, kind, shape, r.buffer_info()[0], k_pages.data_ptr() or None,
-                                    v_pages.data_ptr() or None, ctypes.addressof(scales), bp, cp, qp, tp,
-                                    op or None, lp, scratch.data_ptr() or None, need.value, handle)
+        st = _ready.cache_tree_attn(dt, kind, w, r, kp, vp, scales, bp, cp, qp, tp, op or None, lp, sp, need, handle)
         if st:
             _check(st, "cache_tree_attn")
         return
-    st = _ready.tree_attn_scratch(dt, shape, ctypes.addressof(need))
-    if st:
-        _check(st, "tree_attn_scratch")
-    scratch = torch.empty(need.value, dtype=torch.uint8, device=device)
-    st = _ready.tree_attn_paged(dt, shape, r.buffer_info()[0], k_pages.data_ptr() or None,
-                                v_pages.data_ptr() or None, bp, cp, qp, tp, op or None, lp,
-                                scratch.data_ptr() or None, need.value, handle)
+    st = _ready.tree_attn_paged(dt, w, r, kp, vp, bp, cp, qp, tp, op or None, lp, sp, need, handle)
     if st:
         _check(st, "tree_attn_paged")
 
@@ -496,7 +517,7 @@ def tree_attention(q, k_pages, v_pages, table, ctx, q_rowptr, tree=None, window=
     records no autograd graph."""
     device = _first(q, "q", 3, "three dimensions: rows, heads, D")
     with _On(device, stream) as handle:
-        o = torch.empty(q.shape, dtype=q.dtype, device=device)
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
         lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=device)
         _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks, scale, k_scale,
               v_scale, device, handle)
@@ -506,8 +527,8 @@ def tree_attention(q, k_pages, v_pages, table, ctx, q_rowptr, tree=None, window=
 # ------------------------------------------------------------------ pages
 
 def _pool(k_pool, v_pool, one=False):
-    """attn_pool_t of pools [layers, pages, page, ...], contiguous, of one
-    shape and type, that do not overlap (one: or are one), and their device."""
+    """The fields of attn_pool_t of pools [layers, pages, page, ...], contiguous, of
+    one shape and type, that do not overlap (one: or are one), and their device."""
     _lib()
     _is_tensor(k_pool, "k_pool")
     device = k_pool.device
@@ -526,12 +547,12 @@ def _pool(k_pool, v_pool, one=False):
     kp, vp = k_pool.data_ptr(), v_pool.data_ptr()
     if abs(kp - vp) < layers * pages * page * row and not (one and kp == vp):
         raise ValueError("the pools must not overlap")
-    return _Pool(kp or None, vp or None, layers, pages, page, row), device
+    return (kp, vp, layers, pages, page, row), device
 
 
 def _code_pool(pool, k_pool, k_scale, v_scale, device):
-    """cache_pool_t of pools of codes [layers, pages, page, heads, D] and their
-    scales [layers, pages, page / block, heads], contiguous."""
+    """cache_pool_t, packed, of pools of codes [layers, pages, page, heads, D] and
+    their scales [layers, pages, page / block, heads], contiguous."""
     if k_pool.dim() != 5:
         raise ValueError("a pool with scales must have five dimensions: layers, pages, page, heads, D")
     _codes(k_pool, "k_pool")
@@ -549,10 +570,10 @@ def _code_pool(pool, k_pool, k_scale, v_scale, device):
     if blocks < 1 or page % blocks:
         raise ValueError("the blocks of a page must divide its positions")
     ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    same = pool.k == pool.v
+    same = pool[0] == pool[1]
     if (ks == vs) != same or (not same and abs(ks - vs) < 4 * layers * pages * blocks * heads):
         raise ValueError("the scales must not overlap, or be one where the pools are")
-    return _CodePool(pool, ks or None, vs or None, max(1, page // blocks), heads)
+    return _PACK_CODE_POOL.pack(*pool, ks, vs, max(1, page // blocks), heads)
 
 
 def copy_pages(k_pool, v_pool, src, dst, stream=None, k_scale=None, v_scale=None) -> None:
@@ -566,13 +587,15 @@ def copy_pages(k_pool, v_pool, src, dst, stream=None, k_scale=None, v_scale=None
     held = k_scale is not None or v_scale is not None
     if held:
         pool = _code_pool(pool, k_pool, k_scale, v_scale, device)
+    else:
+        pool = _PACK_POOL.pack(*pool)
     _is_tensor(src, "src")
     n = src.numel()
     sp = _index(src, "src", device, torch.int32, (n,))
     dp = _index(dst, "dst", device, torch.int32, (n,))
     with _On(device, stream) as handle:
         copy = _ready.cache_copy if held else _ready.pages_copy
-        st = copy(ctypes.addressof(pool), sp, dp, n, handle)
+        st = copy(pool, sp, dp, n, handle)
     if st:
         _check(st, "cache_copy" if held else "pages_copy")
 
@@ -589,6 +612,8 @@ def compact_pages(k_pool, v_pool, table, ctx, keep, stream=None, k_scale=None, v
     held = k_scale is not None or v_scale is not None
     if held:
         pool, kind = _code_pool(pool, k_pool, k_scale, v_scale, device), _codes(k_pool, "k_pool")
+    else:
+        pool = _PACK_POOL.pack(*pool)
     _is_tensor(table, "table")
     _is_tensor(ctx, "ctx")
     _is_tensor(keep, "keep")
@@ -601,8 +626,8 @@ def compact_pages(k_pool, v_pool, table, ctx, keep, stream=None, k_scale=None, v
     kp = _index(keep, "keep", device, torch.int32, (S, kept))
     with _On(device, stream) as handle:
         if held:
-            st = _ready.cache_compact(kind, ctypes.addressof(pool), bp, wide, cp, kp, S, kept, handle)
+            st = _ready.cache_compact(kind, pool, bp, wide, cp, kp, S, kept, handle)
         else:
-            st = _ready.pages_compact(ctypes.addressof(pool), bp, wide, cp, kp, S, kept, handle)
+            st = _ready.pages_compact(pool, bp, wide, cp, kp, S, kept, handle)
     if st:
         _check(st, "cache_compact" if held else "pages_compact")

@@ -3,10 +3,10 @@ argument marshalling only."""
 from __future__ import annotations
 
 import ctypes
-from array import array
+from struct import Struct
 
 from . import _attn
-from ._attn import (_ROWS, CACHE_AS_IS, _codes, _dtype, _first, _index, _is_tensor, _On, _paging, _rows, _scales,
+from ._attn import (_PACK_ROWS, CACHE_AS_IS, _codes, _dtype, _first, _index, _is_tensor, _On, _paging, _rows, _scales,
                     _with)
 from ._binding import _check
 
@@ -17,17 +17,19 @@ class _Append(ctypes.Structure):
         "rotated", "angles")] + [("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+_PACK_APPEND = Struct("13q2i")
+
+
 def _tables(cos, sin, device):
     """Addresses of the tables of the rotation, their rows and twice their columns."""
     if cos is None and sin is None:
         return None, None, 0, 0
-    _with(cos, "cos", device)
-    _with(sin, "sin", device)
-    if cos.dim() != 2:
+    _is_tensor(cos, "cos")
+    shape = tuple(cos.shape)
+    if len(shape) != 2:
         raise ValueError("cos must have two dimensions: positions, pairs")
     f32 = _attn.torch.float32
-    return (_index(cos, "cos", device, f32, cos.shape), _index(sin, "sin", device, f32, cos.shape),
-            cos.shape[0], 2 * cos.shape[1])
+    return _index(cos, "cos", device, f32, shape), _index(sin, "sin", device, f32, shape), shape[0], 2 * shape[1]
 
 
 def append_pages(k, v, k_pages, v_pages, table, ctx, rowptr, q=None, cos=None, sin=None, tree=None,
@@ -59,8 +61,8 @@ def append_pages(k, v, k_pages, v_pages, table, ctx, rowptr, q=None, cos=None, s
     dt = _dtype(k, "k")
     _with(k_pages, "k_pages", device)
     _with(v_pages, "v_pages", device)
-    _with(table, "table", device)
-    _with(ctx, "ctx", device)
+    _is_tensor(table, "table")
+    _is_tensor(ctx, "ctx")
     if k_pages.dim() != 4:
         raise ValueError("the pools must have four dimensions: pages, page, heads, D")
     if table.dim() != 2:
@@ -102,20 +104,19 @@ def append_pages(k, v, k_pages, v_pages, table, ctx, rowptr, q=None, cos=None, s
             if Hq < 1:
                 raise ValueError("q must have heads")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
             _rows(r, q, "q", device, k.dtype, q.shape)
             _rows(r, q_out, "q_out", device, k.dtype, q.shape)
             if r[9] and (r[9] in (r[0], r[3]) or (r[9] == r[6] and r[10:] != r[7:9])):
                 raise ValueError("q_out must not overlap k or v, and be q itself or apart from it")
         elif q_out is not None:
             raise ValueError("q_out goes with q")
-        a = array("q", r)
-        at = a.buffer_info()[0]
-        w = _Append(S, T, Hq, Hkv, D, page, pages, ps, rs, hs, table.shape[1], rotated, angles, bool(interleaved), 0)
+        pack = _PACK_ROWS.pack
+        w = _PACK_APPEND.pack(S, T, Hq, Hkv, D, page, pages, ps, rs, hs, table.shape[1], rotated, angles,
+                              bool(interleaved), 0)
         st = _attn._ready.cache_append(
-            dt, held, ctypes.addressof(w), at + 2 * _ROWS if Hq else None, at, at + _ROWS, cosp, sinp, bp, cp, rp, tp,
-            k_pages.data_ptr() or None, v_pages.data_ptr() or None, ctypes.addressof(scales) if scales else None,
-            at + 3 * _ROWS if Hq else None, handle)
+            dt, held, w, pack(*r[6:9]) if Hq else None, pack(*r[:3]), pack(*r[3:6]), cosp, sinp, bp, cp, rp, tp,
+            k_pages.data_ptr() or None, v_pages.data_ptr() or None, scales, pack(*r[9:]) if Hq else None, handle)
     if st:
         _check(st, "cache_append")
     return q_out
