@@ -226,6 +226,8 @@ spmm_status_t cache_tree_attn(int32_t dtype, int32_t held, const attn_tree_t *sh
         a.slot_rows = a.block_rows * a.wave_heads;
         if ((st = check_threads(tree_threads(a))) != SPMM_SUCCESS)
             return st;
+    } else {
+        a.tile_keys = 128;
     }
     return launched(held == CACHE_E4M3 ? launch_tree_e4m3(dtype, a, (hipStream_t)stream)
                                        : launch_tree_int8(dtype, a, (hipStream_t)stream),

@@ -202,7 +202,6 @@ spmm_status_t check_tree_call(int32_t dtype, int32_t held, const attn_tree_t *sh
     a.block_rows = sh.block_rows;
     a.slot_rows = sh.block_rows * sh.wave_heads;
     a.wave_heads = sh.wave_heads;
-    a.tile_keys = 128;
     a.mean_rows = (int32_t)(sh.rows < 128 ? sh.rows : 128);
     return check_threads(tree_threads(a));
 }

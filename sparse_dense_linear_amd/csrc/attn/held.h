@@ -48,6 +48,22 @@ __device__ inline bf16x4 wide_bf16(uint32_t w)
     }
 }
 
+// The same times a scale that is a power of two (or 0, for codes that are 0).
+template <class H>
+__device__ inline bf16x4 wide_scaled(uint32_t w, float scale)
+{
+    if constexpr (std::is_same_v<H, E4M3>) {
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
+        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3);
+    } else {
+        const f32x4 x = wide<H>(w) * scale;
+        const uint32_t a = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302);
+        const uint32_t b = __builtin_amdgcn_perm(__float_as_uint(x[3]), __float_as_uint(x[2]), 0x07060302);
+        return __builtin_bit_cast(bf16x4, (uint64_t)b << 32 | a);
+    }
+}
+
 // Largest value of a code, and the codes of four values that are divided by
 // their scale already (no larger than that, or no number), to nearest even.
 template <class H> inline constexpr float kMost = std::is_same_v<H, E4M3> ? 448.0f : 127.0f;

@@ -16,6 +16,10 @@ TreeShape tree_shape(int dtype, int held, int64_t S, int64_t Tq, int64_t Hq, int
     if (held != 0 && sh.block_rows == 16) {
         sh.workers = 256 * stream_per_cu(dtype == SPMM_DTYPE_BF16 ? 2 : 4, DP);
         sh.wave_heads = Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1);
+    } else if (held != 0) {
+        sh.workers = 256 * 2;                  // tree_tiles
+        if (dtype != SPMM_DTYPE_BF16 && sh.block_rows > 64)
+            sh.block_rows = 64;
     } else if (dtype == SPMM_DTYPE_BF16) {
         sh.workers = 256 * (DP == 64 ? per_cu<__bf16, 64>(sh.block_rows) : per_cu<__bf16, 128>(sh.block_rows));
     } else {

@@ -613,6 +613,326 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
     }
 }
 
+// Blocks of 32 to 128 query rows, RG groups of C of them; the 4 / RG wavefronts of a
+// group share the keys of a tile.  Tiles of 128 keys are widened to bf16 on their way
+// into LDS, once for all query groups; the next tile is under way while one is worked
+// on.  Where all scales of a tile are powers of two that cannot leave bf16's range, as
+// append writes them, they go into the widening, which is exact still; else they are
+// applied to scores and weights.
+// q in fp32 is taken in three bf16 parts, weights too (tree_stream).
+// (Two buffers of 64 keys with one barrier to a tile instead of two: prompt pieces 418
+// us against 355, most of it the finding and widening of rows, which every tile
+// waits for.)
+constexpr int kTileKeys8 = 128;
+
+template <class T, class H, int DP, int DU, int C, int RG>
+__global__ __launch_bounds__(kAttnThreads, 2) void tree_tiles(TreeArgs a)
+{
+    constexpr int KS = 4 / RG, RB = C * RG, KEYS = kTileKeys8;
+    constexpr int QP = sizeof(T) == 4 ? 3 : 1;
+    typedef Cols<__bf16, DP, DU, KEYS, C> Co;
+    typedef typename Co::Acc Acc;
+    constexpr int STEPS = Co::kSteps, DB = Co::kBlocks;
+    typedef Tile<__bf16, DP, KEYS> Tl;
+    typedef Tile<float, DP, C> Out;
+    constexpr int kPieces = DP / 16, kPiecesPer = KEYS * kPieces / kAttnThreads;
+    constexpr int kBytes = 2 * Tl::kBytes > 4 * Out::kBytes ? 2 * Tl::kBytes : 4 * Out::kBytes;
+    static_assert(kPiecesPer * kAttnThreads == KEYS * kPieces, "whole pieces per thread");
+    static_assert(KEYS / C % KS == 0, "keys for every wavefront of a group");
+    __shared__ __align__(16) char lds[kBytes];
+    __shared__ Drafts drafts;
+    __shared__ float tops[4][C], totals[4][C];
+    __shared__ int redo[RB];
+    __shared__ int64_t place_of[2][KEYS];          // of a tile's rows, in the pools
+    __shared__ __align__(16) float scale_of[2][2][KEYS];
+    __shared__ int folds[2][2];                    // whether the scales of half a tile go into its rows
+    __shared__ int strange;                        // an infinite scale, which has no second part (tree_stream)
+
+    const int t = threadIdx.x, lane = t & 63, part = lane / C;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int group = a.Hq / a.Hkv;
+    const int rg = wave % RG, ks = wave / RG;
+    const float c2 = a.scale * kLog2e;
+    const Slots slots(a);
+
+    Span span;
+    if (!span.begin<H>(a, slots))
+        return;
+    int64_t at = uniform(span.at), base = uniform(span.base);
+    const int64_t stop = uniform(span.stop);
+    int seq = __builtin_amdgcn_readfirstlane(span.seq);
+    bool later = false;
+    while (at < stop) {
+        Unit u = unit_of<H>(a, seq);
+        int64_t mine = (int64_t)a.Hkv * u.blocks * u.tiles;
+        while (at >= base + mine) {            // the next sequence that has tiles
+            base += mine;
+            ++seq;
+            u = unit_of<H>(a, seq);
+            mine = (int64_t)a.Hkv * u.blocks * u.tiles;
+        }
+        const int unit = (int)Spans::divide(at - base, u.tiles);
+        const int hk = unit / u.blocks, block = unit % u.blocks;
+        const int n0 = (int)(at - base - (int64_t)unit * u.tiles);
+        const int n1 = stop - at < u.tiles - n0 ? n0 + (int)(stop - at) : u.tiles;
+        const int rows = u.drafts * group;
+
+        __syncthreads();
+        if (t < RB)
+            redo[t] = 0;
+        if (t == 0)
+            strange = 0;
+        if (wave == 3 && a.tree != nullptr)    // (the first one finds the rows)
+            find_drafts(a, u, lane, drafts);
+
+        // this lane's query
+        const int r = block * RB + C * rg + lane % C;
+        const int token = (r < rows ? r : rows - 1) / group, head = hk * group + (r < rows ? r : rows - 1) % group;
+        DraftSeen seen;
+        seen.ctx = u.ctx;
+        seen.drafts = u.drafts;
+        seen.window = a.window;
+        seen.sinks = a.sinks;
+        seen.mask = a.tree != nullptr ? draft_mask(a.tree[u.q_begin + token], u.drafts) : 0;
+        seen.pos = a.tree != nullptr ? draft_place(u.ctx, seen.mask) : u.ctx + token;
+        seen.place = a.tree != nullptr ? drafts.place : nullptr;
+        const T *q = (const T *)a.q + (int64_t)(u.q_begin + token) * a.q_row + head * a.q_head;
+        bf16x8 qf[STEPS][QP];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int d = Co::kTerms * s + 8 * part;
+            const Frag<T> x = d < a.D ? load8(q + d) : zero_frag<T>();
+            if constexpr (QP == 1)
+                qf[s][0] = x;
+            else
+                split<QP>(x, qf[s]);
+        }
+
+        Acc O[DB];
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+            O[d] = Acc(0.0f);
+        float top = SDL_NEG_INF, total = 0.0f;
+
+        // A chain's block ends where its last row stands: later tiles hold nothing for it,
+        // later keys nothing for a wavefront.
+        int e1 = n1, last_pos = u.end - 1;
+        if (a.tree == nullptr) {
+            auto stands = [&](int last) { return u.ctx + (last < rows ? last : rows - 1) / group; };
+            last_pos = stands(block * RB + C * rg + C - 1);
+            const int e = u.first_tiles + stands(block * RB + RB - 1) / KEYS - u.band + 1;
+            e1 = e < n1 ? (e > n0 ? e : n0) : n1;
+        }
+        const int32_t *table = a.table + (int64_t)seq * a.table_stride;
+        const H *kp = (const H *)a.k_pages + hk * a.head_stride, *vp = (const H *)a.v_pages + hk * a.head_stride;
+        struct Rows {                          // a thread's share of a tile on its way
+            u32x4 k[kPiecesPer], v[kPiecesPer];
+        };
+        int id = 0, in_page = 0;               // in_page < 0: a row that is not read
+        float scale_k = 0.0f, scale_v = 0.0f;
+        auto whole = [&](int n) { return all_seen(a, u, first_key(u, n), first_key(u, n) + KEYS - 1); };
+        auto find_row = [&](int n) {
+            const int j = first_key(u, n) + t;
+            in_page = -1;
+            if (whole(n) || seen_rows(a, u, drafts)(j)) {
+                const int p = divided(j, a.by_page);
+                in_page = j - p * a.page;
+                id = table[p];
+            }
+        };
+        auto keep_row = [&](int n) {
+            place_of[n & 1][t] = in_page < 0 ? -1 : (int64_t)id * a.page_stride + (int64_t)in_page * a.row_stride;
+            scale_k = scale_v = 0.0f;
+            if (in_page >= 0) {
+                const int64_t s =
+                    (int64_t)id * a.scale_page + divided(in_page, a.by_block) * a.scale_block + hk * a.scale_head;
+                scale_k = a.k_scale[s];
+                scale_v = a.v_scale[s];
+            }
+        };
+        auto folding = [](float s) {           // 2^-100 .. 2^100, or a row that is not read
+            const uint32_t b = __float_as_uint(s);
+            return b == 0 || ((b & 0x807fffff) == 0 && b >> 23 >= 27 && b >> 23 <= 227);
+        };
+        auto keep_scales = [&](int n) {
+            scale_of[n & 1][0][t] = scale_k;
+            scale_of[n & 1][1][t] = scale_v;
+            const bool all = __all(folding(scale_k) && folding(scale_v)), odd = __any(!finite(scale_v));
+            if (lane == 0) {
+                folds[n & 1][wave] = all;
+                if (odd)
+                    strange = 1;
+            }
+        };
+        auto fetch = [&](int n, Rows &to) {
+            const int tt = renewed(t);
+            int64_t from[kPiecesPer];          // all of them before the loads, which then go out together
+#pragma unroll
+            for (int i = 0; i < kPiecesPer; ++i)
+                from[i] = place_of[n & 1][(tt + i * kAttnThreads) / kPieces];
+            auto load = [&](bool all) {
+#pragma unroll
+                for (int i = 0; i < kPiecesPer; ++i) {
+                    const int p = (tt + i * kAttnThreads) % kPieces;
+                    const int d = p * 16 < a.D ? p * 16 : a.D - 16;
+                    if (!all) {
+                        to.k[i] = u32x4(0);
+                        to.v[i] = u32x4(0);
+                    }
+                    if (all || from[i] >= 0) {
+                        to.k[i] = *(const u32x4 *)(kp + from[i] + d);
+                        to.v[i] = *(const u32x4 *)(vp + from[i] + d);
+                    }
+                }
+            };
+            if (whole(n))
+                load(true);
+            else
+                load(false);
+        };
+        auto put = [&](int n, const Rows &of) {
+            char *kt = lds, *vt = kt + Tl::kBytes;
+            const bool fold = (folds[n & 1][0] & folds[n & 1][1]) != 0;
+#pragma unroll
+            for (int i = 0; i < kPiecesPer; ++i) {
+                const int m = t + i * kAttnThreads, row = m / kPieces, p = m % kPieces;
+                const float sk = fold ? scale_of[n & 1][0][row] : 1.0f, sv = fold ? scale_of[n & 1][1][row] : 1.0f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // (new to the compiler here, which else widens all pieces first and
+                    // has no registers for them)
+                    uint32_t k[2] = {of.k[i][2 * h], of.k[i][2 * h + 1]}, v[2] = {of.v[i][2 * h], of.v[i][2 * h + 1]};
+                    asm volatile("" : "+v"(k[0]), "+v"(k[1]), "+v"(v[0]), "+v"(v[1]) : : "memory");
+                    const auto k0 = wide_scaled<H>(k[0], sk), k1 = wide_scaled<H>(k[1], sk);
+                    const auto v0 = wide_scaled<H>(v[0], sv), v1 = wide_scaled<H>(v[1], sv);
+                    *(bf16x8 *)(kt + Tl::at(row, 2 * p + h)) = __builtin_shufflevector(k0, k1, 0, 1, 2, 3, 4, 5, 6, 7);
+                    *(bf16x8 *)(vt + Tl::at(row, 2 * p + h)) = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+                }
+            }
+        };
+        __syncthreads();                       // what the drafts see is there
+        const bool finds = t < KEYS;           // the first two wavefronts
+        if (finds && n0 < e1) {
+            find_row(n0);
+            keep_row(n0);
+            keep_scales(n0);
+            if (n0 + 1 < e1) {
+                find_row(n0 + 1);
+                keep_row(n0 + 1);
+            }
+        }
+        Rows next;
+        __syncthreads();
+        if (n0 < e1)
+            fetch(n0, next);
+        for (int n = n0; n < e1; ++n) {
+            const char *kt = lds, *vt = kt + Tl::kBytes;
+            const bool fold = (folds[n & 1][0] & folds[n & 1][1]) != 0;
+            put(n, next);
+            const bool find = finds && n + 2 < e1;
+            if (finds && n + 1 < e1)
+                keep_scales(n + 1);            // loaded a tile ago
+            if (find)
+                find_row(n + 2);
+            if (n + 1 < e1)
+                fetch(n + 1, next);
+            __syncthreads();
+#pragma unroll 1
+            for (int b = ks; b < KEYS / C; b += KS) {
+                const int j0 = first_key(u, n) + C * b, j1 = j0 + C - 1;
+                if (j0 > last_pos || (j1 < u.low && j0 >= a.sinks) || block * RB + C * rg >= rows)
+                    continue;
+                const int rows_at = renewed(Co::row_base(lane) + C * b * Tl::kRowBytes);
+                const int cols_at = renewed(Co::col_base(lane) + C * b * Tl::kRowBytes);
+                Acc x = Acc(0.0f);
+                chain<STEPS, 4>([&](int i) { return Co::key_frag(kt, rows_at, i); },
+                                [&](int i, bf16x8 f) {
+#pragma unroll
+                                    for (int k = 0; k < QP; ++k)
+                                        x = Co::mul(f, qf[i][k], x);
+                                });
+                if (!fold)
+                    times_scales<Co::kAcc>(x, scale_of[n & 1][0] + C * b + 4 * part);
+                if (!(j1 < u.ctx && (u.end - 1 - j0 < a.window || j1 < a.sinks))) {
+                    const int j = renewed(j0 + 4 * part);
+#pragma unroll
+                    for (int i = 0; i < Co::kAcc; ++i)
+                        if (!seen(j + Co::key_of(i)))
+                            x[i] = SDL_NEG_INF;
+                }
+                const float most = Co::most(x) * c2;
+                if (__any(most > top + kLazy)) {
+                    const float now = fmaxf(top, most);
+                    const float less = now == SDL_NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+                    top = now;
+                    total *= less;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int i = 0; i < Co::kAcc; ++i)
+                            O[d][i] *= less;
+                }
+                const float ref = top == SDL_NEG_INF ? 0.0f : top;
+                float sums[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < Co::kAcc; ++i) {
+                    x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c2, -ref));
+                    sums[i & 1] += x[i];
+                }
+                total += sums[0] + sums[1];
+                if (!fold)
+                    times_scales<Co::kAcc>(x, scale_of[n & 1][1] + C * b + 4 * part);
+                // bf16 parts of the weights: one for q in bf16, rounded here
+                typename Co::Weights pf[QP][Co::kGroups];
+#pragma unroll
+                for (int k = 0; k < QP; ++k) {
+                    Acc z = x;
+                    if (k < QP - 1)
+#pragma unroll
+                        for (int i = 0; i < Co::kAcc; ++i) {
+                            z[i] = __uint_as_float(__float_as_uint(x[i]) & 0xffff0000);
+                            x[i] -= z[i];
+                        }
+#pragma unroll
+                    for (int i = 0; i < Co::kGroups; ++i)
+                        pf[k][i] = Co::weights(z, i);
+                }
+                chain<Co::kGroups * DB, 4>(
+                    [&](int i) { return Co::val_frag(vt, cols_at, i / DB, i % DB); },
+                    [&](int i, typename Co::Weights f) {
+#pragma unroll
+                        for (int k = 0; k < QP; ++k)
+                            O[i % DB] = Co::apply(f, pf[k][i / DB], O[i % DB]);
+                    });
+            }
+            if (find)
+                keep_row(n + 2);
+            __syncthreads();
+        }
+        if (QP > 1 && strange != 0)
+            total = __builtin_nanf("");
+
+        // ---- join the wavefronts of a query group, and write
+        total = Co::sum(total);
+        if (part == 0) {
+            tops[wave][lane] = top;
+            totals[wave][lane] = total;
+        }
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int g = 0; g < Co::kAcc / 4; ++g)
+                store4((float *)(lds + wave * Out::kBytes +
+                                 Out::at(lane % C, (C * d + Co::key_of(4 * g)) / 4 + part)),
+                       O[d][4 * g], O[d][4 * g + 1], O[d][4 * g + 2], O[d][4 * g + 3]);
+        __syncthreads();
+        join_waves<T, H, DP, DU, C, RG>(a, u, {span.w, seq, hk, block, n0, n1, later}, slots, lds, tops, totals, redo,
+                                        drafts, wave, lane);
+        at += n1 - n0;
+        later = true;
+    }
+}
+
 // Joins the slots of units that were cut, a row's pieces by the lanes of part of a
 // wavefront and its spans by the wavefronts in turn (250 spans to a unit took 27 us
 // with every span added by the same lanes).
@@ -713,12 +1033,17 @@ hipError_t launch_codes(const TreeArgs &a, hipStream_t stream)
 {
     if (a.block_rows <= 16)
         return launch_stream<T, H, DP>(a, stream);
-    if (a.block_rows == 32)
-        tree_attn<T, H, DP, DU, 32, 1><<<a.workers, kAttnThreads, 0, stream>>>(a);
-    else if (a.block_rows == 64)
-        tree_attn<T, H, DP, DU, 32, 2><<<a.workers, kAttnThreads, 0, stream>>>(a);
-    else
-        tree_attn<T, H, DP, DU, 32, 4><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    // 16 queries to a wavefront where q in three parts leaves no registers for 32
+    if (a.block_rows == 32) {
+        tree_tiles<T, H, DP, DU, 16, 2><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    } else if constexpr (sizeof(T) == 4) {
+        tree_tiles<T, H, DP, DU, 16, 4><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    } else {
+        if (a.block_rows == 64)
+            tree_tiles<T, H, DP, DU, 32, 2><<<a.workers, kAttnThreads, 0, stream>>>(a);
+        else
+            tree_tiles<T, H, DP, DU, 32, 4><<<a.workers, kAttnThreads, 0, stream>>>(a);
+    }
     return launch_join<T, H, DP, DU>(a, stream);
 }
 
@@ -726,7 +1051,8 @@ hipError_t launch_codes(const TreeArgs &a, hipStream_t stream)
 template <class T, class H>
 hipError_t launch_codes_sized(const TreeArgs &a, hipStream_t stream)
 {
-    return a.D <= 64 ? launch_codes<T, H, 64, 64>(a, stream) : launch_codes<T, H, 128, 128>(a, stream);
+    return a.D <= 64 ? launch_codes<T, H, 64, 64>(a, stream)
+                     : (a.D <= 96 ? launch_codes<T, H, 128, 96>(a, stream) : launch_codes<T, H, 128, 128>(a, stream));
 }
 
 }  // namespace
