@@ -256,6 +256,118 @@ __global__ __launch_bounds__(kAttnThreads) void compact_codes(PagesArgs a)
     }
 }
 
+// The same for lists of up to kFew kept drafts.  All rows and the scales of where they
+// come from are read at once, then all are written: no row waits for another, and
+// blocks neither (128 sequences, 32 layers, up to 8 rows of 1 KB: 34 us taking row
+// after row).  Workgroup: one sequence, `items` of its (layer, pool) pairs, as many
+// as have a thread for each 16-byte column.
+constexpr int kFew = 8;
+
+template <class H>
+__global__ __launch_bounds__(kAttnThreads) void compact_few(PagesArgs a, int items)
+{
+    __shared__ int64_t from[kFew], to[kFew];       // rows of a layer; -1: nothing
+    __shared__ int64_t from_block[kFew], to_block[kFew];
+    const int t = threadIdx.x;
+    const int64_t seq = blockIdx.x, first = (int64_t)blockIdx.y * items, ctx = a.ctx[seq];
+    const uint32_t cols = (uint32_t)(a.row_bytes / 16), D = (uint32_t)(a.row_bytes / a.heads);
+    const int64_t left = 2 * a.layers - first;
+    const uint32_t all = cols * (uint32_t)(left < items ? left : items);
+    const int64_t layer_rows = a.pages * a.page, layer_scales = layer_rows / a.block * a.heads;
+    if (t < 64) {
+        const int32_t *table = a.table + seq * a.table_stride, *keep = a.keep + seq * a.kept;
+        const bool mine = t < kFew && t < a.kept;
+        const int64_t of = mine ? keep[t] : 0;
+        const uint64_t ends = __ballot(mine && of < 0);        // nothing counts from the first on
+        auto row_at = [&](int64_t pos) -> int64_t {
+            if (pos < 0 || pos / a.page >= a.table_stride)
+                return -1;
+            const int64_t number = table[pos / a.page];
+            return number < 0 || number >= a.pages ? -1 : number * a.page + pos % a.page;
+        };
+        if (t < kFew) {
+            const bool counts = mine && (ends & (((uint64_t)2 << t) - 1)) == 0;
+            const int64_t f = counts ? row_at(ctx + of) : -1, g = f < 0 ? -1 : row_at(ctx + t);
+            from[t] = g < 0 ? -1 : f;
+            to[t] = g;
+            from_block[t] = g < 0 ? 0 : f / a.block;
+            to_block[t] = g < 0 ? 0 : g / a.block;
+        }
+    }
+    __syncthreads();
+    const int off = (int)(ctx % a.block);                      // rows of the context in the first block
+    int which[kFew];                                           // block of the i-th place
+#pragma unroll
+    for (int i = 0; i < kFew; ++i)
+        which[i] = (off + i) / (int)a.block;
+    const uint32_t turn = kAttnThreads / (D / 16) * (D / 16);  // whole heads
+    for (uint32_t m0 = 0; m0 < all; m0 += turn) {
+        const uint32_t m = m0 + t, item = m / cols, col = m - item * cols;
+        const bool in = (uint32_t)t < turn && m < all;
+        char *pool = nullptr;
+        float *scales = nullptr;
+        u32x4 piece[kFew];
+        float come[kFew], before = 0.0f, now[kFew];
+        if (in) {
+            const int64_t n = first + item, layer = n < a.layers ? n : n - a.layers;
+            pool = (n < a.layers ? a.k : a.v) + layer * layer_rows * a.row_bytes + 16 * (int64_t)col;
+            scales = (n < a.layers ? a.k_scale : a.v_scale) + layer * layer_scales + 16 * col / D;
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                come[i] = 0.0f;
+                if (from[i] >= 0) {
+                    come[i] = scales[from_block[i] * a.heads];
+                    piece[i] = *(const u32x4 *)(pool + from[i] * a.row_bytes);
+                }
+            }
+            // the block of the context's last row, if a kept row moves into it
+            int into = -1;
+#pragma unroll
+            for (int i = kFew - 1; i >= 0; --i)
+                into = which[i] == 0 && from[i] >= 0 ? i : into;
+            if (off > 0 && into >= 0)
+                before = scales[to_block[into] * a.heads];
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                now[i] = which[i] == 0 ? before : 0.0f;
+#pragma unroll
+                for (int j = 0; j < kFew; ++j)
+                    if (from[j] >= 0 && which[j] == which[i])
+                        now[i] = larger_scale(now[i], come[j]);
+            }
+            auto convert = [&](u32x4 x, float old, const Divide &divide) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const f32x4 u = wide<H>(x[e]);
+                    x[e] = narrow<H>(divide(f32x4{u[0] * old, u[1] * old, u[2] * old, u[3] * old}));
+                }
+                return x;
+            };
+            if (off > 0 && into >= 0 && now[into] != before) {
+                const Divide divide(now[into]);
+                const int64_t row = to[into] - into - off;     // the block's first
+                for (int r = 0; r < off; ++r) {
+                    u32x4 *p = (u32x4 *)(pool + (row + r) * a.row_bytes);
+                    *p = convert(*p, before, divide);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kFew; ++i)
+                if (from[i] >= 0 && (from[i] != to[i] || come[i] != now[i]))
+                    *(u32x4 *)(pool + to[i] * a.row_bytes) =
+                        come[i] != now[i] ? convert(piece[i], come[i], Divide(now[i])) : piece[i];
+        }
+        __syncthreads();                       // all have read the scales
+        if (in && 16 * col % D == 0) {
+#pragma unroll
+            for (int i = 0; i < kFew; ++i)
+                if (from[i] >= 0)
+                    scales[to_block[i] * a.heads] = now[i];
+        }
+        __syncthreads();
+    }
+}
+
 }  // namespace
 
 int64_t pages_copy_parts(int64_t page_bytes) { return (page_bytes + kCopyBytes - 1) / kCopyBytes; }
@@ -276,6 +388,16 @@ hipError_t launch_pages_compact(const PagesArgs &a, hipStream_t stream)
 
 hipError_t launch_cache_compact(int held, const PagesArgs &a, hipStream_t stream)
 {
+    if (a.kept <= kFew) {
+        const int64_t cols = a.row_bytes / 16, fit = kAttnThreads / cols;
+        const int items = (int)(fit < 1 ? 1 : (fit > 8 ? 8 : fit));
+        const dim3 grid((uint32_t)a.count, (uint32_t)((2 * a.layers + items - 1) / items));
+        if (held == CACHE_E4M3)
+            compact_few<E4M3><<<grid, kAttnThreads, 0, stream>>>(a, items);
+        else
+            compact_few<Int8><<<grid, kAttnThreads, 0, stream>>>(a, items);
+        return hipGetLastError();
+    }
     const dim3 grid((uint32_t)a.count, (uint32_t)((2 * a.layers + kCodeItems - 1) / kCodeItems));
     if (held == CACHE_E4M3)
         compact_codes<E4M3><<<grid, kAttnThreads, 0, stream>>>(a);

@@ -772,13 +772,19 @@ def test_compact(held, page, block):
     ctx = [0, 5, 16, 31, 100, 7, 3]
     keep = [sorted(r.sample(range(64), n)) for n in (1, 8, 20, 64, 5)] + [[], [0, 1, 2]]
     check_compact(held, 3, page, block, 2, 64, ctx, keep, seed=page)
+    # lists of up to eight, of neighbours and of drafts far apart
+    for n in (1, 3, 8):
+        keep = [sorted(r.sample(range(m), n)) for m in (8, 9, 20, 64, 30)] + [[], list(range(n))]
+        check_compact(held, 3, page, block, 2, 64, ctx, keep, seed=page + n)
 
 
 @CODES
 @pytest.mark.parametrize("heads,D", [(1, 16), (3, 48), (8, 128), (24, 80), (40, 112), (2, 96)])
 def test_compact_heads(held, heads, D):
     """Up to rows of more columns than a workgroup takes in a turn."""
-    check_compact(held, 2, 16, 8, heads, D, [3, 13], [[1, 2, 3, 9, 30], [0, 4, 5, 6, 7, 8, 20]], seed=D)
+    keep = [[1, 2, 3, 9, 30], [0, 4, 5, 6, 7, 8, 20]]
+    check_compact(held, 2, 16, 8, heads, D, [3, 13], keep, seed=D)
+    check_compact(held, 2, 16, 8, heads, D, [3, 13], [x + [40, 41, 50] for x in keep], seed=D)
 
 
 @CODES
@@ -799,6 +805,9 @@ def test_compact_scales_and_places_out_of_range(held):
         table[2][0] = len(ks[0])
     check_compact(held, 2, 16, 8, 2, 64, [3, 30, 5], [[2, 9, 40, 60], [1, 3, 20], [0, 1, 14, 15]], change=foreign)
     check_compact(held, 2, 16, 8, 2, 64, [3, 30], [[2, 9, 40, 90], [1, 3, 20]], rows=30)
+    more = [[2, 9, 40, 60, 61, 62, 63, 70, 71, 72], [1, 3, 20], list(range(14)) + [15]]
+    check_compact(held, 2, 16, 8, 2, 64, [3, 30, 5], more, change=foreign)
+    check_compact(held, 2, 16, 8, 2, 64, [3, 30], more[:2], rows=30)
 
 
 @CODES
