@@ -2,9 +2,9 @@
 // scale, one fp32 scale for each block of positions and head.
 //
 // Codes are exact in bf16 and fp32 (e4m3 has 4 significant bits, an integer 8),
-// so the matrix instructions take them as they are, and the scales, which
-// differ from key to key, are applied in fp32 to the scores and to the softmax
-// weights: nothing is rounded that rows of bf16 would not round.
+// so the matrix instructions take them as they are.  The scales, which differ from
+// key to key, are applied in fp32 to the scores and to the softmax weights, or, where
+// they are powers of two, in the widening, which stays exact.
 #pragma once
 
 #include "tile.h"
@@ -131,25 +131,6 @@ __device__ inline f32x8 load8(CodeRow<H> r)
     const uint32_t *w = (const uint32_t *)r.at;
     const f32x4 a = wide<H>(w[0]) * r.scale, b = wide<H>(w[1]) * r.scale;
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// A 16-byte piece of a pool's row into an LDS tile of T.
-template <class T, class H, class Tl>
-__device__ inline void put_piece(char *tile, int row, int piece, u32x4 x)
-{
-    if constexpr (!kCodes<H>) {
-        *(u32x4 *)(tile + Tl::at(row, piece)) = x;
-    } else if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const auto a = wide_bf16<H>(x[2 * i]), b = wide_bf16<H>(x[2 * i + 1]);
-            *(bf16x8 *)(tile + Tl::at(row, 2 * piece + i)) = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *(f32x4 *)(tile + Tl::at(row, 4 * piece + i)) = wide<H>(x[i]);
-    }
 }
 
 // Scores or weights of a result's rows times the scales of their keys, four
