@@ -80,6 +80,7 @@ typedef struct cache_scales {
  * index or page number (0 .. pages - 1) is out of range are passed over, in
  * pools of codes whole blocks.  Nothing else of the pools is written but, in
  * pools of codes, the scales and the earlier rows of the blocks written to.
+ * Strides by which rows of a pool, or scales, would overlap are refused.
  */
 typedef struct cache_append {
     int64_t S, T;                                   /* sequences, rows */

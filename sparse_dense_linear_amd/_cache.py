@@ -88,8 +88,13 @@ def append_pages(k, v, k_pages, v_pages, table, ctx, rowptr, q=None, cos=None, s
     if k_scale is not None or v_scale is not None:
         held = _codes(k_pages, "k_pages")
         scales = _scales(k_scale, v_scale, device, pages, page, Hkv)
+        if k_scale.data_ptr() == v_scale.data_ptr() and pages:
+            raise ValueError("the scales must not overlap")
     elif k_pages.dtype is not k.dtype:
         raise TypeError("the pools (without scales) must have the element type of k")
+    kpp, vpp = k_pages.data_ptr() or None, v_pages.data_ptr() or None
+    if kpp == vpp and kpp is not None:
+        raise ValueError("the pools must not overlap")
     cosp, sinp, angles, rotated = _tables(cos, sin, device)
     r = []
     _rows(r, k, "k", device, k.dtype, k.shape)
@@ -116,7 +121,7 @@ def append_pages(k, v, k_pages, v_pages, table, ctx, rowptr, q=None, cos=None, s
                               bool(interleaved), 0)
         st = _attn._ready.cache_append(
             dt, held, w, pack(*r[6:9]) if Hq else None, pack(*r[:3]), pack(*r[3:6]), cosp, sinp, bp, cp, rp, tp,
-            k_pages.data_ptr() or None, v_pages.data_ptr() or None, scales, pack(*r[9:]) if Hq else None, handle)
+            kpp, vpp, scales, pack(*r[9:]) if Hq else None, handle)
     if st:
         _check(st, "cache_append")
     return q_out

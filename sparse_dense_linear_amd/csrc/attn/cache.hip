@@ -1,5 +1,7 @@
 // cache.hip -- host side of the C ABI declared in include/cache.h: checks
 // arguments before any HIP call, then enqueues.
+#include <utility>
+
 #include "checks.h"
 
 using namespace sdl;
@@ -24,6 +26,35 @@ spmm_status_t check_scales(const cache_scales_t *s, int64_t page)
     if (s->k == nullptr || s->v == nullptr || !aligned(s->k, 4) || !aligned(s->v, 4))
         return bad("scales are null or not 4-byte aligned");
     return SPMM_SUCCESS;
+}
+
+struct Dim {
+    int64_t count, stride;
+};
+
+// Whether runs of `length` elements lie apart, in dimensions that each step over all
+// of those of smaller strides (counts below 2^30, strides up to 2^32).
+bool apart(Dim a, Dim b, Dim c, int64_t length)
+{
+    Dim d[] = {a, b, c};
+    for (Dim &x : d)
+        if (x.count <= 1)
+            x.stride = 0;
+    if (d[0].stride > d[1].stride)
+        std::swap(d[0], d[1]);
+    if (d[1].stride > d[2].stride)
+        std::swap(d[1], d[2]);
+    if (d[0].stride > d[1].stride)
+        std::swap(d[0], d[1]);
+    uint64_t extent = (uint64_t)length;
+    for (const Dim &x : d) {
+        if (x.count <= 1)
+            continue;
+        if ((uint64_t)x.stride < extent)
+            return false;
+        extent += (uint64_t)(x.count - 1) * (uint64_t)x.stride;
+    }
+    return true;
 }
 
 spmm_status_t check_code_heads(int64_t D)
@@ -57,6 +88,8 @@ spmm_status_t check_append(int32_t dtype, int32_t held, const cache_append_t *w)
         return bad("S, T, table_stride and pages must be below 2^30");
     if ((st = check_paging(w, pool_unit(dtype, held))) != SPMM_SUCCESS)
         return st;
+    if (!apart({w->pages, w->page_stride}, {w->page, w->row_stride}, {w->Hkv, w->head_stride}, w->D))
+        return bad("rows of the pools overlap");
     if (w->rotated < 0 || w->rotated > w->D)
         return bad("rotated must be in 0 .. D");
     if (w->rotated % 8 != 0)
@@ -135,6 +168,10 @@ spmm_status_t cache_append(int32_t dtype, int32_t held, const cache_append_t *sh
         return bad("cosines or sines are null or not 16-byte aligned");
     if (held != CACHE_AS_IS && (st = check_scales(scales, shape->page)) != SPMM_SUCCESS)
         return st;
+    if (held != CACHE_AS_IS &&
+        !apart({shape->pages, scales->page_stride}, {shape->page / scales->block, scales->block_stride},
+               {shape->Hkv, scales->head_stride}, 1))
+        return bad("scales overlap");
     if (held == CACHE_AS_IS && scales != nullptr)
         return bad("pools of the operands' type have no scales");
     AppendArgs a = {};

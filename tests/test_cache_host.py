@@ -143,6 +143,32 @@ def test_append_refuses_the_rest():
                             FAKE, None, rows(), None) == INVALID
 
 
+@pytest.mark.parametrize("change,fine", [
+    (dict(page_stride=0), False), (dict(row_stride=0), False), (dict(head_stride=0), False),
+    (dict(page_stride=2032), False), (dict(row_stride=112), False), (dict(head_stride=48), False),
+    (dict(page_stride=0, pages=1), True), (dict(row_stride=0, page=1, page_stride=128), True),
+    (dict(head_stride=0, Hkv=1, Hq=0), True),
+    # heads outside the rows, pages inside them
+    (dict(row_stride=64, head_stride=1024, page_stride=2048), True),
+    (dict(row_stride=64, head_stride=1008, page_stride=2048), False),
+    (dict(page_stride=64, head_stride=8 * 64, row_stride=16 * 64), True),
+    (dict(page_stride=64, head_stride=8 * 64, row_stride=15 * 64), False),
+    (dict(page_stride=1 << 32, row_stride=1 << 32, head_stride=1 << 32, page=(1 << 30) - 1, pages=(1 << 30) - 1), False),
+    (dict(page_stride=1 << 32), True)])
+def test_append_refuses_pools_that_overlap_themselves(change, fine):
+    for held in (AS_IS, E4M3, INT8):
+        block = scales(block=1, page_stride=64, block_stride=2) if held != AS_IS else None
+        st = append(ashape(T=0, **change), held=held, sc=block)
+        assert st == (0 if fine else INVALID)
+
+
+@pytest.mark.parametrize("change", [dict(page_stride=0), dict(block_stride=0), dict(head_stride=0),
+                                    dict(page_stride=3), dict(block_stride=1), dict(head_stride=2)])
+def test_append_refuses_scales_that_overlap(change):
+    assert append(held=INT8, sc=scales(**change)) == INVALID
+    assert b"overlap" in sdl.lib().spmm_last_error()
+
+
 def test_nothing_to_do():
     empty = rows(data=None)
     assert append(ashape(S=0), table=None, ctx=None, rp=None, kp=None, vp=None) == 0
@@ -211,8 +237,9 @@ def test_calls_that_no_launch_holds_are_refused(call, held):
 def test_appends_that_no_launch_holds_are_refused():
     big = (1 << 30) - 1
     for held in (AS_IS, E4M3, INT8):
-        assert append(ashape(T=big, Hq=64, Hkv=64), held=held, q=rows(64), q_out=rows(64), k=rows(64),
-                      v=rows(64)) == UNSUPPORTED
+        w = ashape(T=big, Hq=64, Hkv=64, row_stride=64 * 64, page_stride=16 * 64 * 64)
+        sc = None if held == AS_IS else scales(block_stride=64, page_stride=128)
+        assert append(w, held=held, q=rows(64), q_out=rows(64), k=rows(64), v=rows(64), sc=sc) == UNSUPPORTED
     # two blocks of each sequence, head and pool, four to a workgroup
     assert append(ashape(S=big, Hq=0), held=E4M3) == UNSUPPORTED
     if not torch.cuda.is_available():

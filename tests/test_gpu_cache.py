@@ -80,7 +80,7 @@ class CodeCache:
     """A paged cache of codes: scales of any size, no powers of two; unused rows
     hold NaN (77 where there is none) and unused blocks the scale NaN."""
 
-    def __init__(self, lengths, page, block, Hkv, D, held, seed, dead=()):
+    def __init__(self, lengths, page, block, Hkv, D, held, seed, dead=(), power=None):
         g = torch.Generator().manual_seed(seed)
         self.table, pool = page_table(lengths, page, seed)
         shape = (pool, page, Hkv, D)
@@ -93,7 +93,13 @@ class CodeCache:
             for pool_, scale, rows in ((self.k, self.ks, self.rows_k), (self.v, self.vs, self.rows_v)):
                 blocks = -(-n // block)
                 sc = (torch.rand(blocks, Hkv, generator=g) + 0.5) / (MOST[held] / 4)
+                if power is not None:                     # of two; the values of all sizes
+                    sc = torch.exp2(sc.log2().round())
+                    if pool_ is self.v:
+                        sc = sc * torch.exp2(torch.randint(-3, 4, sc.shape, generator=g).float())
                 x = torch.randn(n, Hkv, D, generator=g)
+                if power is not None:
+                    sc, x = sc * 2.0 ** power, x * 2.0 ** power
                 each = sc.repeat_interleave(block, 0)[:n]
                 code = codes_of((x / each[..., None]).clamp(-MOST[held], MOST[held]), held)
                 for b in range(blocks):
@@ -139,9 +145,9 @@ def want_rows(q, qs, rows_k, rows_v, seen_of, Hkv, sc, dtype):
 
 
 def check(ctx, drafts, Hq, Hkv, D, dtype, held, page, block, window, sinks, masks="tree", seed=0, dead=(),
-          scale=None):
+          scale=None, power=None):
     r = random.Random(seed)
-    cache = CodeCache([c + t for c, t in zip(ctx, drafts)], page, block, Hkv, D, held, seed, dead)
+    cache = CodeCache([c + t for c, t in zip(ctx, drafts)], page, block, Hkv, D, held, seed, dead, power)
     q = torch.randn(sum(drafts), Hq, D, generator=torch.Generator().manual_seed(seed + 1)).to(dtype)
     qs = starts(drafts)
     if masks == "tree":
@@ -194,6 +200,19 @@ def test_windows(dtype, held, window, sinks):
 def test_shared_heads(dtype, held, Hq, Hkv, drafts):
     """From one column of a matrix to many blocks of them."""
     check([300, 77], drafts, Hq, Hkv, 64, dtype, held, 32, 16, 200, 2, seed=Hq)
+
+
+@TYPES
+@CODES
+@pytest.mark.parametrize("power", [0, -90, 60, 112])
+@pytest.mark.parametrize("drafts", [[1, 1], [40, 9], [130, 64]])
+def test_scales_of_powers_of_two(dtype, held, power, drafts):
+    """As append_pages writes them, whole tiles of them and tiles that a page of
+    another sequence's end cuts; small and large, within what is widened with its
+    scale and past it."""
+    masks = None if max(drafts) > 64 else "tree"
+    check([700, 77], drafts, 4, 2, 64, dtype, held, 32, 8, 300, 2, masks=masks, seed=11, power=power,
+          scale=2.0 ** (-3 - power))
 
 
 @TYPES
@@ -914,3 +933,123 @@ def test_prompt_drafts_acceptance_and_next_token(dtype, kind):
         ctx = [c + len(x) for c, x in zip(ctx, keep)]
         step(ctx, [1, 1, 1], None)
         ctx = [c + 1 for c in ctx]
+
+
+# ----------------------------------------------------------------- refusals
+
+def refused(exc, match, f, *a, **kw):
+    with pytest.raises(exc, match=match):
+        f(*a, **kw)
+
+
+@CODES
+def test_attention_refuses(held):
+    q = torch.zeros(4, 4, 64, device="cuda")
+    pages = torch.zeros(3, 16, 2, 64).to(held).cuda()
+    sc = torch.ones(3, 2, 2, device="cuda")
+    a = (i32([[0, 1]]), i32([20]), i32([0, 4]))
+
+    def call(q=q, k=pages, v=pages, ks=sc, vs=sc, **kw):
+        return sdl.tree_attention(q, k, v, *a, k_scale=ks, v_scale=vs, **kw)
+
+    call()
+    refused(TypeError, "k_scale", call, ks=None)
+    refused(TypeError, "v_scale", call, vs=None)
+    refused(TypeError, "float32 or bfloat16", call, q=q.half())
+    refused(TypeError, "float8_e4m3fn or int8", call, k=pages.float(), v=pages.float())
+    other = INT8 if held is E4M3 else E4M3
+    refused(TypeError, "one element type", call, v=pages.view(other))
+    refused(TypeError, "without scales", call, ks=None, vs=None)
+    refused(TypeError, "scales must be float32", call, ks=sc.double(), vs=sc.double())
+    refused(ValueError, "same GPU", call, ks=sc.cpu())
+    refused(ValueError, "pages, blocks", call, ks=sc[:2], vs=sc[:2])
+    refused(ValueError, "pages, blocks", call, ks=sc[..., :1], vs=sc[..., :1])
+    refused(ValueError, "pages, blocks", call, ks=sc[0], vs=sc[0])
+    three = torch.ones(3, 3, 2, device="cuda")
+    refused(ValueError, "must divide", call, ks=three, vs=three)
+    refused(ValueError, "same strides", call, vs=sc.permute(2, 0, 1).contiguous().permute(1, 2, 0))
+    refused(ValueError, "same strides", call, v=pages.transpose(1, 2).contiguous().transpose(1, 2))
+    refused(sdl.SpmmError, "multiple of 16", call, q=q[..., :24], k=pages[..., :24], v=pages[..., :24])
+    refused(sdl.SpmmError, "window", call, window=0)
+    o, lse = torch.empty_like(q), torch.empty(4, 4, device="cuda")
+    refused(TypeError, "o that of q", sdl.tree_attn_paged, q, pages, pages, *a, None, o.bfloat16(), lse, k_scale=sc,
+            v_scale=sc)
+    refused(ValueError, "overlap", sdl.tree_attn_paged, q, pages, pages, *a, None, q, lse, k_scale=sc, v_scale=sc)
+
+
+@KINDS
+def test_append_refuses(kind):
+    k, q = torch.zeros(4, 2, 64, device="cuda"), torch.zeros(4, 4, 64, device="cuda")
+    kp, vp, ks, vs = (None if x is None else x.cuda()
+                      for x in a_pool(3, 16, 8, 2, 64, kind, F32, torch.Generator().manual_seed(1)))
+    cos = torch.ones(50, 32, device="cuda")
+    a = (i32([[0, 1]]), i32([20]), i32([0, 4]))
+
+    def call(k=k, v=k, kp=kp, vp=vp, a=a, ks=ks, vs=vs, **kw):
+        return sdl.append_pages(k, v, kp, vp, *a, k_scale=ks, v_scale=vs, **kw)
+
+    before = [None if x is None else x.clone() for x in (kp, vp, ks, vs)]
+    refused(TypeError, "float32 or bfloat16", call, k=k.half())
+    refused(TypeError, "element type", call, v=k.bfloat16())
+    refused(ValueError, "three dimensions", call, k=k[0])
+    refused(ValueError, "shape", call, v=k[:3])
+    refused(ValueError, "pools must not overlap", call, vp=kp)
+    refused(ValueError, "heads of k", call, k=k[:, :1], v=k[:, :1])
+    refused(ValueError, "D of q", call, k=k[..., :32], v=k[..., :32])
+    refused(ValueError, "four dimensions", call, kp=kp[0], vp=vp[0])
+    refused(sdl.SpmmError, "rows of the pools overlap", call, kp=kp[:1].expand(3, 16, 2, 64),
+            vp=vp[:1].expand(3, 16, 2, 64))
+    refused(ValueError, "cos must have two", call, cos=cos[0], sin=cos[0])
+    refused(TypeError, "sin", call, cos=cos)
+    refused(TypeError, "cos", call, sin=cos)
+    refused(TypeError, "float32", call, cos=cos.double(), sin=cos.double())
+    refused(ValueError, "contiguous", call, cos=cos.t(), sin=cos.t())
+    refused(sdl.SpmmError, "rotated", call, cos=torch.cat([cos, cos], 1), sin=torch.cat([cos, cos], 1))
+    refused(sdl.SpmmError, "multiple of 8", call, cos=cos[:, :2].contiguous(), sin=cos[:, :2].contiguous())
+    refused(TypeError, "64-bit masks", call, tree=i32([1, 1, 1, 1]))
+    refused(ValueError, "shape", call, tree=i64([1, 1]))
+    refused(TypeError, "int32", call, a=(a[0], a[1].long(), a[2]))
+    refused(ValueError, "shape", call, a=(a[0], a[1], a[2][:1]))
+    refused(ValueError, "two dimensions", call, a=(a[0][0], a[1], a[2]))
+    refused(ValueError, "goes with q", call, q_out=q)
+    refused(ValueError, "three dimensions", call, q=q[:3])
+    refused(ValueError, "three dimensions", call, q=q[..., :32])
+    refused(ValueError, "have heads", call, q=q[:, :0])
+    refused(sdl.SpmmError, "multiple of Hkv", call, q=q[:, :3].contiguous())
+    refused(ValueError, "overlap", call, q=q, q_out=q.as_strided(q.shape, (64, 256, 1)))
+    refused(sdl.SpmmError, "overlap", call, q=q, q_out=torch.zeros(1, 4, 64, device="cuda").expand(4, 4, 64))
+    refused(ValueError, "overlap", call, q=q[:, :2], q_out=k)
+    if kind is not None:
+        refused(TypeError, "v_scale", call, vs=None)
+        refused(ValueError, "scales must not overlap", call, vs=ks)
+        refused(sdl.SpmmError, "scales overlap", call, ks=ks[:, :1].expand(3, 2, 2), vs=vs[:, :1].expand(3, 2, 2))
+        refused(TypeError, "without scales", call, ks=None, vs=None)
+    else:
+        refused(TypeError, "float8_e4m3fn or int8", call, ks=torch.ones(3, 2, 2, device="cuda"),
+                vs=torch.ones(3, 2, 2, device="cuda"))
+    torch.cuda.synchronize()
+    for x, y in zip((kp, vp, ks, vs), before):
+        if x is not None:
+            assert torch.equal(bits(x), bits(y))
+
+
+@CODES
+def test_moves_refuse(held):
+    kp, vp, ks, vs = (x.cuda() for x in layered(2, 4, 16, 8, 2, 64, held, 1))
+    one = i32([0])
+    for f, a in ((sdl.copy_pages, (one, i32([1]))), (sdl.compact_pages, (i32([[0, 1]]), one, i32([[1]])))):
+        def call(kp=kp, vp=vp, ks=ks, vs=vs):
+            f(kp, vp, *a, k_scale=ks, v_scale=vs)
+
+        refused(TypeError, "k_scale", call, ks=None)
+        refused(TypeError, "v_scale", call, vs=None)
+        refused(TypeError, "float8_e4m3fn or int8", call, kp=kp.float(), vp=vp.float())
+        refused(TypeError, "float32", call, ks=ks.double(), vs=vs.double())
+        refused(ValueError, "same GPU", call, ks=ks.cpu())
+        refused(ValueError, "five dimensions", call, kp=kp.flatten(3), vp=vp.flatten(3))
+        refused(ValueError, "layers, pages", call, ks=ks[:1], vs=vs[:1])
+        refused(ValueError, "must be contiguous", call, ks=ks.transpose(0, 1).contiguous().transpose(0, 1))
+        refused(ValueError, "overlap", call, vs=ks)
+        refused(ValueError, "must divide", call, ks=ks[:, :, :1].expand(2, 4, 3, 2).contiguous(),
+                vs=vs[:, :, :1].expand(2, 4, 3, 2).contiguous())
+        refused(sdl.SpmmError, "multiple of 16", call, kp=kp[..., :24].contiguous(), vp=vp[..., :24].contiguous())
