@@ -613,6 +613,20 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
     }
 }
 
+// What a query sees of 32 keys from j0 on, bit by bit.
+struct BlockSeen {
+    int pos, cached;      // where it stands; keys before `cached` go by the window alone
+    uint64_t mask;        // of the drafts it sees (0: a chain, whose keys all lie before `cached`)
+    __device__ static uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1); }
+    __device__ uint32_t operator()(int j0, int ctx, int window, int sinks) const
+    {
+        const uint32_t near = (~below(pos - window + 1 - j0) | below(sinks - j0)) & below(cached - j0);
+        const int d = j0 - ctx;
+        const uint64_t drafts = d >= 64 || d <= -32 ? 0 : (d >= 0 ? mask >> d : mask << -d);
+        return near | (uint32_t)drafts;
+    }
+};
+
 // Blocks of 32 to 128 query rows, RG groups of C of them; the 4 / RG wavefronts of a
 // group share the keys of a tile.  Tiles of 128 keys are widened to bf16 on their way
 // into LDS, once for all query groups; the next tile is under way while one is worked
@@ -688,14 +702,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void tree_tiles(TreeArgs a)
         // this lane's query
         const int r = block * RB + C * rg + lane % C;
         const int token = (r < rows ? r : rows - 1) / group, head = hk * group + (r < rows ? r : rows - 1) % group;
-        DraftSeen seen;
-        seen.ctx = u.ctx;
-        seen.drafts = u.drafts;
-        seen.window = a.window;
-        seen.sinks = a.sinks;
+        BlockSeen seen;
         seen.mask = a.tree != nullptr ? draft_mask(a.tree[u.q_begin + token], u.drafts) : 0;
         seen.pos = a.tree != nullptr ? draft_place(u.ctx, seen.mask) : u.ctx + token;
-        seen.place = a.tree != nullptr ? drafts.place : nullptr;
+        seen.cached = a.tree != nullptr ? u.ctx : seen.pos + 1;
         const T *q = (const T *)a.q + (int64_t)(u.q_begin + token) * a.q_row + head * a.q_head;
         bf16x8 qf[STEPS][QP];
 #pragma unroll
@@ -715,11 +725,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void tree_tiles(TreeArgs a)
         float top = SDL_NEG_INF, total = 0.0f;
 
         // A chain's block ends where its last row stands: later tiles hold nothing for it,
-        // later keys nothing for a wavefront.
-        int e1 = n1, last_pos = u.end - 1;
+        // later keys nothing for a wavefront.  Its rows see all keys up to the first one's
+        // place (of a tree, the context) that are in the window of the last.
+        int e1 = n1, first_pos = u.ctx - 1, last_pos = u.end - 1, low = u.low;
         if (a.tree == nullptr) {
             auto stands = [&](int last) { return u.ctx + (last < rows ? last : rows - 1) / group; };
+            first_pos = stands(block * RB + C * rg);
             last_pos = stands(block * RB + C * rg + C - 1);
+            low = window_low(first_pos, a.window);
             const int e = u.first_tiles + stands(block * RB + RB - 1) / KEYS - u.band + 1;
             e1 = e < n1 ? (e > n0 ? e : n0) : n1;
         }
@@ -811,6 +824,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void tree_tiles(TreeArgs a)
             }
         };
         __syncthreads();                       // what the drafts see is there
+        if (a.tree != nullptr && a.window < 64)
+            for (int d = 0; d < 64; ++d)       // (further apart they do not stand)
+                if (seen.mask >> d & 1 && seen.pos - drafts.place[d] >= a.window && drafts.place[d] >= a.sinks)
+                    seen.mask &= ~((uint64_t)1 << d);
         const bool finds = t < KEYS;           // the first two wavefronts
         if (finds && n0 < e1) {
             find_row(n0);
@@ -840,7 +857,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void tree_tiles(TreeArgs a)
 #pragma unroll 1
             for (int b = ks; b < KEYS / C; b += KS) {
                 const int j0 = first_key(u, n) + C * b, j1 = j0 + C - 1;
-                if (j0 > last_pos || (j1 < u.low && j0 >= a.sinks) || block * RB + C * rg >= rows)
+                if (j0 > last_pos || (j1 < low && j0 >= a.sinks) || block * RB + C * rg >= rows)
                     continue;
                 const int rows_at = renewed(Co::row_base(lane) + C * b * Tl::kRowBytes);
                 const int cols_at = renewed(Co::col_base(lane) + C * b * Tl::kRowBytes);
@@ -853,12 +870,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void tree_tiles(TreeArgs a)
                                 });
                 if (!fold)
                     times_scales<Co::kAcc>(x, scale_of[n & 1][0] + C * b + 4 * part);
-                if (!(j1 < u.ctx && (u.end - 1 - j0 < a.window || j1 < a.sinks))) {
-                    const int j = renewed(j0 + 4 * part);
+                if (!(j1 <= first_pos && (last_pos - j0 < a.window || j1 < a.sinks))) {
+                    const uint32_t bits = renewed((int)(seen(j0, u.ctx, a.window, a.sinks) >> (4 * part)));
 #pragma unroll
                     for (int i = 0; i < Co::kAcc; ++i)
-                        if (!seen(j + Co::key_of(i)))
-                            x[i] = SDL_NEG_INF;
+                        x[i] = bits >> Co::key_of(i) & 1 ? x[i] : SDL_NEG_INF;
                 }
                 const float most = Co::most(x) * c2;
                 if (__any(most > top + kLazy)) {
