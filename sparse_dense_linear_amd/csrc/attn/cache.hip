@@ -110,6 +110,9 @@ spmm_status_t check_code_pool(const cache_pool_t *p)
         return bad("heads must divide row_bytes");
     if (p->block < 1 || p->pool.page % p->block != 0)
         return bad("a block must divide the page");
+    // (a turn of the threads that move rows holds whole heads)
+    if (p->pool.row_bytes / p->heads > kMaxHeadDim)
+        return unsupported("D must be a multiple of 16 up to 128");
     return check_code_heads(p->pool.row_bytes / p->heads);
 }
 

@@ -210,6 +210,14 @@ def test_moves_refuse_pools(change, expect):
     assert copy(pool(**change)) == expect and compact(pool(**change)) == expect
 
 
+@pytest.mark.parametrize("heads,row", [(1, 144), (1, 4096), (1, 8192), (1, 1 << 20), (2, 1 << 16)])
+def test_moves_refuse_heads_that_no_turn_of_threads_holds(heads, row):
+    """Past 256 threads of 16 bytes to a head a workgroup would make no headway."""
+    assert copy(pool(heads=heads, row_bytes=row)) == UNSUPPORTED
+    for kept in (3, 100):
+        assert compact(pool(heads=heads, row_bytes=row), kept=kept) == UNSUPPORTED
+
+
 def test_moves_refuse_the_rest():
     assert copy(src=None) == INVALID and copy(dst=FAKE + 1) == INVALID and copy(count=-1) == INVALID
     assert copy(count=1 << 30) == UNSUPPORTED
