@@ -108,10 +108,12 @@ def append_pages(k, v, k_pages, v_pages, table, ctx, rowptr, q=None, cos=None, s
             Hq = q.shape[1]
             if Hq < 1:
                 raise ValueError("q must have heads")
+            _rows(r, q, "q", device, k.dtype, q.shape)
             if q_out is None:
                 q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            _rows(r, q, "q", device, k.dtype, q.shape)
-            _rows(r, q_out, "q_out", device, k.dtype, q.shape)
+                r += (q_out.data_ptr(), Hq * D, D)
+            else:
+                _rows(r, q_out, "q_out", device, k.dtype, q.shape)
             if r[9] and (r[9] in (r[0], r[3]) or (r[9] == r[6] and r[10:] != r[7:9])):
                 raise ValueError("q_out must not overlap k or v, and be q itself or apart from it")
         elif q_out is not None:
