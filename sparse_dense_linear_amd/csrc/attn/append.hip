@@ -123,18 +123,20 @@ __device__ inline int64_t page_of(const AppendArgs &a, int seq, int pos)
     return number >= 0 && number < a.pages ? number : -1;
 }
 
-constexpr int kHeadsAtOnce = 4;
+// Heads of a wavefront, all of which are loaded before one is stored (17000 rows of 48
+// heads: 80 us, with four such turns to a wavefront, which find their rows once, 85).
+constexpr int kHeads = 4;
 
 // Rows of q and, where the pools hold them as they are, of k and v: kRowsPer
-// rows to a wavefront and `heads` heads of them, counted through q, k and v.
+// rows to a wavefront and kHeads heads of them, counted through q, k and v.
 template <class T, bool CODES, int LPR>
-__device__ inline void move_rows(const AppendArgs &a, int64_t wave, int heads, int lane)
+__device__ inline void move_rows(const AppendArgs &a, int64_t wave, int lane)
 {
     constexpr int ROWS = kRowsPer<LPR>;
-    const int all = a.Hq + (CODES ? 0 : 2 * a.Hkv), parts = (all + heads - 1) / heads;
+    const int all = a.Hq + (CODES ? 0 : 2 * a.Hkv), parts = (all + kHeads - 1) / kHeads;
     if (all == 0)
         return;
-    const int h0 = (int)(wave % parts) * heads, h1 = h0 + heads < all ? h0 + heads : all;
+    const int h = (int)(wave % parts) * kHeads;
     const int64_t first = wave / parts * ROWS;
     if (first >= a.T)
         return;
@@ -158,34 +160,32 @@ __device__ inline void move_rows(const AppendArgs &a, int64_t wave, int heads, i
         if (number >= 0)
             at = number * a.page_stride + (int64_t)(pos % a.page) * a.row_stride;
     }
-    for (int h = h0; h < h1; h += kHeadsAtOnce) {
-        f32x4 x[kHeadsAtOnce], y[kHeadsAtOnce];
+    f32x4 x[kHeads], y[kHeads];
 #pragma unroll
-        for (int i = 0; i < kHeadsAtOnce; ++i) {
-            if (h + i >= h1)
-                break;
-            const bool is_q = h + i < a.Hq, is_k = h + i < a.Hq + a.Hkv;
-            const Rows &from = is_q ? a.q : (is_k ? a.k : a.v);
-            const int head = h + i - (is_q ? 0 : (is_k ? a.Hq : a.Hq + a.Hkv));
-            const T *p = (const T *)from.base + row * from.row_stride + head * from.head_stride;
-            x[i] = load4(p + group.d0);
-            y[i] = load4(p + group.d1);
-        }
+    for (int i = 0; i < kHeads; ++i) {
+        if (h + i >= all)
+            break;
+        const bool is_q = h + i < a.Hq, is_k = h + i < a.Hq + a.Hkv;
+        const Rows &from = is_q ? a.q : (is_k ? a.k : a.v);
+        const int head = h + i - (is_q ? 0 : (is_k ? a.Hq : a.Hq + a.Hkv));
+        const T *p = (const T *)from.base + row * from.row_stride + head * from.head_stride;
+        x[i] = load4(p + group.d0);
+        y[i] = load4(p + group.d1);
+    }
 #pragma unroll
-        for (int i = 0; i < kHeadsAtOnce; ++i) {
-            if (h + i >= h1)
-                break;
-            const bool is_q = h + i < a.Hq, is_k = h + i < a.Hq + a.Hkv;
-            const int head = h + i - (is_q ? 0 : (is_k ? a.Hq : a.Hq + a.Hkv));
-            if (is_k)
-                group.turn(a, angles, x[i], y[i]);
-            if (!is_q && at < 0)
-                continue;
-            T *to = is_q ? (T *)a.q_out.base + row * a.q_out.row_stride + head * a.q_out.head_stride
-                         : (T *)(is_k ? a.k_pages : a.v_pages) + at + head * a.head_stride;
-            store4(to + group.d0, x[i][0], x[i][1], x[i][2], x[i][3]);
-            store4(to + group.d1, y[i][0], y[i][1], y[i][2], y[i][3]);
-        }
+    for (int i = 0; i < kHeads; ++i) {
+        if (h + i >= all)
+            break;
+        const bool is_q = h + i < a.Hq, is_k = h + i < a.Hq + a.Hkv;
+        const int head = h + i - (is_q ? 0 : (is_k ? a.Hq : a.Hq + a.Hkv));
+        if (is_k)
+            group.turn(a, angles, x[i], y[i]);
+        if (!is_q && at < 0)
+            continue;
+        T *to = is_q ? (T *)a.q_out.base + row * a.q_out.row_stride + head * a.q_out.head_stride
+                     : (T *)(is_k ? a.k_pages : a.v_pages) + at + head * a.head_stride;
+        store4(to + group.d0, x[i][0], x[i][1], x[i][2], x[i][3]);
+        store4(to + group.d1, y[i][0], y[i][1], y[i][2], y[i][3]);
     }
 }
 
@@ -311,7 +311,7 @@ __device__ inline void code_block(const AppendArgs &a, int64_t wave, int lane)
 
 // The first `blocks` wavefronts take blocks of codes, the others rows.
 template <class T, class H, int LPR>
-__global__ __launch_bounds__(kAttnThreads) void append_kernel(AppendArgs a, int64_t blocks, int heads)
+__global__ __launch_bounds__(kAttnThreads) void append_kernel(AppendArgs a, int64_t blocks)
 {
     const int lane = threadIdx.x & 63;
     const int64_t wave = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -321,12 +321,11 @@ __global__ __launch_bounds__(kAttnThreads) void append_kernel(AppendArgs a, int6
             return;
         }
     }
-    move_rows<T, kCodes<H>, LPR>(a, wave - blocks, heads, lane);
+    move_rows<T, kCodes<H>, LPR>(a, wave - blocks, lane);
 }
 
 struct AppendShape {
     int64_t blocks, waves;
-    int heads;
 };
 
 AppendShape append_shape(int held, const AppendArgs &a)
@@ -335,9 +334,7 @@ AppendShape append_shape(int held, const AppendArgs &a)
     const bool codes = held != CACHE_AS_IS;
     const int64_t all = a.Hq + (codes ? 0 : 2 * a.Hkv), per = a.D > 64 ? kRowsPer<16> : kRowsPer<8>;
     sh.blocks = codes ? block_numbers(a) * 2 * a.Hkv : 0;
-    const int64_t groups = (a.T + per - 1) / per;
-    sh.heads = groups * all >= 16384 ? 16 : 4;
-    sh.waves = sh.blocks + groups * ((all + sh.heads - 1) / sh.heads);
+    sh.waves = sh.blocks + (a.T + per - 1) / per * ((all + kHeads - 1) / kHeads);
     return sh;
 }
 
@@ -349,9 +346,9 @@ hipError_t launch_as(int held, const AppendArgs &a, hipStream_t stream)
     if (grid == 0)
         return hipSuccess;
     if (a.D > 64)
-        append_kernel<T, H, 16><<<grid, kAttnThreads, 0, stream>>>(a, sh.blocks, sh.heads);
+        append_kernel<T, H, 16><<<grid, kAttnThreads, 0, stream>>>(a, sh.blocks);
     else
-        append_kernel<T, H, 8><<<grid, kAttnThreads, 0, stream>>>(a, sh.blocks, sh.heads);
+        append_kernel<T, H, 8><<<grid, kAttnThreads, 0, stream>>>(a, sh.blocks);
     return hipGetLastError();
 }
 

@@ -13,12 +13,11 @@
 //   Values: it loads DP / 16 codes from (DP / 16) c on of the eight keys whose
 //   weights it holds; bytes of key pairs are put side by side (one permutation
 //   for two pairs) and widened.
-// The 16 columns of a matrix are COLS query rows (4, 8 or 16: as many as there
-// are) times 16 / COLS steps: the scores of several steps are moved into one
-// register, column by column, before the softmax, which so works on full
-// wavefronts; each step's weights are an operand whose other columns are zero.  A
-// column keeps a maximum and a sum of its own, and the columns of a row are joined
-// at the end.
+// The 16 columns of a matrix are COLS query rows (16, or up to 8 of them) times 16 /
+// COLS steps: the scores of two steps are moved into one register, column by column,
+// before the softmax, which so works on full wavefronts; each step's weights are an
+// operand whose other columns are zero.  A column keeps a maximum and a sum of its
+// own, and the columns of a row are joined at the end.
 // Wavefronts of a workgroup take neighbouring heads (up to four) of the same keys:
 // rows of 128 bytes that are read together lie beside each other in memory.
 // Codes are exact in bf16.  q in fp32 is the sum of three bf16 parts (8 bits
@@ -407,8 +406,7 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
                         y[b][i] = s[b][i];
                     else
                         y[b][i] = __int_as_float(__builtin_amdgcn_update_dpp(
-                            __float_as_int(y[b][i]), __float_as_int(s[b][i]), 0x110 + COLS * st, 0xf,
-                            COLS == 4 ? 1 << st : 0xc, false));
+                            __float_as_int(y[b][i]), __float_as_int(s[b][i]), 0x118, 0xf, 0xc, false));
         };
         bf16x8 pf[PP];
         bool masked = false;
@@ -463,10 +461,6 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
             f(std::integral_constant<int, 0>());
             if constexpr (STEPS > 1)
                 f(std::integral_constant<int, 1>());
-            if constexpr (STEPS > 2) {
-                f(std::integral_constant<int, 2>());
-                f(std::integral_constant<int, 3>());
-            }
         };
         int n = after(n0 - 1);
         if (n < n1) {
@@ -537,19 +531,14 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
         // ---- join the columns of a row, then the wavefronts of a head, and write
         total = sum_quarters(total);
         if constexpr (STEPS > 1) {
-            // row_ror:8, then for four classes row_ror:4
+            // row_ror:8
             float best = top;
             best = fmaxf(best, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(best), 0x128, 15, 15, true)));
-            if constexpr (STEPS > 2)
-                best = fmaxf(best, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(best), 0x124, 15, 15, true)));
             const float f = best == SDL_NEG_INF ? 0.0f : __builtin_amdgcn_exp2f(top - best);
             top = best;
             auto joined = [&](float v) {
                 v *= f;
-                v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x128, 15, 15, true));
-                if constexpr (STEPS > 2)
-                    v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x124, 15, 15, true));
-                return v;
+                return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x128, 15, 15, true));
             };
             total = joined(total);
 #pragma unroll
@@ -1024,8 +1013,6 @@ hipError_t launch_stream(const TreeArgs &a, hipStream_t stream)
 {
     if (!a.together)
         tree_stream<T, H, DP, 16, false><<<a.workers, kAttnThreads, 0, stream>>>(a);
-    else if (a.block_rows == 4)
-        tree_stream<T, H, DP, 4, true><<<a.workers, kAttnThreads, 0, stream>>>(a);
     else if (a.block_rows == 8)
         tree_stream<T, H, DP, 8, true><<<a.workers, kAttnThreads, 0, stream>>>(a);
     else

@@ -232,8 +232,8 @@ def test_moves_refuse_the_rest():
 @pytest.mark.parametrize("call,held", [(c, h) for c in range(3) for h in (E4M3, INT8)])
 def test_calls_that_no_launch_holds_are_refused(call, held):
     edge = 1 << 24
-    # blocks of four queries: ten queries have two numbers more than there are sequences
-    calls = [(lambda n: tree(tshape(S=n, Hq=1, Hkv=1), held=held), edge - 3),
+    # blocks of eight queries: ten queries have one number more than there are sequences
+    calls = [(lambda n: tree(tshape(S=n, Hq=1, Hkv=1), held=held), edge - 2),
              (lambda n: copy(pool(layers=64), count=n), edge // 128 - 1),
              (lambda n: compact(S=n, held=held), edge - 1)]
     run, most = calls[call]
