@@ -9,6 +9,11 @@
 // before the first code is written: a wavefront takes one block of one head
 // and one pool, and keeps its rows in registers, or reads them again from L2
 // where there are more than it holds.
+//
+// Bound by memory: 16384 rows of bf16, 48 heads of 128, 411 MB in 81 us = 5.1 TB/s,
+// the rate of a large copy; 8192 rows into codes, 189 MB in 37 us (46 with caches that
+// other work has filled).  A batch of single rows takes 6 to 8 us, a launch and four
+// loads that wait for each other: the sequence, its context, the page, the scale.
 #include "ops.h"
 
 #include "cache.h"
