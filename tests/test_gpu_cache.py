@@ -807,6 +807,31 @@ def test_compact_heads(held, heads, D):
 
 
 @CODES
+@pytest.mark.parametrize("kept", [3, 12])
+def test_moves_past_32_bits(held, kept):
+    """Pages more than 2^32 bytes from the first one of a layer, in the last of two
+    layers, against the same pages in a small pool."""
+    page, block, heads, D, few = 16, 8, 2, 64, 6
+    small = [x.cuda() for x in layered(2, few, page, block, heads, D, held, 31)]
+    pages = (1 << 32) // (page * heads * D) + few
+    at = [pages - 1, 0, pages - 2, 5, (1 << 31) // (page * heads * D), pages // 2]
+    big = [torch.empty((2, pages, *x.shape[2:]), dtype=torch.uint8, device="cuda").view(held) for x in small[:2]]
+    big += [torch.empty((2, pages, *x.shape[2:]), device="cuda") for x in small[2:]]
+    for b, x in zip(big, small):
+        for i, n in enumerate(at):
+            b[:, n].copy_(x[:, i])
+    keep = i32([[2 * t + 1 for t in range(kept)]])
+    for pools, name in ((small, list(range(few))), (big, at)):
+        kw = dict(k_scale=pools[2], v_scale=pools[3])
+        sdl.copy_pages(*pools[:2], i32([name[0]]), i32([name[3]]), **kw)
+        sdl.compact_pages(*pools[:2], i32([[name[1], name[3], name[2], name[4], name[5]]]), i32([19]), keep, **kw)
+    torch.cuda.synchronize()
+    for b, x in zip(big, small):
+        for i, n in enumerate(at):
+            assert torch.equal(bits(b[:, n]), bits(x[:, i])), (i, n)
+
+
+@CODES
 def test_compact_long_lists(held):
     """More kept rows than are found at once, in one block and over many."""
     check_compact(held, 1, 256, 256, 1, 32, [40, 250], [list(range(1, 180)), list(range(0, 400, 2))])
