@@ -279,27 +279,43 @@ __global__ __launch_bounds__(kAttnThreads) void compact_few(PagesArgs a, int ite
         const bool mine = t < kFew && t < a.kept;
         const int64_t of = mine ? keep[t] : 0;
         const uint64_t ends = __ballot(mine && of < 0);        // nothing counts from the first on
-        auto row_at = [&](int64_t pos) -> int64_t {
-            if (pos < 0 || pos / a.page >= a.table_stride)
-                return -1;
-            const int64_t number = table[pos / a.page];
-            return number < 0 || number >= a.pages ? -1 : number * a.page + pos % a.page;
+        // a position's row and block, -1 if it has none (positions and sizes fit 32 bits;
+        // a division of 64 costs some hundred instructions)
+        const uint32_t page = (uint32_t)a.page, block = (uint32_t)a.block, blocks = page / block;
+        auto find = [&](int64_t pos, int64_t &row, int64_t &block_row) {
+            row = -1;
+            const uint32_t p = (uint32_t)pos / page, in = (uint32_t)pos - p * page;
+            if (pos < 0 || p >= a.table_stride)
+                return;
+            const int64_t number = table[p];
+            if (number < 0 || number >= a.pages)
+                return;
+            row = number * page + in;
+            block_row = number * blocks + in / block;
         };
         if (t < kFew) {
             const bool counts = mine && (ends & (((uint64_t)2 << t) - 1)) == 0;
-            const int64_t f = counts ? row_at(ctx + of) : -1, g = f < 0 ? -1 : row_at(ctx + t);
-            from[t] = g < 0 ? -1 : f;
-            to[t] = g;
-            from_block[t] = g < 0 ? 0 : f / a.block;
-            to_block[t] = g < 0 ? 0 : g / a.block;
+            int64_t f = -1, g = -1, f_block = 0, g_block = 0;
+            if (counts) {
+                find(ctx + of, f, f_block);
+                find(ctx + t, g, g_block);
+            }
+            const bool moves = f >= 0 && g >= 0;
+            from[t] = moves ? f : -1;
+            to[t] = moves ? g : -1;
+            from_block[t] = moves ? f_block : 0;
+            to_block[t] = moves ? g_block : 0;
         }
     }
     __syncthreads();
     const int off = (int)(ctx % a.block);                      // rows of the context in the first block
     int which[kFew];                                           // block of the i-th place
+    which[0] = 0;
 #pragma unroll
-    for (int i = 0; i < kFew; ++i)
-        which[i] = (off + i) / (int)a.block;
+    for (int i = 1, in = off; i < kFew; ++i) {
+        in = in + 1 == (int)a.block ? 0 : in + 1;
+        which[i] = which[i - 1] + (in == 0 ? 1 : 0);
+    }
     const uint32_t turn = kAttnThreads / (D / 16) * (D / 16);  // whole heads
     for (uint32_t m0 = 0; m0 < all; m0 += turn) {
         const uint32_t m = m0 + t, item = m / cols, col = m - item * cols;
@@ -327,14 +343,14 @@ __global__ __launch_bounds__(kAttnThreads) void compact_few(PagesArgs a, int ite
                 into = which[i] == 0 && from[i] >= 0 ? i : into;
             if (off > 0 && into >= 0)
                 before = scales[to_block[into] * a.heads];
+            // the largest so far of each block (where nothing comes from: 0), then of all
+            now[0] = larger_scale(before, come[0]);
 #pragma unroll
-            for (int i = 0; i < kFew; ++i) {
-                now[i] = which[i] == 0 ? before : 0.0f;
+            for (int i = 1; i < kFew; ++i)
+                now[i] = which[i] == which[i - 1] ? larger_scale(now[i - 1], come[i]) : come[i];
 #pragma unroll
-                for (int j = 0; j < kFew; ++j)
-                    if (from[j] >= 0 && which[j] == which[i])
-                        now[i] = larger_scale(now[i], come[j]);
-            }
+            for (int i = kFew - 2; i >= 0; --i)
+                now[i] = which[i] == which[i + 1] ? now[i + 1] : now[i];
             auto convert = [&](u32x4 x, float old, const Divide &divide) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
