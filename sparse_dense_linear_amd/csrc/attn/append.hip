@@ -135,14 +135,14 @@ constexpr int kHeads = 4;
 // Rows of q and, where the pools hold them as they are, of k and v: kRowsPer
 // rows to a wavefront and kHeads heads of them, counted through q, k and v.
 template <class T, bool CODES, int LPR>
-__device__ inline void move_rows(const AppendArgs &a, int64_t wave, int lane)
+__device__ inline void move_rows(const AppendArgs &a, uint32_t wave, int lane)
 {
     constexpr int ROWS = kRowsPer<LPR>;
     const int all = a.Hq + (CODES ? 0 : 2 * a.Hkv), parts = (all + kHeads - 1) / kHeads;
     if (all == 0)
         return;
-    const int h = (int)(wave % parts) * kHeads;
-    const int64_t first = wave / parts * ROWS;
+    const int h = (int)(wave % (uint32_t)parts) * kHeads;
+    const int64_t first = (int64_t)(wave / (uint32_t)parts) * ROWS;
     if (first >= a.T)
         return;
     int seq = -1;
@@ -199,22 +199,24 @@ __device__ inline void move_rows(const AppendArgs &a, int64_t wave, int lane)
 // numbers from rowptr[s] / block + 2 s on.
 __host__ __device__ inline int64_t block_numbers(const AppendArgs &a) { return a.T / a.block + 2 * (int64_t)a.S; }
 
-// One block of one head and one pool, by a wavefront.
+// One block of one head and one pool, by a wavefront.  (Wavefronts, positions and rows
+// fit 32 bits; a division of 64 costs some hundred instructions.)
 template <class T, class H, int LPR>
-__device__ inline void code_block(const AppendArgs &a, int64_t wave, int lane)
+__device__ inline void code_block(const AppendArgs &a, uint32_t wave, int lane)
 {
     constexpr int ROWS = kRowsPer<LPR>, kHold = 4;
-    const int which = (int)(wave % (2 * a.Hkv));
-    const int64_t number = wave / (2 * a.Hkv);
+    const uint32_t columns = 2 * (uint32_t)a.Hkv, block = (uint32_t)a.block;
+    const int which = (int)(wave % columns);
+    const int64_t number = wave / columns;
     const bool is_k = which < a.Hkv;
     const int head = is_k ? which : which - a.Hkv;
-    const int seq = last_not_above([&](int n) { return (int64_t)a.rowptr[n] / a.block + 2 * (int64_t)n; }, a.S,
-                                   number, lane);
+    const int seq = last_not_above([&](int n) { return (int64_t)((uint32_t)a.rowptr[n] / block) + 2 * (int64_t)n; },
+                                   a.S, number, lane);
     if (seq < 0)
         return;
     const Rowed rows(a, seq);
     const int64_t begin =
-        ((int64_t)rows.ctx / a.block + number - (rows.first / a.block + 2 * (int64_t)seq)) * a.block;
+        ((int64_t)((uint32_t)rows.ctx / block) + number - ((uint32_t)rows.first / block + 2 * (int64_t)seq)) * block;
     const int64_t end = (int64_t)rows.ctx + rows.count;
     if (rows.count <= 0 || begin >= end)
         return;
@@ -319,14 +321,14 @@ template <class T, class H, int LPR>
 __global__ __launch_bounds__(kAttnThreads) void append_kernel(AppendArgs a, int64_t blocks)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t wave = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t wave = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if constexpr (kCodes<H>) {
-        if (wave < blocks) {
+        if (wave < (uint32_t)blocks) {
             code_block<T, H, LPR>(a, wave, lane);
             return;
         }
     }
-    move_rows<T, kCodes<H>, LPR>(a, wave - blocks, lane);
+    move_rows<T, kCodes<H>, LPR>(a, wave - (uint32_t)blocks, lane);
 }
 
 struct AppendShape {
