@@ -431,11 +431,13 @@ struct Cut {
         const int number = blockIdx.x % numbers;
         hk = blockIdx.x / numbers;
         const int64_t tiles = slots.base[a.S];
+        // (all queries are fewer than 2^31)
+        auto first = [&](int s) { return (int)((uint32_t)a.q_rowptr[s] * (uint32_t)group / (uint32_t)RB) + s; };
         int left = a.S;              // the last sequence whose first number is <= number
         seq = 0;
         while (left > 1) {
             const int step = (left + 63) / 64, s = seq + lane * step;
-            const bool at = lane * step < left && (int64_t)a.q_rowptr[s] * group / RB + s <= number;
+            const bool at = lane * step < left && first(s) <= number;
             const int n = __popcll(__ballot(at)) - 1;
             if (n < 0)
                 return false;
@@ -443,7 +445,7 @@ struct Cut {
             left = left - n * step < step ? left - n * step : step;
         }
         u = unit_of<H>(a, seq);
-        block = number - (int)((int64_t)u.q_begin * group / RB + seq);
+        block = number - first(seq);
         if (block < 0 || block >= u.blocks || block * RB + row0 >= u.drafts * group)
             return false;
         Spans spans;
