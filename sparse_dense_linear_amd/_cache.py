@@ -55,7 +55,7 @@ def append_pages(k, v, k_pages, v_pages, table, ctx, rowptr, q=None, cos=None, s
     need a larger one than the rows before them, these are rounded to it.
 
     Returns the rotated q (q_out, which may be q itself; None: allocated, on
-    `stream` if given), or None without q."""
+    `stream` if given), or None without q.  Records no autograd graph."""
     device = _first(k, "k", 3, "three dimensions: rows, heads, D")
     torch = _attn.torch
     dt = _dtype(k, "k")

@@ -27,6 +27,29 @@ struct DraftSeen {
     }
 };
 
+// What draft t sees of 32 keys from j0 on, bit by bit.
+struct BlockSeen {
+    int pos, cached;      // where it stands; keys before `cached` go by the window alone
+    uint64_t mask;        // of the drafts it sees (0: a chain, whose keys all lie before `cached`)
+    __host__ __device__ static uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1); }
+    // Drops the drafts that the window hides, once for all blocks (further apart than
+    // 63 they do not stand).
+    __host__ __device__ void keep_near(const int *place, int window, int sinks)
+    {
+        if (window < 64)
+            for (int d = 0; d < 64; ++d)
+                if (mask >> d & 1 && pos - place[d] >= window && place[d] >= sinks)
+                    mask &= ~((uint64_t)1 << d);
+    }
+    __host__ __device__ uint32_t operator()(int j0, int ctx, int window, int sinks) const
+    {
+        const uint32_t near = (~below(pos - window + 1 - j0) | below(sinks - j0)) & below(cached - j0);
+        const int d = j0 - ctx;
+        const uint64_t drafts = d >= 64 || d <= -32 ? 0 : (d >= 0 ? mask >> d : mask << -d);
+        return near | (uint32_t)drafts;
+    }
+};
+
 // The drafts of its sequence that a mask names.
 SDL_BOTH uint64_t draft_mask(uint64_t mask, int drafts)
 {

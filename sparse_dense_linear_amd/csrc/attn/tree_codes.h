@@ -606,20 +606,6 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
     }
 }
 
-// What a query sees of 32 keys from j0 on, bit by bit.
-struct BlockSeen {
-    int pos, cached;      // where it stands; keys before `cached` go by the window alone
-    uint64_t mask;        // of the drafts it sees (0: a chain, whose keys all lie before `cached`)
-    __device__ static uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1); }
-    __device__ uint32_t operator()(int j0, int ctx, int window, int sinks) const
-    {
-        const uint32_t near = (~below(pos - window + 1 - j0) | below(sinks - j0)) & below(cached - j0);
-        const int d = j0 - ctx;
-        const uint64_t drafts = d >= 64 || d <= -32 ? 0 : (d >= 0 ? mask >> d : mask << -d);
-        return near | (uint32_t)drafts;
-    }
-};
-
 // Blocks of 32 to 128 query rows, RG groups of C of them; the 4 / RG wavefronts of a
 // group share the keys of a tile.  Tiles of 128 keys are widened to bf16 on their way
 // into LDS, once for all query groups; the next tile is under way while one is worked
@@ -822,10 +808,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void tree_tiles(TreeArgs a)
             }
         };
         __syncthreads();                       // what the drafts see is there
-        if (a.tree != nullptr && a.window < 64)
-            for (int d = 0; d < 64; ++d)       // (further apart they do not stand)
-                if (seen.mask >> d & 1 && seen.pos - drafts.place[d] >= a.window && drafts.place[d] >= a.sinks)
-                    seen.mask &= ~((uint64_t)1 << d);
+        if (a.tree != nullptr)
+            seen.keep_near(drafts.place, a.window, a.sinks);
         const bool finds = t < KEYS;           // the first two wavefronts
         if (finds && n0 < e1) {
             find_row(n0);
