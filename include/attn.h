@@ -34,8 +34,8 @@
  *
  * Preconditions, as for the CSR arrays of spmm.h not checked by the fast
  * path: row pointers non-decreasing and within the row counts, page numbers
- * (of what a draft may see) within the pool, tables long enough, contexts with
- * their drafts below 2^30.  Outputs, gradients and scratch memory overlap
+ * (of what a draft may see) within the pool, tables long enough, contexts from 0
+ * on and, with their drafts, below 2^30.  Outputs, gradients and scratch memory overlap
  * neither each other nor any input: rows are written while others are still
  * read, and a row that comes out non-finite is computed again from its inputs.
  * (Inputs may overlap each other.)

@@ -77,8 +77,8 @@ typedef struct cache_scales {
  *
  * q_out takes the rotated q; it may be q itself.  Hq = 0: no queries, q and
  * q_out are not looked at.  v is stored as it is.  Rows of k and v whose table
- * index or page number (0 .. pages - 1) is out of range are passed over, in
- * pools of codes whole blocks.  Nothing else of the pools is written but, in
+ * index or page number (0 .. pages - 1) is out of range, or whose position is
+ * negative, are passed over, in pools of codes whole blocks.  Nothing else of the pools is written but, in
  * pools of codes, the scales and the earlier rows of the blocks written to.
  * Strides by which rows of a pool, or scales, would overlap are refused.
  */

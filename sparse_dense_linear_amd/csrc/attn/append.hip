@@ -59,7 +59,7 @@ struct Group {
     {
         const float nan = __builtin_nanf("");
         Angles t = {f32x4(nan), f32x4(nan)};
-        if (turned && place < a.angles) {
+        if (turned && has_angles(place, a.angles)) {
             const int64_t at = (int64_t)place * (a.rotated / 2) + 4 * g;
             t.c = *(const f32x4 *)(a.cosines + at);
             t.s = *(const f32x4 *)(a.sines + at);
@@ -216,7 +216,7 @@ __device__ inline void code_block(const AppendArgs &a, uint32_t wave, int lane)
         return;
     const Rowed rows(a, seq);
     const int64_t begin =
-        ((int64_t)((uint32_t)rows.ctx / block) + number - ((uint32_t)rows.first / block + 2 * (int64_t)seq)) * block;
+        (block_of(rows.ctx, a.block) + number - ((uint32_t)rows.first / block + 2 * (int64_t)seq)) * block;
     const int64_t end = (int64_t)rows.ctx + rows.count;
     if (rows.count <= 0 || begin >= end)
         return;

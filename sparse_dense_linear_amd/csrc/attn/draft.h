@@ -62,6 +62,18 @@ SDL_BOTH int draft_place(int ctx, uint64_t mask)
     return ctx + (n > 1 ? n - 1 : 0);
 }
 
+// Whether the tables of a rotation have the position where a row stands.
+SDL_BOTH bool has_angles(int place, int angles) { return (uint32_t)place < (uint32_t)angles; }
+
+// The block of positions (of `block` each) that holds a position, also one in front of
+// the sequence, which no page holds.
+SDL_BOTH int64_t block_of(int pos, int block)
+{
+    // (32 bits: a division of 64 costs some hundred instructions)
+    return pos >= 0 ? (int64_t)((uint32_t)pos / (uint32_t)block)
+                    : -1 - (int64_t)((uint32_t)~pos / (uint32_t)block);
+}
+
 // The keys that some draft of a sequence sees.  No other row of the cache may
 // be read: its page may have been given away, and the table's entry may be
 // anything.
