@@ -22,9 +22,12 @@
  * earlier rows, its scale is the larger of s and the one it had; if that
  * raises it, the codes of the earlier rows become round(code * old / new).
  * A code is round(x / scale), to nearest even, and products and quotients are
- * rounded once each to fp32.  With powers of two that is exact but for the last
- * rounding, so raising a scale costs codes of e4m3 nothing (but for those below
- * the smallest normal one), and integers their last bit.
+ * rounded once each to fp32.  Where x is finite and that code times its scale is
+ * not, it is the next smaller code (values from 248 * 2^120 on are held as 240 *
+ * 2^120, in integers from 63.5 * 2^122 on as 63 * 2^122).  With powers of two that
+ * is exact but for the last rounding, so raising a scale costs codes of e4m3
+ * nothing (but for those below the smallest normal one), and integers their last
+ * bit.
  * A value that is not finite becomes the code NaN in e4m3.  Integers have no
  * such code: the scale of its block and head becomes NaN, and all rows of the
  * block and head read as NaN until the block is begun anew.  Rows of a block

@@ -285,8 +285,8 @@ __device__ inline void code_block(const AppendArgs &a, uint32_t wave, int lane)
         for (int r = lane / LPR; r < lo; r += ROWS) {
             uint32_t *w = (uint32_t *)(pool + (int64_t)r * a.row_stride + 8 * group.g);
             const f32x4 u = wide<H>(w[0]), v = wide<H>(w[1]);
-            w[0] = narrow<H>(divide(f32x4{u[0] * before, u[1] * before, u[2] * before, u[3] * before}));
-            w[1] = narrow<H>(divide(f32x4{v[0] * before, v[1] * before, v[2] * before, v[3] * before}));
+            w[0] = divide.codes<H>(f32x4{u[0] * before, u[1] * before, u[2] * before, u[3] * before});
+            w[1] = divide.codes<H>(f32x4{v[0] * before, v[1] * before, v[2] * before, v[3] * before});
         }
     }
     auto put = [&](int r, f32x4 u, f32x4 w) {
@@ -298,8 +298,8 @@ __device__ inline void code_block(const AppendArgs &a, uint32_t wave, int lane)
             }
         }
         H *to = pool + (int64_t)r * a.row_stride;
-        *(uint32_t *)(to + group.d0) = narrow<H>(divide(u));
-        *(uint32_t *)(to + group.d1) = narrow<H>(divide(w));
+        *(uint32_t *)(to + group.d0) = divide.codes<H>(u);
+        *(uint32_t *)(to + group.d1) = divide.codes<H>(w);
     };
     if (group.in) {
 #pragma unroll

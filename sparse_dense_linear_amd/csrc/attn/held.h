@@ -83,6 +83,15 @@ __device__ inline uint32_t narrow(f32x4 x)
     }
 }
 
+// Code number e of w next nearer to zero.
+template <class H>
+__device__ inline uint32_t smaller(uint32_t w, int e, bool negative)
+{
+    const uint32_t code = w >> (8 * e) & 0xff;
+    const uint32_t to = std::is_same_v<H, Int8> && negative ? code + 1 : code - 1;
+    return (w & ~(0xffu << (8 * e))) | (to & 0xff) << (8 * e);
+}
+
 // The smallest power of two s >= 2^-126 with top <= kMost s, for a finite top >= 0.
 template <class H>
 __device__ inline float scale_of_top(float top)
@@ -110,6 +119,26 @@ struct Divide {
         if (power)
             return f32x4{x[0] * inverse, x[1] * inverse, x[2] * inverse, x[3] * inverse};
         return f32x4{x[0] / by, x[1] / by, x[2] / by, x[3] / by};
+    }
+    // Codes of four values.  Next to the end of fp32's range rounding up may lead to a
+    // code that times its scale is infinite (from 248 * 2^120 on 256 * 2^120): then the
+    // next smaller one, so that what is finite is read as finite.
+    template <class H>
+    __device__ uint32_t codes(f32x4 x) const
+    {
+        const f32x4 q = (*this)(x);
+        uint32_t w = narrow<H>(q);
+        if (by >= 0x1p119f) {                  // below, 448 times the scale is finite
+#pragma unroll
+            for (int step = 0; step < 2; ++step) {     // (twice: quotients by other scales are rounded)
+                const f32x4 code = wide<H>(w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (finite(q[e]) && !finite(code[e] * by))
+                        w = smaller<H>(w, e, code[e] < 0.0f);
+            }
+        }
+        return w;
     }
 };
 

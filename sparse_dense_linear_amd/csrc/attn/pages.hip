@@ -219,7 +219,7 @@ __global__ __launch_bounds__(kAttnThreads) void compact_codes(PagesArgs a)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const f32x4 u = wide<H>(x[e]);
-                        y[e] = narrow<H>(divide(f32x4{u[0] * old, u[1] * old, u[2] * old, u[3] * old}));
+                        y[e] = divide.codes<H>(f32x4{u[0] * old, u[1] * old, u[2] * old, u[3] * old});
                     }
                 *(u32x4 *)(pool[c] + dest * a.row_bytes) = y;
             };
@@ -355,7 +355,7 @@ __global__ __launch_bounds__(kAttnThreads) void compact_few(PagesArgs a, int ite
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const f32x4 u = wide<H>(x[e]);
-                    x[e] = narrow<H>(divide(f32x4{u[0] * old, u[1] * old, u[2] * old, u[3] * old}));
+                    x[e] = divide.codes<H>(f32x4{u[0] * old, u[1] * old, u[2] * old, u[3] * old});
                 }
                 return x;
             };

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import sparse_dense_linear_amd as sdl
-from cache_ref import E4M3, INT8
+from cache_ref import E4M3, INT8, MOST, codes_of, scale_of_top
 from test_gpu_cache import BF16, CODES, F32, KINDS, TYPES, a_pool, bits, i32, tables
 
 pytestmark = [pytest.mark.gpu,
@@ -38,3 +38,74 @@ def test_append_in_front_of_a_sequence(dtype, kind, ctx):
     assert torch.equal(out[:front, :, rotated:], q[:front, :, rotated:])
     for x, y in zip(got, want):
         assert x is None or torch.equal(bits(x), bits(y))
+
+
+def held_as(x, scale, held):
+    """The codes of finite x, in 64 bits: the nearest one whose value is finite in fp32,
+    of two that are as near the even one."""
+    every = torch.arange(256, dtype=torch.uint8).view(held)
+    every = every[every.float().isfinite() & (every.float() >= -MOST[held])]
+    every = every[(every.float() * scale).isfinite()]
+    even = every.view(torch.uint8) % 2 if held is E4M3 else every % 2 != 0
+    off = (every.double() * float(scale) - x.double()[..., None]).abs() / float(scale)
+    return every.float()[(off * 2.0 ** 40 + even.double()).argmin(-1)]
+
+
+@TYPES
+@CODES
+def test_finite_values_are_read_as_finite(dtype, held):
+    """Next to the end of fp32's range, where the nearest code would be read as infinite."""
+    top = float(torch.finfo(dtype).max)
+    end = 2.0 ** 128
+    for most in (0.9, 0.96, 0.96875, 0.97, 0.9921875, 0.99609375):
+        x = torch.zeros(3, 1, 16)
+        for i, part in enumerate((1.0, 0.999, 0.97, 0.9375, 0.8, 0.51, 0.25, 0.01)):
+            x[i % 3, 0, i], x[i % 3, 0, i + 8] = most * part * end, -most * part * end
+        x = x.to(dtype)
+        x[1, 0, 15] = top
+        assert bool(x.isfinite().all())
+        pools = [codes_of(torch.zeros(1, 16, 1, 16), held).cuda() for _ in range(2)]
+        ks, vs = (torch.zeros(1, 2, 1, device="cuda") for _ in range(2))
+        sdl.append_pages(x.cuda(), x.cuda(), *pools, i32([[0]]), i32([0]), i32([0, 3]), k_scale=ks, v_scale=vs)
+        for pool, scale in zip(pools, (ks, vs)):
+            scale = scale[0, 0, 0].cpu()
+            assert float(scale) == scale_of_top(top, held)
+            assert torch.equal(pool[0, :3].cpu().float(), held_as(x.float(), scale, held))
+            assert bool((pool[0, :3].cpu().float() * scale).isfinite().all())
+        # and so is attention of the first row alone
+        q = torch.zeros(1, 1, 16, dtype=dtype, device="cuda")
+        o, lse = sdl.tree_attention(q, *pools, i32([[0]]), i32([0]), i32([0, 1]), k_scale=ks, v_scale=vs)
+        assert torch.equal(o[0].float(), (pool[0, 0].float() * vs[0, 0, 0]).to(dtype).float()) and float(lse) == 0.0
+
+
+@pytest.mark.parametrize("kept", [2, 9])
+def test_integers_whose_scale_rises_are_read_as_finite(kept):
+    """127 * 2^121 under a scale of 2^122: 63.5, whose nearest even code would be read as
+    infinite.  Raised by appending, and by moves (both kernels) into another block."""
+    top = torch.finfo(F32).max
+    small, large = (torch.full((1, 1, 16), x, device="cuda") for x in (127 * 2.0 ** 121, top))
+    small[0, 0, 1] = -small[0, 0, 1]
+    want = torch.full((1, 16), 63.0)
+    want[0, 1] = -63.0
+
+    def pool():
+        return ([codes_of(torch.zeros(1, 32, 1, 16), INT8).cuda() for _ in range(2)],
+                dict(zip(("k_scale", "v_scale"), (torch.ones(1, 2, 1, device="cuda") for _ in range(2)))))
+
+    table = i32([[0]])
+    pools, scales = pool()
+    for t, x in enumerate((small, large)):
+        sdl.append_pages(x, x, *pools, table, i32([t]), i32([0, 1]), **scales)
+    for p, s in zip(pools, scales.values()):
+        assert float(s[0, 0, 0]) == 2.0 ** 122
+        assert torch.equal(p[0, 0].cpu().float(), want) and torch.equal(p[0, 1].cpu().float(), want.abs())
+    # the same two rows, each of a block of its own, brought together
+    pools, scales = pool()
+    for t, x in ((3, small), (16, large)):
+        sdl.append_pages(x, x, *pools, table, i32([t]), i32([0, 1]), **scales)
+    keep = [0, 13] + [-1] * (kept - 2)
+    sdl.compact_pages(*(p[None] for p in pools), table, i32([3]), i32([keep]),
+                      **{n: s[None] for n, s in scales.items()})
+    for p, s in zip(pools, scales.values()):
+        assert float(s[0, 0, 0]) == 2.0 ** 122
+        assert torch.equal(p[0, 3].cpu().float(), want) and torch.equal(p[0, 4].cpu().float(), want.abs())
