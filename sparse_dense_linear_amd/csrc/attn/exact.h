@@ -8,11 +8,12 @@
 // more here, from the pairs that are seen alone, if a row that a masked pair
 // of its tiles brought in is not finite (any_odd): a few dozen rows at the
 // edges of the window.  An output whose sum left the range of fp32 before it was
-// divided (weights reach 2^8 there, TooLarge) is computed again too.  So
-// infinities and NaN that are seen cost no more than those two looks, and the
-// tiles pay one test per output.  Finite data come here only so, and for a
-// draft that sees no key.  A row all of whose elements have become NaN is not
-// followed to its end.
+// divided (weights reach 2^8 there) is computed again too (too_large).  So a value that
+// is seen and not finite costs those two looks, of which the second goes over all
+// values (OddColumns), and the tiles pay one test per output.  Finite data come here
+// only so, and for a draft that sees no key; so do scores that are infinite or, over
+// rows, no number.  A row all of whose elements have become NaN is not followed to its
+// end.
 #pragma once
 
 #include "tile.h"
@@ -61,30 +62,87 @@ __device__ inline bool any_odd(Row row, int from, int to, int D, int lane)
     return any_odd(row, [](int) { return true; }, from, to, D, lane);
 }
 
-// Whether an output is infinite or no number though no value that it sums up is:
-// first the columns in which some value is not finite (of rows that may be
-// more than a query sees), then, for each output, what it holds in the others.
-template <class T>
-struct TooLarge {
-    bool odd0 = false, odd1 = false;           // of the lane's columns, lane and lane + 64
+// x of lane n.  (Not __shfl, whose indexes the compiler would find once for the whole
+// kernel and keep in registers all along.)
+__device__ inline int of_lane(int x, int n) { return __builtin_amdgcn_ds_bpermute(n << 2, x); }
+__device__ inline int of_one_lane(int x, int n) { return __builtin_amdgcn_readlane(x, n); }      // the same n in all lanes
+
+// The row whose address lane n has found; ONE: the same n in all lanes.
+template <bool ONE, class T>
+__device__ inline const T *row_of_lane(const T *row, int n)
+{
+    const uint64_t at = (uint64_t)(uintptr_t)row;
+    const uint32_t lo = ONE ? of_one_lane((int)at, n) : of_lane((int)at, n);
+    const uint32_t hi = ONE ? of_one_lane((int)(at >> 32), n) : of_lane((int)(at >> 32), n);
+    return (const T *)(uintptr_t)((uint64_t)hi << 32 | lo);
+}
+
+// Columns in which some row of many holds an infinity or a NaN.  A wavefront finds
+// the addresses of 64 rows at once and looks at four of them at a time, 16 lanes to a
+// row, with no load behind a branch.
+struct OddColumns {
+    uint32_t odd = 0;          // of the lane's columns, 8 (lane % 16) .. + 7
+    // rows from .. to - 1 that counts(j) lets through, 64 of them in turn to each of `waves`
     template <class Row, class Counts>
-    __device__ void look(Row val, Counts counts, int from, int to, int D, int lane)
+    __device__ void look(Row at, Counts counts, int from, int to, int D, int lane, int wave = 0, int waves = 1)
     {
-#pragma unroll 4
-        for (int j = from; j < to; ++j) {
-            if (!counts(j))
+        const int part = lane & 15, d = 8 * part < D ? 8 * part : 0;
+        uint32_t found = 0;
+        for (int j0 = from + 64 * wave; j0 < to; j0 += 64 * waves) {
+            const int j = j0 + lane;
+            const bool mine = j < to && counts(j);
+            const uint64_t rows = __ballot(mine);
+            if (rows == 0)
                 continue;
-            const auto v = val(j);
-            odd0 = odd0 || (lane < D && !finite((float)v[lane]));
-            odd1 = odd1 || (lane + 64 < D && !finite((float)v[lane + 64]));
+            // a row that does not count is replaced by one that does
+            const int some = __ffsll((unsigned long long)rows) - 1;
+            decltype(at(j)) row{};
+            if (mine)
+                row = at(j);
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const int n = 4 * i + (lane >> 4);
+                const auto x = load8(row_of_lane<false>(row, rows >> n & 1 ? n : some) + d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    found |= finite((float)x[e]) ? 0u : 1u << e;
+            }
         }
+        odd |= 8 * part < D ? found : 0u;
     }
-    __device__ bool operator()(const T *o, int D, int lane) const
+    // what the wavefronts have found, together; by all of the workgroup's
+    __device__ void join(int lane, int wave)
     {
-        return __any((lane < D && !odd0 && !finite((float)o[lane])) ||
-                     (lane + 64 < D && !odd1 && !finite((float)o[lane + 64])));
+        __shared__ uint32_t columns[16];
+        __syncthreads();                       // an earlier call's have been read
+        if (wave == 0)
+            columns[lane & 15] = 0;
+        __syncthreads();
+        atomicOr(&columns[lane & 15], odd);
+        __syncthreads();
+        odd = columns[lane & 15];
+    }
+    // of lanes with the same columns
+    __device__ uint32_t all() const
+    {
+        auto two = __builtin_amdgcn_permlane16_swap(odd, odd, false, false);
+        const uint32_t x = two[0] | two[1];
+        two = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        return two[0] | two[1];
     }
 };
+
+// Whether an output is infinite or no number in a column in which no value that it
+// sums up is (`values`: of rows that may be more than a query sees).
+template <class T>
+__device__ inline bool too_large(const OddColumns &values, const T *o, int D, int lane)
+{
+    const uint32_t odd = values.all();
+    const bool odd0 = of_lane(odd, lane >> 3) >> (lane & 7) & 1;
+    const bool odd1 = of_lane(odd, 8 + (lane >> 3)) >> (lane & 7) & 1;
+    return __any((lane < D && !odd0 && !finite((float)o[lane])) ||
+                 (lane + 64 < D && !odd1 && !finite((float)o[lane + 64])));
+}
 
 // Whether every lane's share of a row has become NaN.
 __device__ inline bool all_nan(float a0, float a1, int D, int lane)
@@ -114,6 +172,35 @@ __device__ inline void add_row(Row row, float w, int D, int lane, float &a0, flo
         a0 = fmaf(w, (float)row[lane], a0);
     if (lane + 64 < D)
         a1 = fmaf(w, (float)row[lane + 64], a1);
+}
+
+// The same of the rows whose lanes `left` names, one after another, each by its
+// lane's weight; several are under way at once.
+template <class Row>
+__device__ inline void add_rows(Row row, float w, uint64_t left, int D, int lane, float &a0, float &a1)
+{
+    constexpr int kBatch = 8;
+    if (left == 0)
+        return;
+    const int some = __ffsll((unsigned long long)left) - 1;
+#pragma unroll 1
+    for (int n0 = 0; n0 < 64; n0 += kBatch) {
+        const uint32_t which = (uint32_t)(left >> n0);
+        float x0[kBatch], x1[kBatch], by[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {     // (in the place of one that does not count: some other, not added)
+            const int n = which >> i & 1 ? n0 + i : some;
+            const Row r = row_of_lane<true>(row, n);
+            x0[i] = (float)r[lane < D ? lane : 0];
+            x1[i] = (float)r[lane + 64 < D ? lane + 64 : 0];
+            by[i] = __int_as_float(of_one_lane(__float_as_int(w), n));
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            a0 = which >> i & 1 ? fmaf(by[i], x0[i], a0) : a0;
+            a1 = which >> i & 1 ? fmaf(by[i], x1[i], a1) : a1;
+        }
+    }
 }
 
 template <class T>
@@ -160,12 +247,14 @@ __device__ inline void exact_row(const T *q, Key key, Val val, SeenAt seen, int 
                 total += p;
                 continue;
             }
-            for (uint64_t left = __ballot(in); left != 0; left &= left - 1) {
-                const int n = __ffsll((unsigned long long)left) - 1;
-                add_row(val(j0 + n), __shfl(p, n) * inv, D, lane, a0, a1);
-            }
-            if (have_lse && all_nan(a0, a1, D, lane)) {
+            decltype(val(j)) row{};
+            if (in)
+                row = val(j);
+            add_rows(row, p * inv, __ballot(in), D, lane, a0, a1);
+            if (all_nan(a0, a1, D, lane)) {
                 put_row(o, nan, nan, D, lane);
+                if (!have_lse && lane == 0)
+                    *lse = kLn2 * (top + __builtin_amdgcn_logf(total));
                 return;
             }
         }

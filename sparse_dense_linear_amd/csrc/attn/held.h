@@ -7,6 +7,7 @@
 // they are powers of two, in the widening, which stays exact.
 #pragma once
 
+#include "exact.h"
 #include "tile.h"
 
 namespace sdl {
@@ -153,6 +154,13 @@ struct CodeRow {
     __device__ CodeRow operator+(int d) const { return {at + d, scale}; }
     __device__ float operator[](int d) const { return wide<H>(*(const uint8_t *)(at + d))[0] * scale; }
 };
+
+template <bool ONE, class H>
+__device__ inline CodeRow<H> row_of_lane(CodeRow<H> r, int n)
+{
+    const int scale = __float_as_int(r.scale);
+    return {row_of_lane<ONE>(r.at, n), __int_as_float(ONE ? of_one_lane(scale, n) : of_lane(scale, n))};
+}
 
 template <class H>
 __device__ inline f32x8 load8(CodeRow<H> r)

@@ -195,7 +195,7 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
             O[e] = f32x4(0.0f);
         float top = SDL_NEG_INF, total = 0.0f;
         // A weight times an infinite scale has no second part.  Such units come out
-        // as no number, and are computed again.
+        // as if a score were infinite, and are computed again.
         bool strange = false;
 
         const int32_t *table = a.table + (int64_t)seq * a.table_stride;
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
             if constexpr (!TOGETHER) {
                 scale_of[wave][slot][0][lane & 31] = scale_k;
                 scale_of[wave][slot][1][lane & 31] = scale_v;
-                strange = strange || !finite(scale_v);
+                strange = strange || fabsf(scale_v) == __builtin_inff();
             }
         };
         const uint32_t row = (uint32_t)a.row_stride, k_off = k_row * row + kd, v_off = 4 * part * row + vd;
@@ -438,7 +438,7 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
             for (int b = 0; b < 2; ++b)
                 if constexpr (TOGETHER) {
                     y[b] *= of.vs[b];
-                    strange = strange || !finite(of.vs[b]);
+                    strange = strange || fabsf(of.vs[b]) == __builtin_inff();
                 } else {
                     times_scales<4>(y[b], scale_of[wave][of.slot][1] + 16 * b + 4 * part);
                 }
@@ -529,8 +529,10 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
             softmax(y, now);
             steps([&](auto step) { apply(now, step, step > 0 ? last_v[step] : x.v); });
         }
-        if (__any(strange))
+        if (__any(strange)) {
+            top = __builtin_inff();
             total = __builtin_nanf("");
+        }
 
         // ---- join the columns of a row, then the wavefronts of a head, and write
         total = sum_quarters(total);
@@ -595,7 +597,7 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
                 }
                 continue;
             }
-            finish<T>(a, u.q_begin + rr / group, (hg * heads + h) * group + rr % group, p, best, sum, o, &redo[h][lr]);
+            finish<T, H>(a, u.q_begin + rr / group, (hg * heads + h) * group + rr % group, p, best, sum, o, &redo[h][lr]);
         }
         __syncthreads();
         if (done)
@@ -754,7 +756,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void tree_tiles(TreeArgs a)
         auto keep_scales = [&](int n) {
             scale_of[n & 1][0][t] = scale_k;
             scale_of[n & 1][1][t] = scale_v;
-            const bool all = __all(folding(scale_k) && folding(scale_v)), odd = __any(!finite(scale_v));
+            const bool all = __all(folding(scale_k) && folding(scale_v)), odd = __any(fabsf(scale_v) == __builtin_inff());
             if (lane == 0) {
                 folds[n & 1][wave] = all;
                 if (odd)
@@ -907,8 +909,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void tree_tiles(TreeArgs a)
                 keep_row(n + 2);
             __syncthreads();
         }
-        if (QP > 1 && strange != 0)
+        if (QP > 1 && strange != 0) {
+            top = __builtin_inff();
             total = __builtin_nanf("");
+        }
 
         // ---- join the wavefronts of a query group, and write
         total = Co::sum(total);
@@ -990,7 +994,7 @@ __global__ __launch_bounds__(1024) void join_codes(TreeArgs a, int numbers)
             for (int e = 0; e < 4; ++e)
                 o[e] = fmaf(f, x[e], o[e]);
         }
-        finish<T>(a, cut.u.q_begin + r / group, cut.hk * group + r % group, p, best, sum, o, redo + lr);
+        finish<T, H>(a, cut.u.q_begin + r / group, cut.hk * group + r % group, p, best, sum, o, redo + lr);
     }
     __syncthreads();
     if (!__any(lane < ROWS && redo[lane] != 0))        // the same in all wavefronts

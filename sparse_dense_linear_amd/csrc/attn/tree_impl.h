@@ -143,9 +143,7 @@ __device__ inline bool all_seen(const TreeArgs &a, const Unit &u, int j0, int j1
                              : j1 < u.ctx && (j0 >= u.low + 63 || j1 < a.sinks);
 }
 
-// Row j of a pool, and whether a row that some draft does not see, but that
-// its tiles brought in, is not finite: keys at the lower end of the window,
-// and the drafts.
+// Row j of a pool.
 template <class H>
 struct PoolRows {
     const TreeArgs &a;
@@ -163,13 +161,18 @@ struct PoolRows {
     }
 };
 
+// Whether a row that some draft does not see, but that its tiles brought in as
+// another one does, is not finite: keys that the window of the last draft has left,
+// and the drafts.
 template <class H>
-__device__ bool odd_unseen(const Unit &u, const SeenRows &rows, const PoolRows<H> &k, const PoolRows<H> &v, int D,
-                           int lane)
+__device__ bool odd_unseen(const TreeArgs &a, const Unit &u, const SeenRows &rows, const PoolRows<H> &k,
+                           const PoolRows<H> &v, int D, int lane)
 {
-    const int edge = u.low + u.drafts < u.ctx ? u.low + u.drafts : u.ctx;
+    if (u.drafts == 1)
+        return false;                          // it sees all that is brought in
+    const int left = u.end - a.window < u.ctx ? u.end - a.window : u.ctx;
     auto odd = [&](const PoolRows<H> &x) {
-        return any_odd(x, rows.low, edge, D, lane) || any_odd(x, rows, u.ctx, u.end, D, lane);
+        return any_odd(x, rows.low, left, D, lane) || any_odd(x, rows, u.ctx, u.end, D, lane);
     };
     return odd(k) || odd(v);
 }
@@ -289,8 +292,9 @@ struct Span {
 // weights and the unnormalised values.  redo[lr]: 1, the output is to be
 // computed again if a row that is masked is not finite, or its sum became too
 // large; 2, the sum of weights too (no key was seen, or a score is infinite
-// or no number).
-template <class T>
+// or no number).  Over codes a score is no number where a key holds a NaN, or its scale
+// is one, and then nor are the results: they are right as they are.
+template <class T, class H>
 __device__ inline void finish(const TreeArgs &a, int64_t token, int head, int p, float best, float sum,
                               const f32x4 &o, int *redo)
 {
@@ -308,32 +312,37 @@ __device__ inline void finish(const TreeArgs &a, int64_t token, int head, int p,
     }
     if (p == 0)
         a.lse[head * a.Tq + token] = lse;
-    if (!clean)
+    if (!clean && !(kCodes<H> && sum != sum && best < __builtin_inff()))
         atomicMax(redo, finite(lse) ? 1 : 2);
 }
 
 // What finish() left to do in rows first .. first + count - 1 of a sequence's
-// query rows, by the first `waves` wavefronts of a workgroup; place: the drafts'
-// positions.
+// query rows, by the `waves` wavefronts of a workgroup, all of them; place: the
+// drafts' positions.
 template <class T, class H>
 __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, int hk, int first, int count,
                                     const int *redo, const Drafts &drafts, int wave, int lane, int waves = 4)
 {
-    const int group = a.Hq / a.Hkv;
     bool some = false, outputs = false;
     for (int lr = lane; lr < count; lr += 64)
         some = some || redo[lr] != 0, outputs = outputs || redo[lr] == 1;
-    if (!__any(some))
+    // (so seldom that no loop behind this is worth a register of one before it)
+    if (__builtin_expect_with_probability(__any(some) == 0, 1, 0.999999))
         return;
+    lane = renewed(lane);      // what goes by the lane is found here, not kept all along
+    const int group = a.Hq / a.Hkv;
     const int32_t *table = a.table + (int64_t)seq * a.table_stride;
     const PoolRows<H> key{a, table, (const H *)a.k_pages + hk * a.head_stride, a.k_scale + hk * a.scale_head};
     const PoolRows<H> val{a, table, (const H *)a.v_pages + hk * a.head_stride, a.v_scale + hk * a.scale_head};
     const SeenRows rows = seen_rows(a, u, drafts);
-    const bool odd = odd_unseen<H>(u, rows, key, val, a.D, lane);
-    TooLarge<T> too_large;
-    if (!odd && __any(outputs)) {
-        too_large.look(val, rows, 0, a.sinks < u.low ? a.sinks : u.low, a.D, lane);
-        too_large.look(val, rows, u.low, u.end, a.D, lane);
+    const bool odd = odd_unseen<H>(a, u, rows, key, val, a.D, lane);
+    OddColumns values;
+    if (!odd && __any(outputs)) {              // (the same for the whole workgroup)
+        const int gap = a.sinks < u.low ? a.sinks : u.low;
+        auto key_of = [&](int i) { return i < gap ? i : i - gap + u.low; };
+        values.look([&](int i) { return val(key_of(i)); }, [&](int i) { return rows(key_of(i)); }, 0,
+                    gap + u.end - u.low, a.D, lane, wave, waves);
+        values.join(lane, wave);
     }
     for (int lr = wave; lr < count; lr += waves) {
         const int why = redo[lr];              // uniform over the wavefront
@@ -342,7 +351,7 @@ __device__ inline void finish_again(const TreeArgs &a, const Unit &u, int seq, i
         const int r = first + lr, t = r / group, head = hk * group + r % group;
         const int64_t token = u.q_begin + t;
         T *o = (T *)a.o + (token * a.Hq + head) * a.D;
-        if (why == 1 && !odd && !too_large(o, a.D, lane))
+        if (why == 1 && !odd && !too_large(values, o, a.D, lane))
             continue;
         DraftSeen seen;
         seen.ctx = u.ctx;
@@ -410,7 +419,7 @@ __device__ inline void join_waves(const TreeArgs &a, const Unit &u, const Piece 
             }
             continue;
         }
-        finish<T>(a, u.q_begin + rr / group, c.hk * group + rr % group, p, best, sum, o, redo + lr);
+        finish<T, H>(a, u.q_begin + rr / group, c.hk * group + rr % group, p, best, sum, o, redo + lr);
     }
     __syncthreads();
     if (done)
@@ -507,7 +516,7 @@ __global__ __launch_bounds__(kAttnThreads) void tree_join(TreeArgs a, int number
 #pragma unroll 4
         for (int w = cut.w0 + 1; w <= cut.w1; ++w)     // a unit that goes on is a span's first
             add(2 * (int64_t)w);
-        finish<T>(a, u.q_begin + r / group, hk * group + r % group, p, best, sum, o, redo + lr);
+        finish<T, H>(a, u.q_begin + r / group, hk * group + r % group, p, best, sum, o, redo + lr);
     }
     __syncthreads();
     if (!__any(lane < kJoinRows && redo[lane] != 0))    // the same in all wavefronts

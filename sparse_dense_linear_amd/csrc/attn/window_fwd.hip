@@ -94,12 +94,12 @@ __device__ inline void again(const WindowArgs &a, const Seen &seen, uint64_t red
     auto key_row = [&](int j) { return K + (int64_t)j * a.k.row_stride; };
     auto val_row = [&](int j) { return V + (int64_t)j * a.v.row_stride; };
     const bool odd = odd_masked_keys<T>(seen, key_row, val_row, wp0, p1, walk.first_tiles, walk.band, KT, lk, a.D, lane);
-    TooLarge<T> too_large;
+    OddColumns values;
     if (!odd && (redo & __ballot(finite(lse))) != 0) {
         const int lo = wp0 - seen.window + 1 > 0 ? wp0 - seen.window + 1 : 0;
         auto every = [](int) { return true; };
-        too_large.look(val_row, every, 0, seen.sinks < lo ? seen.sinks : lo, a.D, lane);
-        too_large.look(val_row, every, lo, p1 + 1, a.D, lane);
+        values.look(val_row, every, 0, seen.sinks < lo ? seen.sinks : lo, a.D, lane);
+        values.look(val_row, every, lo, p1 + 1, a.D, lane);
         __threadfence_block();                 // the outputs, which other lanes stored
     }
     for (uint32_t left = (uint32_t)(redo | (redo >> 32)); left != 0; left &= left - 1) {
@@ -109,7 +109,7 @@ __device__ inline void again(const WindowArgs &a, const Seen &seen, uint64_t red
         // score, a score that is no number, or an infinite key times the zeros
         // past D)
         const bool have_lse = finite(__shfl(lse, n));
-        if (!odd && have_lse && !too_large(o, a.D, lane))
+        if (!odd && have_lse && !too_large(values, o, a.D, lane))
             continue;
         const int lo = p - seen.window + 1 > 0 ? p - seen.window + 1 : 0;
         exact_row<T>(

@@ -1,5 +1,7 @@
 """A paged cache that is appended to and held in 8 bits (include/cache.h) at the edges of
 its definition: contexts, values and scales that calls seldom have."""
+import math
+
 import pytest
 import torch
 
@@ -109,3 +111,86 @@ def test_integers_whose_scale_rises_are_read_as_finite(kept):
     for p, s in zip(pools, scales.values()):
         assert float(s[0, 0, 0]) == 2.0 ** 122
         assert torch.equal(p[0, 3].cpu().float(), want) and torch.equal(p[0, 4].cpu().float(), want.abs())
+
+
+@TYPES
+@KINDS
+@pytest.mark.parametrize("ctx,drafts", [(131071, 1), (9000, 40)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_one_value_that_is_no_finite_number_costs_little(dtype, kind, ctx, drafts, bad):
+    """The outputs and log-sums beside it are what they are without it; and where a row of
+    values or what append_pages writes for one holds it, finding that out takes no longer
+    than some turns over the cache (a look at one value after another took 100 ms at the
+    longer context, the call without such a value 0.1 ms)."""
+    page, Hkv, Hq, D, at = 64, 2, 8, 128, ctx - 300
+    g = torch.Generator(device="cuda").manual_seed(7)
+    pages = -(-(ctx + drafts) // page)
+    shape = (pages, page, Hkv, D)
+    q = torch.randn(drafts, Hq, D, device="cuda", generator=g).to(dtype)
+    k, v = (torch.randn(shape, device="cuda", generator=g) * 16 for _ in range(2))
+    scales = {}
+    if kind is None:
+        k, v = (x.to(dtype) / 16 for x in (k, v))
+    else:
+        k, v = (codes_of(x.clamp(-100, 100), kind) for x in (k, v))
+        scales = {n: torch.full((pages, page, Hkv), 2.0 ** -4, device="cuda") for n in ("k_scale", "v_scale")}
+    args = (i32([list(range(pages))]), i32([ctx]), i32([0, drafts]))
+    clean, clean_lse = sdl.tree_attention(q, k, v, *args, **scales)
+    where, columns = (at // page, at % page, 1), [37]
+    if kind is None:
+        v[where][37] = bad
+    else:
+        v.view(torch.uint8)[where][37] = 0x7f if kind is E4M3 and math.isnan(bad) else 1
+        if kind is INT8 or math.isinf(bad):            # which such codes cannot be: all of the row is
+            v.view(torch.uint8)[where] = 1
+            scales["v_scale"][where], columns = bad, list(range(D))
+    took = []
+    for _ in range(3):
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        o, lse = sdl.tree_attention(q, k, v, *args, **scales)
+        end.record()
+        torch.cuda.synchronize()
+        took.append(begin.elapsed_time(end))
+    # an infinite scale is taken from the definition, whose sums have another order: scores
+    # of 128 products (whose sizes add up to less than 16), and ctx / 64 weights to a lane
+    tol = 0.0 if columns == [37] or math.isnan(bad) else 2 * (128 * 16 + ctx / 64 + 64) * 2.0 ** -24
+    assert bool(((lse - clean_lse).abs() <= tol).all())
+    assert torch.equal(o[:, :Hq // 2], clean[:, :Hq // 2])
+    rest = [d for d in range(D) if d not in columns]
+    got = o[:, Hq // 2:]
+    assert bool(got[..., columns].isnan().all() if math.isnan(bad) else (got[..., columns] == bad).all())
+    assert torch.equal(got[..., rest], clean[:, Hq // 2:][..., rest])
+    assert min(took) < 20.0 or not tol == 0.0, took
+
+
+@TYPES
+@CODES
+@pytest.mark.parametrize("ctx,drafts", [(131071, 1), (9000, 40)])
+def test_a_key_that_is_no_number_costs_nothing(dtype, held, ctx, drafts):
+    """What append_pages writes for a key that is not finite: all results of its head are
+    no numbers, the others what they are without it."""
+    page, Hkv, Hq, D, at = 64, 2, 8, 128, ctx - 300
+    g = torch.Generator(device="cuda").manual_seed(8)
+    pages = -(-(ctx + drafts) // page)
+    q = torch.randn(drafts, Hq, D, device="cuda", generator=g).to(dtype)
+    k, v = (codes_of((torch.randn(pages, page, Hkv, D, device="cuda", generator=g) * 16).clamp(-100, 100), held)
+            for _ in range(2))
+    scales = {n: torch.full((pages, page, Hkv), 2.0 ** -4, device="cuda") for n in ("k_scale", "v_scale")}
+    args = (i32([list(range(pages))]), i32([ctx]), i32([0, drafts]))
+    clean, clean_lse = sdl.tree_attention(q, k, v, *args, **scales)
+    if held is INT8:
+        scales["k_scale"][at // page, at % page, 1] = math.nan
+    else:
+        k.view(torch.uint8)[at // page, at % page, 1, 37] = 0x7f
+    took = []
+    for _ in range(3):
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        o, lse = sdl.tree_attention(q, k, v, *args, **scales)
+        end.record()
+        torch.cuda.synchronize()
+        took.append(begin.elapsed_time(end))
+    assert torch.equal(o[:, :4], clean[:, :4]) and torch.equal(lse[:4], clean_lse[:4])
+    assert bool(o[:, 4:].isnan().all()) and bool(lse[4:].isnan().all())
+    assert min(took) < 5.0, took
