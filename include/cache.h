@@ -30,8 +30,10 @@
  * bit.
  * A value that is not finite becomes the code NaN in e4m3.  Integers have no
  * such code: the scale of its block and head becomes NaN, and all rows of the
- * block and head read as NaN until the block is begun anew.  Rows of a block
- * behind the last one that was written hold codes of no meaning.
+ * block and head read as NaN until the block is begun anew.  The earlier rows of
+ * the block are lost with it (codes and scale are written over), also where the
+ * value was that of a draft which is not kept.  Rows of a block behind the last one
+ * that was written hold codes of no meaning.
  *
  * Preconditions, beyond those of attn.h: scales of blocks that keep rows are
  * positive (or NaN); no two sequences of a call write the same block; pools,

@@ -52,7 +52,10 @@ def append_pages(k, v, k_pages, v_pages, table, ctx, rowptr, q=None, cos=None, s
     The pools hold rows of k's type, or, with k_scale and v_scale [pages, page /
     block, Hkv] float32, codes of 8 bits (float8_e4m3fn or int8).  A block's
     scale is the smallest power of two that holds its values; where new rows
-    need a larger one than the rows before them, these are rounded to it.
+    need a larger one than the rows before them, these are rounded to it.  A value
+    that is not finite is a code of its own in float8_e4m3fn; in int8 it makes all
+    rows of its block and head NaN, those before it too, even if it is a draft's
+    that is not kept.
 
     Returns the rotated q (q_out, which may be q itself; None: allocated, on
     `stream` if given), or None without q.  Records no autograd graph."""

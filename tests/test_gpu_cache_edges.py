@@ -7,7 +7,7 @@ import torch
 
 import sparse_dense_linear_amd as sdl
 from cache_ref import E4M3, INT8, MOST, codes_of, scale_of_top
-from test_gpu_cache import BF16, CODES, F32, KINDS, TYPES, a_pool, bits, i32, tables
+from test_gpu_cache import CODES, F32, KINDS, TYPES, a_pool, bits, i32, tables
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -194,3 +194,38 @@ def test_a_key_that_is_no_number_costs_nothing(dtype, held, ctx, drafts):
     assert torch.equal(o[:, :4], clean[:, :4]) and torch.equal(lse[:4], clean_lse[:4])
     assert bool(o[:, 4:].isnan().all()) and bool(lse[4:].isnan().all())
     assert min(took) < 5.0, took
+
+
+@TYPES
+@CODES
+def test_a_draft_that_is_no_finite_number_and_is_not_kept(dtype, held):
+    """Its block's context: as it was in e4m3, lost in integers until the block is begun
+    anew; other heads and blocks as they were."""
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(21, 2, 64, generator=g).to(dtype).cuda()
+    table = i32([[1, 0]])
+    pools = [codes_of(torch.zeros(2, 16, 2, 64), held).cuda() for _ in range(2)]
+    scales = dict(zip(("k_scale", "v_scale"), (torch.ones(2, 2, 2, device="cuda") for _ in range(2))))
+    q = torch.randn(1, 2, 64, generator=g).to(dtype).cuda()
+
+    def append(rows, at):
+        sdl.append_pages(rows, rows, *pools, table, i32([at]), i32([0, len(rows)]), **scales)
+
+    def answer(keys):                                      # of keys 0 .. keys - 1
+        return sdl.tree_attention(q, *pools, table, i32([keys - 1]), i32([0, 1]), **scales)
+
+    append(x[:20], 0)                                      # blocks of 8: the third has 4 rows
+    before, block = answer(20), answer(16)
+    bad = x[20:].clone()
+    bad[0, 1, 7] = math.inf
+    append(bad, 20)
+    o, lse = answer(20)
+    if held is E4M3:
+        # a scale that a draft raises costs e4m3 nothing
+        assert torch.equal(o, before[0]) and torch.equal(lse, before[1])
+    else:
+        assert torch.equal(o[:, 0], before[0][:, 0]) and torch.equal(lse[0], before[1][0])
+        assert bool(o[:, 1].isnan().all()) and bool(lse[1].isnan().all())
+    assert all(torch.equal(a, b) for a, b in zip(answer(16), block))
+    append(x[16:20], 16)
+    assert all(torch.equal(a, b) for a, b in zip(answer(20), before))
