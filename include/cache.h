@@ -113,7 +113,8 @@ spmm_status_t cache_append(int32_t dtype, int32_t held,
 /*
  * tree_attn_paged over pools of codes (held: CACHE_E4M3 or CACHE_INT8): keys
  * and values are code * scale.  Codes are exact in the products; scales are
- * applied in fp32, or exactly.  Softmax weights, times the scale of their value
+ * applied in fp32, or exactly, those of keys to the sum over the codes (which an
+ * infinite one makes infinite).  Softmax weights, times the scale of their value
  * or not, are rounded to the element type, or to more bits.  Codes, scales and table entries of rows that no draft sees
  * have no effect; other rows of pages that hold a row which is seen, and page
  * 0, may be read.  k_pages and v_pages are 16-byte aligned.

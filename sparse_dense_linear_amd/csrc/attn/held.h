@@ -170,6 +170,23 @@ __device__ inline f32x8 load8(CodeRow<H> r)
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// A score's sum goes over the codes, as it does in the tiles.
+template <class A, class H>
+__device__ inline float dot_row(A a, CodeRow<H> b, int D)
+{
+    const float scale = b.scale;
+    b.scale = 1.0f;
+    float s = 0.0f;
+    for (int d = 0; d < D; d += 8) {
+        const auto x = load8(a + d);
+        const auto y = load8(b + d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            s = fmaf((float)x[e], y[e], s);
+    }
+    return s * scale;
+}
+
 // Scores or weights of a result's rows times the scales of their keys, four
 // consecutive ones to a group of registers and eight apart; `scale`: of the
 // lane's first.

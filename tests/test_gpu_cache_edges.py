@@ -6,8 +6,9 @@ import pytest
 import torch
 
 import sparse_dense_linear_amd as sdl
+from attn_ref import assert_close, tree_seen
 from cache_ref import E4M3, INT8, MOST, codes_of, scale_of_top
-from test_gpu_cache import CODES, F32, KINDS, TYPES, a_pool, bits, i32, tables
+from test_gpu_cache import CODES, F32, KINDS, TYPES, CodeCache, a_pool, bits, i32, i64, tables, want_rows
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -229,3 +230,56 @@ def test_a_draft_that_is_no_finite_number_and_is_not_kept(dtype, held):
     assert all(torch.equal(a, b) for a, b in zip(answer(16), block))
     append(x[16:20], 16)
     assert all(torch.equal(a, b) for a, b in zip(answer(20), before))
+
+
+@TYPES
+@CODES
+@pytest.mark.parametrize("what", ["code", "nan scale", "infinite scale"])
+@pytest.mark.parametrize("T", [5, 40])
+def test_masked_places_against_the_definition(dtype, held, what, T):
+    """A draft whose row or scale is no finite number: the drafts that do not see it have
+    the results of the definition; its own are no numbers, or infinite where the
+    definition's are."""
+    page, block, ctx, at, D = 16, 1, 300, 2, 64
+    if what == "code" and held is INT8:
+        return                                             # every code is a number
+    for pool in ("k", "v"):
+        cache = CodeCache([ctx + T], page, block, 1, D, held, 14)
+        number, row = cache.table[0][(ctx + at) // page], (ctx + at) % page
+        code, scale, rows = (cache.k, cache.ks, cache.rows_k) if pool == "k" else (cache.v, cache.vs, cache.rows_v)
+        if what == "code":
+            code[number, row] = math.nan
+        else:
+            scale[number, row] = math.nan if what == "nan scale" else math.inf
+        q = torch.randn(T, 4, D, generator=torch.Generator().manual_seed(15)).to(dtype)
+        masks = [(1 << a | 1) & ~(1 << at) for a in range(T)]
+        masks[at] = 1 << at | 1                            # seen by itself alone
+        pools, scales = cache.on_gpu()
+        o, lse = sdl.tree_attention(q.cuda(), *pools, i32([ctx]), i32([0, T]), i64(masks), **scales)
+        keep = [t for t in range(T) if t != at]
+        rows[0][ctx + at] = 0.0                            # of no draft that is kept
+        want = want_rows(q, [0, T], cache.rows_k, cache.rows_v,
+                         lambda s: tree_seen(ctx, masks, sdl.NO_WINDOW, 0), 1, D ** -0.5, dtype)
+        assert_close(o[keep], want["o"][keep], 2 * want["o_tol"][keep], "o")
+        assert_close(lse[:, keep], want["lse"][:, keep], 2 * want["lse_tol"][:, keep], "lse")
+        if pool == "v":
+            # weights do not depend on it: the log-sum is right, the outputs are what the
+            # sums with it are
+            assert_close(lse[:, at], want["lse"][:, at], 2 * want["lse_tol"][:, at], "lse")
+            sign = code[number, row, 0].float().sign()
+            if what != "infinite scale":
+                assert bool(o[at].isnan().all())
+            else:
+                got = o[at].cpu().float()
+                assert bool(torch.where(sign == 0, got.isnan(), got == sign * math.inf).all())
+        elif what != "infinite scale":
+            assert bool(o[at].isnan().all()) and bool(lse[:, at].isnan().all())
+        else:
+            # s = scale * <q, code>: plus infinity, or minus infinity and so no weight
+            up = (q[at].double() @ code[number, row, 0].double()) > 0
+            assert bool(up.any()) and not bool(up.all())
+            assert bool(o[at, up].isnan().all()) and bool((lse[up, at] == math.inf).all())
+            alone = want_rows(q, [0, T], cache.rows_k, cache.rows_v,
+                              lambda s: tree_seen(ctx, [1] * T, sdl.NO_WINDOW, 0), 1, D ** -0.5, dtype)
+            assert_close(o[at, ~up], alone["o"][at, ~up], 2 * alone["o_tol"][at, ~up], "o")
+            assert_close(lse[~up, at], alone["lse"][~up, at], 2 * alone["lse_tol"][~up, at], "lse")
