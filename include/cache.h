@@ -13,7 +13,8 @@
  * A pool of codes has a scale, float32, for each block of `block` positions
  * (which divides the page) and head: value = code * scale.  Scales as written
  * here are powers of two; reading takes any.  In pools of codes D is a
- * multiple of 16 (up to 128, as everywhere), and strides of the pools are in codes (multiples of 16).
+ * multiple of 16 (up to 128, as everywhere), and strides of the pools are in
+ * codes (multiples of 16).
  *
  * How a scale is chosen.  The values that a call brings into a block are held
  * by the smallest power of two s, at least 2^-126, with
@@ -115,9 +116,10 @@ spmm_status_t cache_append(int32_t dtype, int32_t held,
  * and values are code * scale.  Codes are exact in the products; scales are
  * applied in fp32, or exactly, those of keys to the sum over the codes (which an
  * infinite one makes infinite).  Softmax weights, times the scale of their value
- * or not, are rounded to the element type, or to more bits.  Codes, scales and table entries of rows that no draft sees
- * have no effect; other rows of pages that hold a row which is seen, and page
- * 0, may be read.  k_pages and v_pages are 16-byte aligned.
+ * or not, are rounded to the element type, or to more bits.  Codes, scales and
+ * table entries of rows that no draft sees have no effect; other rows of pages
+ * that hold a row which is seen, and page 0, may be read.  k_pages and v_pages
+ * are 16-byte aligned.
  */
 spmm_status_t cache_tree_attn(int32_t dtype, int32_t held,
                               const attn_tree_t *shape, const attn_rows_t *q,

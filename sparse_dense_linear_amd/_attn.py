@@ -486,9 +486,9 @@ def _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks
 def tree_attn_paged(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window=None,
                     sinks: int = 0, scale: float | None = None, stream=None, k_scale=None, v_scale=None) -> None:
     """Attention of drafted tokens over a paged cache into o [Tq, Hq, D] and
-    lse [Hq, Tq] (tree_attn_paged, with scales cache_tree_attn); see tree_attention.  o and lse overlap
-    nothing that the call reads.  The scratch memory is taken from torch for
-    this call alone."""
+    lse [Hq, Tq] (tree_attn_paged, with scales cache_tree_attn); see
+    tree_attention.  o and lse overlap nothing that the call reads.  The scratch
+    memory is taken from torch for this call alone."""
     device = _first(q, "q", 3, "three dimensions: rows, heads, D")
     with _On(device, stream) as handle:
         _tree(q, k_pages, v_pages, table, ctx, q_rowptr, tree, o, lse, window, sinks, scale, k_scale, v_scale,
@@ -512,6 +512,9 @@ def tree_attention(q, k_pages, v_pages, table, ctx, q_rowptr, tree=None, window=
     bits (float8_e4m3fn or int8): value = code * scale, the scales [pages,
     page / block, Hkv] float32 for each block of positions and head, with any
     strides.  D is then a multiple of 16.
+
+    Work is laid out for the mean sequence: single tokens and long pieces cost
+    less in two calls than in one.
 
     Allocates o [Tq, Hq, D] and lse [Hq, Tq] float32, on `stream` if given;
     records no autograd graph."""

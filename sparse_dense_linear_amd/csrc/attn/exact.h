@@ -65,7 +65,8 @@ __device__ inline bool any_odd(Row row, int from, int to, int D, int lane)
 // x of lane n.  (Not __shfl, whose indexes the compiler would find once for the whole
 // kernel and keep in registers all along.)
 __device__ inline int of_lane(int x, int n) { return __builtin_amdgcn_ds_bpermute(n << 2, x); }
-__device__ inline int of_one_lane(int x, int n) { return __builtin_amdgcn_readlane(x, n); }      // the same n in all lanes
+// The same n in all lanes.
+__device__ inline int of_one_lane(int x, int n) { return __builtin_amdgcn_readlane(x, n); }
 
 // The row whose address lane n has found; ONE: the same n in all lanes.
 template <bool ONE, class T>

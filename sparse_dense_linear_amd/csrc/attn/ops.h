@@ -101,7 +101,7 @@ struct TreeArgs {
     float *partial;
     int32_t workers, block_rows, slot_rows;   // launch shape (tree_shape)
     // pools of codes only: key heads of a workgroup and keys of a tile, whether 16
-    // keys lie together (tree_codes.h),: scales of blocks of positions, and their strides
+    // keys lie together (tree_codes.h); scales of blocks of positions, and their strides
     int32_t wave_heads, tile_keys, together, mean_rows;
     const float *k_scale, *v_scale;
     int64_t scale_page, scale_block, scale_head;

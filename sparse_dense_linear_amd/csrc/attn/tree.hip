@@ -285,14 +285,17 @@ TreeShape tree_shape(int dtype, int held, int64_t S, int64_t Tq, int64_t Hq, int
 {
     TreeShape sh = {};
     const int DP = D <= 64 ? 64 : 128;
-    // as many queries to a block as the mean sequence fills
+    // As many queries to a block as the mean sequence fills.  A batch of unlike sequences
+    // so costs more than its parts: 64 single tokens over codes 155 us, a piece of 512
+    // behind 4096 keys 82, both in one call 300 (q in fp32 169, 186, 614); a piece of 64
+    // 46, both 199.  Two calls, over the sequences of either kind, cost the sum.
     sh.rows = S > 0 ? (Tq + S - 1) / S * (Hq / Hkv) : 0;
     sh.block_rows = sh.rows <= 16 ? 16 : (sh.rows <= 32 ? 32 : (sh.rows <= 64 ? 64 : 128));
     sh.wave_heads = 1;
     // as many workgroups as the 256 CUs hold at once
     if (held != 0 && sh.block_rows == 16) {
         // (neighbouring heads together: loads of whole rows of four heads reach 7.0 TB/s,
-        // of one 5.5)
+        // of one 5.9)
         sh.workers = 256 * stream_per_cu(dtype == SPMM_DTYPE_BF16 ? 2 : 4, DP);
         sh.wave_heads = Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1);
     } else if (held != 0) {

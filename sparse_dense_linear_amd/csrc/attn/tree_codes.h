@@ -20,10 +20,10 @@
 // own, and the columns of a row are joined at the end.
 // Wavefronts of a workgroup take neighbouring heads (up to four) of the same keys:
 // rows of 128 bytes that are read together lie beside each other in memory.
-// 64 answers of 1000 to 16384 positions, 8 heads of 128, 697 MB in 129 us = 5.4 TB/s
-// (reading alone 7.1).  Each further byte costs what 6.8 TB/s cost; some 30 us are the
-// start (six loads that wait for each other), the last turns, which end at different
-// times, and the join.
+// 64 answers of 1000 to 16384 positions, 8 heads of 128, 697 MB in 131 us = 5.3 TB/s
+// (reading alone 7.1).  Each further byte costs what 6.6 TB/s cost; 25 us are the start
+// (six loads that wait for each other) and the last turns, which end at different
+// times, and 6 more the join.
 // Codes are exact in bf16.  q in fp32 is the sum of three bf16 parts (8 bits
 // each, exact), whose products with a code are exact too, so that three
 // instructions of bf16 do what eight of fp32 would; weights are taken as two
@@ -615,9 +615,13 @@ __global__ __launch_bounds__(kAttnThreads, stream_per_cu(sizeof(T), DP)) void tr
 // append writes them, they go into the widening, which is exact still; else they are
 // applied to scores and weights.
 // q in fp32 is taken in three bf16 parts, weights too (tree_stream); for q in bf16 the
-// weights are rounded to bf16, once, as they are over rows of bf16.
+// weights are rounded to bf16, once, as they are over rows of bf16.  (Two parts, as
+// tree_stream has them: pieces of prompts 354 us against 295, trees of drafts 94 against
+// 84; errors against 64 bits 0.0017, which is the rounding of the result, instead of
+// 0.0022.)
 // A piece of 1024 queries behind 8192 keys and two more sequences, 32 heads of 128 on
-// 8: 179 GFLOP in 275 us = 650 TFLOP/s; scales that are no powers of two 330 us.  It is
+// 8: 179 GFLOP in 272 us = 660 TFLOP/s; integers, with scales that are no powers of two,
+// 322 us.  It is
 // bound by LDS, 82 % of what row reads alone reach: each wavefront of 32 queries reads
 // the whole tile.
 // (Two buffers of 64 keys with one barrier to a tile instead of two: prompt pieces 418
@@ -756,7 +760,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void tree_tiles(TreeArgs a)
         auto keep_scales = [&](int n) {
             scale_of[n & 1][0][t] = scale_k;
             scale_of[n & 1][1][t] = scale_v;
-            const bool all = __all(folding(scale_k) && folding(scale_v)), odd = __any(fabsf(scale_v) == __builtin_inff());
+            const bool all = __all(folding(scale_k) && folding(scale_v));
+            const bool odd = __any(fabsf(scale_v) == __builtin_inff());
             if (lane == 0) {
                 folds[n & 1][wave] = all;
                 if (odd)
